@@ -71,13 +71,26 @@ _lib.bi_lab_mfma_rate.argtypes = [_P, _I32, _I32, _I32, _I32, _P]
 _lib.bi_lab_plan.argtypes = [_I32, _I64, _I64, _I64, ctypes.POINTER(_I32)]
 _lib.bi_lab_moe_layout.argtypes = [_I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_I64)]
 _lib.bi_linear_f32_noalloc.argtypes = [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P]
+_lib.bi_gated_linear_bf16.argtypes = [_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _I64, _I64, _I64, _P]
+_lib.bi_gated_linear_bf16_bwd.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _I32, _I64,
+                                          _I64, _I64, _I64, _P, _SZ, _P]
+_lib.bi_linear_bf16_bwd.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _P, _I64, _I64, _I64,
+                                    _P, _SZ, _P]
+_lib.bi_quantize_mxfp4.argtypes = [_P, _I32, _I64, _P, _I64, _P, _I64, _I64, _I64, _P]
+_lib.bi_dequantize_mxfp4.argtypes = [_P, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64, _P]
+_lib.bi_linear_mxfp4.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _I64, _I64, _I64, _I64, _P]
+_lib.bi_gated_linear_bwd_workspace_size.argtypes = [_I64, _I64]
+_lib.bi_linear_bwd_workspace_size.argtypes = [_I64, _I64, _I64]
 for _f in (_lib.bi_linear_f32, _lib.bi_linear_bf16, _lib.bi_negctl_linear_f32, _lib.bi_lab_linear,
+           _lib.bi_gated_linear_bf16, _lib.bi_gated_linear_bf16_bwd, _lib.bi_linear_bf16_bwd,
+           _lib.bi_quantize_mxfp4, _lib.bi_dequantize_mxfp4, _lib.bi_linear_mxfp4,
            _lib.bi_moe_grouped_gemm, _lib.bi_describe_recipe, _lib.bi_indexer_topk,
            _lib.bi_moe_grouped_gemm_ex, _lib.bi_lab_xcc_ids, _lib.bi_lab_empty, _lib.bi_lab_stream_read,
            _lib.bi_lab_clock, _lib.bi_lab_plan, _lib.bi_lab_moe_layout, _lib.bi_linear_f32_noalloc,
            _lib.bi_lab_lds_read, _lib.bi_lab_mfma_rate, _lib.bi_lab_l2_read):
     _f.restype = _I32
-for _f in (_lib.bi_linear_workspace_size, _lib.bi_lab_workspace_size, _lib.bi_moe_workspace_size):
+for _f in (_lib.bi_linear_workspace_size, _lib.bi_lab_workspace_size, _lib.bi_moe_workspace_size,
+           _lib.bi_gated_linear_bwd_workspace_size, _lib.bi_linear_bwd_workspace_size):
     _f.restype = _SZ
 _lib.bi_status_str.restype = ctypes.c_char_p
 
@@ -364,6 +377,232 @@ def bi_indexer_topk(scores, topk: int, row_start=None, row_end=None, out=None):
     _check(_lib.bi_indexer_topk(_ptr(scores), max(scores.stride(0), cols), rows, cols, _ptr(row_start),
                                 _ptr(row_end), topk, _ptr(out), out.stride(0),
                                 ctypes.c_void_p(s.cuda_stream)), "bi_indexer_topk")
+    return out
+
+
+# ------------------------------------------------- feed-forward layers, MXFP4
+
+BI_GATE_SILU, BI_GATE_GELU_TANH = 0, 1
+
+
+def _rows(t, dtype, shape, device, name, what, align=16):
+    """Row pitch (in elements) of a 2-D tensor the kernels take as rows of
+    contiguous elements, after checking it; a single row's pitch is its width
+    rounded up to `align` bytes, whatever stride torch reports for it."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {what} must be {dtype}, got {t.dtype}")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on one GPU; {what} is on {t.device}")
+    if t.dim() != 2 or (t.shape[0], t.shape[1]) != shape:
+        raise ValueError(f"{name}: {what} must have shape {shape}, got {tuple(t.shape)}")
+    es = t.element_size()
+    if shape[0] > 1:
+        ld = t.stride(0)
+        if ld < shape[1] or ld * es % align:
+            raise ValueError(f"{name}: {what} needs a row pitch >= {shape[1]} that is a multiple of {align} bytes")
+    else:
+        ld = -(-shape[1] * es // align) * align // es
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows of {what} must be contiguous")
+    if t.data_ptr() % align:
+        raise ValueError(f"{name}: {what} must be {align}-byte aligned")
+    return ld
+
+
+def _sizes(name, N, K):
+    if N == 0 or K == 0 or N % 16 or K % 32:
+        raise ValueError(f"{name}: needs an output width that is a multiple of 16 and k a multiple of 32, got {N}, {K}")
+
+
+def _scratch(nbytes, device, given, name):
+    """The caller's workspace (checked), else a fresh block from torch's
+    allocator: nothing is kept between calls, and a graph capture takes it
+    from the graph's own pool."""
+    if given is not None:
+        if (given.dtype != torch.uint8 or given.dim() != 1 or not given.is_contiguous() or given.device != device
+                or given.numel() < nbytes):
+            raise ValueError(f"{name}: ws must be a contiguous 1-D uint8 tensor of at least {nbytes} bytes on {device}")
+        return given
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _call(fn, name, device, *args):
+    """Enqueue on the tensors' device and its current stream."""
+    s = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, s)
+    if st != BI_OK:
+        raise BIError(st, name)
+
+
+def _dp(t):
+    return None if t is None else t.data_ptr()
+
+
+_DT = {torch.float32: BI_F32, torch.bfloat16: BI_BF16}
+
+
+def _dtype_code(dtype, name, what):
+    if dtype not in _DT:
+        raise TypeError(f"{name}: {what} must be bfloat16 or float32, got {dtype}")
+    return _DT[dtype]
+
+
+def bi_gated_linear_bf16(x: torch.Tensor, w13t: torch.Tensor, gate: int = BI_GATE_SILU, save_h: bool = False,
+                         out: torch.Tensor | None = None):
+    """y = act(x @ wg) * (x @ wu) in one launch, batch-invariant.  x [M, H] bf16,
+    w13t [H, 2I] = weight.t() of an nn.Linear weight whose rows are the gate
+    projection, then the up projection.  Returns y [M, I] bf16, or (y, h) with
+    save_h: h [M, 2I] bf16, the projections the backward pass needs."""
+    name = "bi_gated_linear_bf16"
+    if x.dim() != 2 or w13t.dim() != 2 or w13t.shape[1] % 2:
+        raise ValueError(f"{name}: x is [M, H] and w13t is [H, 2I]")
+    M, H = x.shape
+    I = w13t.shape[1] // 2
+    _sizes(name, I, H)
+    dev = x.device
+    ldx = _rows(x, torch.bfloat16, (M, H), dev, name, "x")
+    ldw = _rows(w13t.t(), torch.bfloat16, (2 * I, H), dev, name, "w13t.t()")
+    if out is None:
+        out = torch.empty((M, I), dtype=torch.bfloat16, device=dev)
+    ldy = _rows(out, torch.bfloat16, (M, I), dev, name, "out")
+    h = torch.empty((M, 2 * I), dtype=torch.bfloat16, device=dev) if save_h else None
+    _call(_lib.bi_gated_linear_bf16, name, dev, x.data_ptr(), ldx, w13t.data_ptr(), ldw, int(gate), out.data_ptr(), ldy,
+          _dp(h), 2 * I, M, I, H)
+    return (out, h) if save_h else out
+
+
+def bi_gated_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, w13t: torch.Tensor | None, h: torch.Tensor,
+                             gate: int = BI_GATE_SILU, need_dx: bool = True, need_dw: bool = True,
+                             dw_dtype: torch.dtype = torch.bfloat16, ws: torch.Tensor | None = None):
+    """Gradients of bi_gated_linear_bf16 at the projections h its forward pass
+    kept: (dx [M, H] bf16 or None, dw [2I, H] of dw_dtype or None).  x is read
+    for dw only and w13t for dx only; the other may be None."""
+    name = "bi_gated_linear_bf16_bwd"
+    if dy.dim() != 2 or (need_dx and w13t is None) or (need_dw and x is None):
+        raise ValueError(f"{name}: dy is [M, I]; dx needs w13t and dw needs x")
+    M, I = dy.shape
+    H = w13t.shape[0] if need_dx else x.shape[1] if need_dw else 32
+    code = _dtype_code(dw_dtype, name, "dw_dtype")
+    _sizes(name, I, H)
+    dev = dy.device
+    lddy = _rows(dy, torch.bfloat16, (M, I), dev, name, "dy")
+    ldh = _rows(h, torch.bfloat16, (M, 2 * I), dev, name, "h")
+    dx = dw = None
+    ldx = ldw = 0
+    if need_dx:
+        ldw = _rows(w13t.t(), torch.bfloat16, (2 * I, H), dev, name, "w13t.t()")
+        dx = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+    if need_dw:
+        ldx = _rows(x, torch.bfloat16, (M, H), dev, name, "x")
+        dw = torch.empty((2 * I, H), dtype=dw_dtype, device=dev)
+    ws = _scratch(_lib.bi_gated_linear_bwd_workspace_size(M, I), dev, ws, name)
+    _call(_lib.bi_gated_linear_bf16_bwd, name, dev, dy.data_ptr(), lddy, _dp(x) if need_dw else None, ldx,
+          _dp(w13t) if need_dx else None, ldw, h.data_ptr(), ldh, int(gate), _dp(dx), H, _dp(dw), code, H, M, I, H,
+          _dp(ws), 0 if ws is None else ws.numel())
+    return dx, dw
+
+
+def bi_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tensor | None, need_dx: bool = True,
+                       need_dw: bool = True, need_db: bool = True, dw_dtype: torch.dtype = torch.bfloat16,
+                       ws: torch.Tensor | None = None):
+    """Gradients of bi_linear_bf16: (dx [M, K] bf16, dw [N, K] of dw_dtype, db
+    [N] fp32), each None if not wanted.  dy [M, N] bf16; x [M, K] is read for
+    dw only and wt = weight.t() [K, N] for dx only; either may be None."""
+    name = "bi_linear_bf16_bwd"
+    if dy.dim() != 2 or (need_dx and wt is None) or (need_dw and x is None):
+        raise ValueError(f"{name}: dy is [M, N]; dx needs wt and dw needs x")
+    M, N = dy.shape
+    K = wt.shape[0] if need_dx else x.shape[1] if need_dw else 32
+    code = _dtype_code(dw_dtype, name, "dw_dtype")
+    _sizes(name, N, K)
+    dev = dy.device
+    lddy = _rows(dy, torch.bfloat16, (M, N), dev, name, "dy")
+    dx = dw = db = None
+    ldx = ldw = 0
+    if need_dx:
+        ldw = _rows(wt.t(), torch.bfloat16, (N, K), dev, name, "wt.t()")
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    if need_dw:
+        ldx = _rows(x, torch.bfloat16, (M, K), dev, name, "x")
+        dw = torch.empty((N, K), dtype=dw_dtype, device=dev)
+    if need_db:
+        db = torch.empty((N,), dtype=torch.float32, device=dev)
+    ws = _scratch(_lib.bi_linear_bwd_workspace_size(M, N, K), dev, ws, name)
+    _call(_lib.bi_linear_bf16_bwd, name, dev, dy.data_ptr(), lddy, _dp(x) if need_dw else None, ldx,
+          _dp(wt) if need_dx else None, ldw, _dp(dx), K, _dp(dw), code, K, _dp(db), M, N, K, _dp(ws),
+          0 if ws is None else ws.numel())
+    return dx, dw, db
+
+
+def _mx_operand(q, s, device, name, what):
+    """Pitches (bytes) of an MXFP4 operand's codes [rows, K/2] and scales
+    [rows, K/32], and its shape (rows, K)."""
+    if q.dim() != 2:
+        raise ValueError(f"{name}: {what} codes are [rows, K/2]")
+    rows, K = q.shape[0], 2 * q.shape[1]
+    _sizes(name, 16, K)
+    ldq = _rows(q, torch.uint8, (rows, K // 2), device, name, f"{what} codes")
+    lds = _rows(s, torch.uint8, (rows, K // 32), device, name, f"{what} scales", align=4)
+    if rows and s.storage_offset() + (rows - 1) * lds + (K // 32 + 3) // 4 * 4 > s.untyped_storage().nbytes():
+        raise ValueError(f"{name}: {what} scales must be readable in whole 32-bit words up to the last row's end")
+    return ldq, lds, rows, K
+
+
+def bi_quantize_mxfp4(x: torch.Tensor):
+    """Rows of x [rows, K] (bf16 or fp32) as MXFP4: (codes uint8 [rows, K/2], the
+    even element in a byte's low half; scales uint8 [rows, K/32], 2^(s - 127)
+    for each block of 32).  The scale rows lie at a pitch of a multiple of 4
+    bytes, as bi_linear_mxfp4 reads them."""
+    name = "bi_quantize_mxfp4"
+    code = _dtype_code(x.dtype, name, "x")
+    if x.dim() != 2:
+        raise ValueError(f"{name}: x is [rows, K]")
+    rows, K = x.shape
+    _sizes(name, 16, K)
+    dev = x.device
+    ldx = _rows(x, x.dtype, (rows, K), dev, name, "x")
+    q = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
+    lds = (K // 32 + 3) // 4 * 4
+    s = torch.empty((rows, lds), dtype=torch.uint8, device=dev)
+    _call(_lib.bi_quantize_mxfp4, name, dev, x.data_ptr(), code, ldx, q.data_ptr(), K // 2, s.data_ptr(), lds, rows, K)
+    return q, s if lds == K // 32 else s[:, :K // 32]
+
+
+def bi_dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The values [rows, K] (bf16 or fp32) that MXFP4 codes and scales stand for."""
+    name = "bi_dequantize_mxfp4"
+    code = _dtype_code(out_dtype, name, "out_dtype")
+    dev = q.device
+    ldq, lds, rows, K = _mx_operand(q, s, dev, name, "q")
+    y = torch.empty((rows, K), dtype=out_dtype, device=dev)
+    _call(_lib.bi_dequantize_mxfp4, name, dev, q.data_ptr(), ldq, s.data_ptr(), lds, y.data_ptr(), code, K, rows, K)
+    return y
+
+
+def bi_linear_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+                    bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """y = x @ w.t() + bias of MXFP4 operands (bi_quantize_mxfp4 of x [M, K] and of
+    an nn.Linear weight w [N, K]), fp32 accumulation, bf16 or fp32 out,
+    batch-invariant."""
+    name = "bi_linear_mxfp4"
+    code = _dtype_code(out_dtype if out is None else out.dtype, name, "out")
+    dev = xq.device
+    ldxq, ldxs, M, K = _mx_operand(xq, xs, dev, name, "x")
+    ldwq, ldws, N, Kw = _mx_operand(wq, ws, dev, name, "w")
+    if K != Kw:
+        raise ValueError(f"{name}: x has k = {K} and w has k = {Kw}")
+    _sizes(name, N, K)
+    _check_bias(bias, N, dev, name)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    ldy = _rows(out, out.dtype, (M, N), dev, name, "out")
+    _call(_lib.bi_linear_mxfp4, name, dev, xq.data_ptr(), ldxq, xs.data_ptr(), ldxs, wq.data_ptr(), ldwq, ws.data_ptr(),
+          ldws, _dp(bias), out.data_ptr(), code, ldy, M, N, K)
     return out
 
 

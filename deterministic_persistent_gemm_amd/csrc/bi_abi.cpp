@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include "bi.h"
+#include "bi_ffn.h"
 #include "bi_launch.h"
 #include "bi_moe.h"
 #include "bi_plan.h"
@@ -55,6 +56,52 @@ bi_status_t run_linear(int xkind, const void* x, int64_t ldx, const void* w, int
         return BI_EWORKSPACE;
     LinearArgs a{x, ldx, w, ldw, bias, y, y_bf16, ldy, (int)M, (int)N, (int)K};
     return launch_linear(xkind, a, p, ws, stream) == hipSuccess ? BI_OK : BI_EHIP;
+}
+
+// One matrix of a feed-forward call: `rows` rows of `cols` elements of `elem`
+// bytes, 16-byte aligned with a pitch that keeps every row so.
+bool matrix_ok(const void* p, int64_t ld, int64_t cols, int elem)
+{
+    return p && aligned16(p) && ld >= cols && (ld * elem) % 16 == 0 && ld < (int64_t(1) << 40);
+}
+
+// Sizes every feed-forward call shares; rows may be 0.
+bi_status_t check_sizes(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 0 || N < 0 || K < 0)
+        return BI_EINVAL;
+    if (N == 0 || K == 0 || N % 16 != 0 || K % 32 != 0)
+        return BI_EUNSUPPORTED;
+    if (M > (int64_t(1) << 30) || N > (int64_t(1) << 29) || K > (int64_t(1) << 29))
+        return BI_EUNSUPPORTED;
+    return BI_OK;
+}
+
+bool dtype_ok(int32_t d) { return d == BI_F32 || d == BI_BF16; }
+int dtype_bytes(int32_t d) { return d == BI_F32 ? 4 : 2; }
+
+// Codes and scales of an MXFP4 operand.
+bool mx_ok(const void* q, int64_t ldq, const void* sc, int64_t lds, int64_t K)
+{
+    return q && sc && aligned16(q) && (reinterpret_cast<uintptr_t>(sc) & 3u) == 0 && ldq >= K / 2 && ldq % 16 == 0 &&
+           lds >= K / 32 && lds % 4 == 0 && ldq < (int64_t(1) << 40) && lds < (int64_t(1) << 40);
+}
+
+size_t dh_bytes(int64_t M, int64_t I) { return (size_t)M * 2 * (size_t)I * 2; }
+
+// dx = dy W, dw = dy^T x; the operands have been checked
+bi_status_t run_bwd_products(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
+                             int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int32_t dw_dtype, int64_t lddw,
+                             int64_t M, int64_t N, int64_t K, hipStream_t stream)
+{
+    if (dx && M > 0 && launch_dgrad(dy, lddy, w, ldw, dx, lddx, M, N, K, stream) != hipSuccess)
+        return BI_EHIP;
+    if (!dw)
+        return BI_OK;
+    const int64_t es = dtype_bytes(dw_dtype);
+    const hipError_t e = M == 0 ? launch_zero_rows(dw, lddw * es, N, K * es, stream)
+                                : launch_wgrad(dy, lddy, x, ldx, dw, dw_dtype == BI_BF16, lddw, M, N, K, stream);
+    return e == hipSuccess ? BI_OK : BI_EHIP;
 }
 
 }  // namespace
@@ -315,6 +362,149 @@ bi_status_t bi_indexer_topk(const float* scores, int64_t ld, int64_t rows, int64
     if (!al(scores, 4) || !al(out, 4) || !al(row_start, 8) || !al(row_end, 8))
         return BI_EINVAL;
     return launch_topk_rows(scores, ld, rows, cols, row_start, row_end, topk, out, ld_out, stream) == hipSuccess
+               ? BI_OK
+               : BI_EHIP;
+}
+
+bi_status_t bi_gated_linear_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w13, int64_t ldw, int32_t gate,
+                                 uint16_t* y, int64_t ldy, uint16_t* h, int64_t ldh, int64_t M, int64_t I, int64_t H,
+                                 hipStream_t stream)
+{
+    if (gate != BI_GATE_SILU && gate != BI_GATE_GELU_TANH)
+        return BI_EINVAL;
+    bi_status_t st = check_sizes(M, I, H);
+    if (st != BI_OK || M == 0)
+        return st;
+    if (!matrix_ok(x, ldx, H, 2) || !matrix_ok(w13, ldw, H, 2) || !matrix_ok(y, ldy, I, 2) ||
+        (h && !matrix_ok(h, ldh, 2 * I, 2)))
+        return BI_EINVAL;
+    if (!gated_fits(ldx, ldw, M, I, H))
+        return BI_EUNSUPPORTED;
+    return launch_gated(x, ldx, w13, ldw, gate, y, ldy, h, ldh, M, I, H, stream) == hipSuccess ? BI_OK : BI_EHIP;
+}
+
+size_t bi_gated_linear_bwd_workspace_size(int64_t M, int64_t I)
+{
+    if (check_sizes(M, I, 32) != BI_OK || M == 0)
+        return 0;
+    return kDecodeCounterBytes + dh_bytes(M, I);
+}
+
+bi_status_t bi_gated_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                     const uint16_t* w13, int64_t ldw, const uint16_t* h, int64_t ldh, int32_t gate,
+                                     uint16_t* dx, int64_t lddx, void* dw, int32_t dw_dtype, int64_t lddw, int64_t M,
+                                     int64_t I, int64_t H, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    if ((gate != BI_GATE_SILU && gate != BI_GATE_GELU_TANH) || !dtype_ok(dw_dtype))
+        return BI_EINVAL;
+    bi_status_t st = check_sizes(M, I, H);
+    if (st != BI_OK || (!dx && !dw))
+        return st;
+    if (dw && !matrix_ok(dw, lddw, H, dtype_bytes(dw_dtype)))
+        return BI_EINVAL;
+    if (M > 0) {
+        if (!matrix_ok(dy, lddy, I, 2) || !matrix_ok(h, ldh, 2 * I, 2))
+            return BI_EINVAL;
+        if (dx && (!matrix_ok(dx, lddx, H, 2) || !matrix_ok(w13, ldw, H, 2)))
+            return BI_EINVAL;
+        if (dw && !matrix_ok(x, ldx, H, 2))
+            return BI_EINVAL;
+        if (!linear_bwd_fits(2 * I, dw ? ldx : 0, dx ? ldw : 0, M, 2 * I, H))
+            return BI_EUNSUPPORTED;
+        if (!ws || ws_bytes < kDecodeCounterBytes + dh_bytes(M, I) || !aligned16(ws))
+            return BI_EWORKSPACE;
+    }
+    uint16_t* dh = M > 0 ? reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(ws) + kDecodeCounterBytes) : nullptr;
+    if (M > 0 && launch_gate_bwd(dy, lddy, h, ldh, gate, dh, 2 * I, M, I, stream) != hipSuccess)
+        return BI_EHIP;
+    return run_bwd_products(dh, 2 * I, x, ldx, w13, ldw, dx, lddx, dw, dw_dtype, lddw, M, 2 * I, H, stream);
+}
+
+size_t bi_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    if (check_sizes(M, N, K) != BI_OK || M == 0)
+        return 0;
+    const size_t need = colsum_ws_bytes(M, N);
+    return need ? kDecodeCounterBytes + need : 0;
+}
+
+bi_status_t bi_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
+                               int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int32_t dw_dtype, int64_t lddw,
+                               float* db, int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
+                               hipStream_t stream)
+{
+    if (!dtype_ok(dw_dtype))
+        return BI_EINVAL;
+    bi_status_t st = check_sizes(M, N, K);
+    if (st != BI_OK || (!dx && !dw && !db))
+        return st;
+    if ((dw && !matrix_ok(dw, lddw, K, dtype_bytes(dw_dtype))) || (db && !aligned16(db)))
+        return BI_EINVAL;
+    if (M > 0) {
+        if (!matrix_ok(dy, lddy, N, 2))
+            return BI_EINVAL;
+        if (dx && (!matrix_ok(dx, lddx, K, 2) || !matrix_ok(w, ldw, K, 2)))
+            return BI_EINVAL;
+        if (dw && !matrix_ok(x, ldx, K, 2))
+            return BI_EINVAL;
+        if (!linear_bwd_fits(lddy, dw ? ldx : 0, dx ? ldw : 0, M, N, K))
+            return BI_EUNSUPPORTED;
+        const size_t need = bi_linear_bwd_workspace_size(M, N, K);
+        if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws)))
+            return BI_EWORKSPACE;
+    }
+    st = run_bwd_products(dy, lddy, x, ldx, w, ldw, dx, lddx, dw, dw_dtype, lddw, M, N, K, stream);
+    if (st != BI_OK || !db)
+        return st;
+    char* scratch = ws ? reinterpret_cast<char*>(ws) + kDecodeCounterBytes : nullptr;
+    const hipError_t e = M == 0 ? launch_zero_rows(db, N * 4, 1, N * 4, stream)
+                                : launch_colsum(dy, lddy, db, M, N, scratch, stream);
+    return e == hipSuccess ? BI_OK : BI_EHIP;
+}
+
+bi_status_t bi_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t ldx, uint8_t* q, int64_t ldq, uint8_t* sc,
+                              int64_t lds, int64_t rows, int64_t K, hipStream_t stream)
+{
+    if (!dtype_ok(x_dtype))
+        return BI_EINVAL;
+    bi_status_t st = check_sizes(rows, 16, K);
+    if (st != BI_OK || rows == 0)
+        return st;
+    if (!matrix_ok(x, ldx, K, dtype_bytes(x_dtype)) || !mx_ok(q, ldq, sc, lds, K))
+        return BI_EINVAL;
+    return launch_mx_quantize(x, x_dtype == BI_BF16, ldx, q, ldq, sc, lds, rows, K, stream) == hipSuccess ? BI_OK : BI_EHIP;
+}
+
+bi_status_t bi_dequantize_mxfp4(const uint8_t* q, int64_t ldq, const uint8_t* sc, int64_t lds, void* y, int32_t y_dtype,
+                                int64_t ldy, int64_t rows, int64_t K, hipStream_t stream)
+{
+    if (!dtype_ok(y_dtype))
+        return BI_EINVAL;
+    bi_status_t st = check_sizes(rows, 16, K);
+    if (st != BI_OK || rows == 0)
+        return st;
+    if (!matrix_ok(y, ldy, K, dtype_bytes(y_dtype)) || !mx_ok(q, ldq, sc, lds, K))
+        return BI_EINVAL;
+    return launch_mx_dequantize(q, ldq, sc, lds, y, y_dtype == BI_BF16, ldy, rows, K, stream) == hipSuccess ? BI_OK
+                                                                                                          : BI_EHIP;
+}
+
+bi_status_t bi_linear_mxfp4(const uint8_t* xq, int64_t ldxq, const uint8_t* xs, int64_t ldxs, const uint8_t* wq,
+                            int64_t ldwq, const uint8_t* wsc, int64_t ldws, const float* bias, void* y, int32_t y_dtype,
+                            int64_t ldy, int64_t M, int64_t N, int64_t K, hipStream_t stream)
+{
+    if (!dtype_ok(y_dtype))
+        return BI_EINVAL;
+    bi_status_t st = check_sizes(M, N, K);
+    if (st != BI_OK || M == 0)
+        return st;
+    if (!mx_ok(xq, ldxq, xs, ldxs, K) || !mx_ok(wq, ldwq, wsc, ldws, K) || (bias && !aligned16(bias)) ||
+        !matrix_ok(y, ldy, N, dtype_bytes(y_dtype)))
+        return BI_EINVAL;
+    if (!mx_fits(ldxq, ldxs, ldwq, ldws, M, N, K))
+        return BI_EUNSUPPORTED;
+    return launch_mx_linear(xq, ldxq, xs, ldxs, wq, ldwq, wsc, ldws, bias, y, y_dtype == BI_BF16, ldy, M, N, K,
+                            stream) == hipSuccess
                ? BI_OK
                : BI_EHIP;
 }

@@ -1,0 +1,98 @@
+// bi_gated.hip -- the gated linear layer, y = act(x Wg^T) * (x Wu^T), and the
+// elementwise part of its backward pass.
+#include "bi_ffn.h"
+#include "bi_tile.h"
+
+namespace bi {
+
+bool gated_fits(int64_t ldx, int64_t ldw, int64_t M, int64_t I, int64_t H)
+{
+    // per-lane byte offsets inside a tile's operands are 32 bits wide (the up
+    // rows lie I rows behind the gate rows), and the grid is one dimension
+    const int64_t lim = int64_t(1) << 32;
+    return 255 * ldx * 2 + H * 2 < lim && (I + 255) * ldw * 2 + H * 2 < lim && H < (int64_t(1) << 29) &&
+           ((M + 15) / 16) * ((I + 7) / 8) < (int64_t(1) << 31);
+}
+
+template <int BM, int BN, int WM, int WN, int KB, int R>
+static hipError_t gated_tile(TileArgs a, hipStream_t s)
+{
+    a.tiles_m = (a.M + BM - 1) / BM;
+    a.tiles_n = (a.N + BN / 2 - 1) / (BN / 2);
+    k_tile<BM, BN, WM, WN, KB, R, false, false, false, kEpiGated>
+        <<<(unsigned)(a.tiles_m * a.tiles_n), WM * WN * 64, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int64_t ldw, int gate, uint16_t* y,
+                        int64_t ldy, uint16_t* h, int64_t ldh, int64_t M, int64_t I, int64_t H, hipStream_t s)
+{
+    TileArgs a{};
+    a.a = reinterpret_cast<const unsigned char*>(x);
+    a.b = reinterpret_cast<const unsigned char*>(w13);
+    a.lda = ldx * 2;
+    a.ldb = ldw * 2;
+    a.y = y;
+    a.ldy = ldy;
+    a.y_bf16 = 1;
+    a.h = h;
+    a.ldh = ldh;
+    a.gate = gate == BI_GATE_SILU ? kGateSilu : kGateGeluTanh;
+    a.M = (int)M;
+    a.N = (int)I;
+    a.K = H;
+    return gated_tile<64, 64, 4, 1, 2, 4>(a, s);
+}
+
+// One thread per eight columns of a row: dy, the gate half and the up half of
+// h in, both halves of dh out.  With s = sigma(z(g)), act = g s:
+//   silu  act' = s + g s (1 - s)
+//   gelu  act' = s + g s (1 - s) z'(g),  z = c (g + b g^3)
+// dh is rounded to bf16 once: it is the matrix instructions' operand in both
+// products that follow.
+__global__ __launch_bounds__(256) void k_gate_bwd(const uint16_t* __restrict__ dy, int64_t lddy,
+                                                  const uint16_t* __restrict__ h, int64_t ldh, int gate,
+                                                  uint16_t* __restrict__ dh, int64_t lddh, int64_t M, int I)
+{
+    const uint32_t cpr = (uint32_t)I / 8;
+    const int64_t total = M * cpr;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / cpr;
+        const int c = (int)(i - m * cpr) * 8;
+        const u32x4 dv = *reinterpret_cast<const u32x4*>(dy + m * lddy + c);
+        const u32x4 gv = *reinterpret_cast<const u32x4*>(h + m * ldh + c);
+        const u32x4 uv = *reinterpret_cast<const u32x4*>(h + m * ldh + I + c);
+        u32x4 og, ou;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float rg[2], ru[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float d = __uint_as_float(q ? dv[j] & 0xffff0000u : dv[j] << 16);
+                const float gg = __uint_as_float(q ? gv[j] & 0xffff0000u : gv[j] << 16);
+                const float uu = __uint_as_float(q ? uv[j] & 0xffff0000u : uv[j] << 16);
+                const float sg = gate_sigma(gg, gate);
+                const float dz = gate == kGateSilu ? 1.0f : kGeluC2 * (1.0f + 3.0f * kGeluB * gg * gg);
+                const float act = gg * sg;
+                rg[q] = d * uu * (sg + act * (1.0f - sg) * dz);
+                ru[q] = d * act;
+            }
+            og[j] = pack_bf16(rg[0], rg[1]);
+            ou[j] = pack_bf16(ru[0], ru[1]);
+        }
+        *reinterpret_cast<u32x4*>(dh + m * lddh + c) = og;
+        *reinterpret_cast<u32x4*>(dh + m * lddh + I + c) = ou;
+    }
+}
+
+hipError_t launch_gate_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* h, int64_t ldh, int gate, uint16_t* dh,
+                           int64_t lddh, int64_t M, int64_t I, hipStream_t s)
+{
+    const int64_t blocks = (M * (I / 8) + 255) / 256;
+    const int64_t grid = blocks < 65536 ? blocks : 65536;
+    k_gate_bwd<<<(unsigned)grid, 256, 0, s>>>(dy, lddy, h, ldh, gate == BI_GATE_SILU ? kGateSilu : kGateGeluTanh, dh,
+                                              lddh, M, (int)I);
+    return hipGetLastError();
+}
+
+}  // namespace bi

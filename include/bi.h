@@ -221,7 +221,101 @@ bi_status_t bi_moe_grouped_gemm_ex(const uint16_t* x,
                                    int32_t* topk_ids, float* topk_probs, float* y,
                                    void* ws, size_t ws_bytes, hipStream_t stream);
 
-/* Workspace bytes the calls above need for a given problem (0 if none, or if
+/* ---------------------------------------------------------------------------
+ * Feed-forward layers: the gated linear layer with its backward pass, the
+ * backward pass of bi_linear_bf16, and 4-bit microscaled (MXFP4) operands.
+ *
+ * They keep the guarantee of the calls above -- a row of y, h or dx has the
+ * same bits whatever M it is computed in (fused-MoE page, "What's included":
+ * inference and training share one rounding) -- with one recipe for every
+ * shape: one fp32 accumulator per output element threaded through all of k in
+ * ascending order, by v_mfma_f32_16x16x32_bf16 on 32 k at a time (4-bit
+ * operands: v_mfma_scale_f32_16x16x128_f8f6f4 on 128).  dw and db sum over the
+ * batch, so their bits depend on M; they repeat exactly from run to run.
+ * All pointers are device pointers on the stream's device, 16-byte aligned
+ * unless stated; row pitches are in elements (bytes for codes and scales);
+ * outputs must not overlap inputs.  Rows past M and columns past the widths
+ * given are neither read nor written.
+ * ------------------------------------------------------------------------- */
+
+typedef enum {
+    BI_GATE_SILU = 0,      /* act(g) = g / (1 + exp(-g))                            */
+    BI_GATE_GELU_TANH = 1  /* act(g) = g / 2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+} bi_gate_t;
+
+/* y[M,I] = bf16( act(g) * u ),  [g | u] = x[M,H] . w13[2I,H]^T, in one launch.
+ * w13 is an nn.Linear weight of 2I rows: gate rows 0..I-1, then up rows.  The
+ * projections stay in fp32 until y's one rounding.  h: NULL, or [M, 2I] bf16,
+ * which receives the rounded projections for the backward pass (y does not
+ * depend on it).  Requires I % 16 == 0, H % 32 == 0, pitches that are multiples
+ * of 8 elements with ldx >= H, ldw >= H, ldy >= I, ldh >= 2I. */
+bi_status_t bi_gated_linear_bf16(const uint16_t* x, int64_t ldx,
+                                 const uint16_t* w13, int64_t ldw, int32_t gate,
+                                 uint16_t* y, int64_t ldy, uint16_t* h, int64_t ldh,
+                                 int64_t M, int64_t I, int64_t H, hipStream_t stream);
+
+/* Gradients of the gated linear layer at the stored projections h = [g | u]:
+ *   dh = bf16( [ dy * u * act'(g) | dy * act(g) ] )      fp32 math, one rounding
+ *   dx[M,H]  = bf16( dh . w13 )
+ *   dw[2I,H] = dh^T . x          bf16 or fp32 (dw_dtype)
+ * dx or dw may be NULL (not wanted; w13 is read for dx only, x for dw only, and
+ * the unread one may be NULL).  M == 0 clears dw.  ws holds dh:
+ * bi_gated_linear_bwd_workspace_size(M, I) bytes. */
+bi_status_t bi_gated_linear_bf16_bwd(const uint16_t* dy, int64_t lddy,
+                                     const uint16_t* x, int64_t ldx,
+                                     const uint16_t* w13, int64_t ldw,
+                                     const uint16_t* h, int64_t ldh, int32_t gate,
+                                     uint16_t* dx, int64_t lddx,
+                                     void* dw, int32_t dw_dtype, int64_t lddw,
+                                     int64_t M, int64_t I, int64_t H,
+                                     void* ws, size_t ws_bytes, hipStream_t stream);
+size_t bi_gated_linear_bwd_workspace_size(int64_t M, int64_t I);
+
+/* Gradients of bi_linear_bf16: dx[M,K] = bf16( dy[M,N] . w[N,K] ),
+ * dw[N,K] = dy^T . x (bf16 or fp32), db[N] = sum of dy's rows (fp32).  Any of
+ * dx, dw, db may be NULL, and w (read for dx only) and x (for dw only) with
+ * them.  M == 0 clears dw and db.  Requires N % 16 == 0, K % 32 == 0.  ws holds
+ * partial sums: bi_linear_bwd_workspace_size(M, N, K) bytes (0: none needed). */
+bi_status_t bi_linear_bf16_bwd(const uint16_t* dy, int64_t lddy,
+                               const uint16_t* x, int64_t ldx,
+                               const uint16_t* w, int64_t ldw,
+                               uint16_t* dx, int64_t lddx,
+                               void* dw, int32_t dw_dtype, int64_t lddw,
+                               float* db,
+                               int64_t M, int64_t N, int64_t K,
+                               void* ws, size_t ws_bytes, hipStream_t stream);
+size_t bi_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/* Rows of x (bf16 or fp32) to MXFP4: blocks of 32 values along a row share the
+ * scale 2^(s - 127), s = max(exponent byte of the block's largest magnitude
+ * - 2, 0); codes are x / scale rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and their negatives, ties to the even code, larger magnitudes to 6.  A
+ * block that holds an infinity or a NaN gets s = 255 (a NaN block) and zero
+ * codes.  q: [rows, K/2] bytes, the even element in the low half; sc: [rows,
+ * K/32] bytes.  Requires K % 32 == 0, ldx a multiple of 16 bytes, ldq (bytes) a
+ * multiple of 16 and lds (bytes) a multiple of 4; sc is 4-byte aligned. */
+bi_status_t bi_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t ldx,
+                              uint8_t* q, int64_t ldq, uint8_t* sc, int64_t lds,
+                              int64_t rows, int64_t K, hipStream_t stream);
+
+/* The values that codes and scales stand for, as bf16 or fp32 (exact wherever
+ * the type holds them; NaN for blocks with s = 255). */
+bi_status_t bi_dequantize_mxfp4(const uint8_t* q, int64_t ldq, const uint8_t* sc, int64_t lds,
+                                void* y, int32_t y_dtype, int64_t ldy,
+                                int64_t rows, int64_t K, hipStream_t stream);
+
+/* y[M,N] = x . w^T + bias of MXFP4 operands, fp32 accumulation, bf16 or fp32
+ * out.  The layouts of bi_quantize_mxfp4; scale rows are read in whole 32-bit
+ * words, so each, the last one included, must be readable up to K/32 rounded
+ * up to a multiple of 4 (the bytes past K/32 may hold anything).  Products
+ * below fp32's normal range may be flushed to zero.  Requires N % 16 == 0,
+ * K % 32 == 0. */
+bi_status_t bi_linear_mxfp4(const uint8_t* xq, int64_t ldxq, const uint8_t* xs, int64_t ldxs,
+                            const uint8_t* wq, int64_t ldwq, const uint8_t* wsc, int64_t ldws,
+                            const float* bias, void* y, int32_t y_dtype, int64_t ldy,
+                            int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/* Workspace bytes the linear and MoE calls need for a given problem (0 if none, or if
  * the arguments are invalid).  For the linear layer the workspace holds the
  * counter region and the k tile partials of the decode kernel M selects
  * (GateLinear page, "A correction to why the key excludes M": M picks the
