@@ -18,17 +18,27 @@ namespace bi {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+
+// A wave-uniform pointer in scalar registers (nothing is emitted where it
+// already is).
+__device__ __forceinline__ const void* uniform_ptr(const void* p)
+{
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    return (const void*)(uintptr_t)((uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v));
+}
+
 // 16 bytes per lane: a wave-uniform base, a 32-bit byte offset per lane.
 __device__ __forceinline__ void async16(uint32_t voff, const void* sbase, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(uniform_ptr(sbase)), "s"(lds)
                  : "memory", "m0");
 }
 
 // 4 bytes per lane.
 __device__ __forceinline__ void async4(uint32_t voff, const void* sbase, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(sbase), "s"(lds)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(uniform_ptr(sbase)), "s"(lds)
                  : "memory", "m0");
 }
 
@@ -36,8 +46,6 @@ __device__ __forceinline__ uint32_t lds_byte(const void* p)
 {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
-
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
 
 // s_waitcnt with vmcnt <= N (N < 64), other counters untouched
 template <int N>

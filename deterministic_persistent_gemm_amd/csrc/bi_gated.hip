@@ -41,6 +41,8 @@ hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int
     a.M = (int)M;
     a.N = (int)I;
     a.K = H;
+    if (M > 512)
+        return gated_tile<256, 256, 4, 2, 1, 4>(a, s);
     return gated_tile<64, 64, 4, 1, 2, 4>(a, s);
 }
 

@@ -38,6 +38,8 @@ hipError_t launch_dgrad(const uint16_t* dy, int64_t lddy, const uint16_t* w, int
     a.M = (int)M;
     a.N = (int)K;
     a.K = N;
+    if (M > 512)
+        return bwd_tile<256, 256, 4, 2, 1, 4, false>(a, s);
     return bwd_tile<64, 64, 4, 1, 2, 4, false>(a, s);
 }
 
@@ -55,6 +57,8 @@ hipError_t launch_wgrad(const uint16_t* dy, int64_t lddy, const uint16_t* x, int
     a.M = (int)N;
     a.N = (int)K;
     a.K = M;
+    if (M > 512)
+        return bwd_tile<256, 256, 4, 2, 1, 4, true>(a, s);
     return bwd_tile<64, 64, 4, 1, 2, 4, true>(a, s);
 }
 

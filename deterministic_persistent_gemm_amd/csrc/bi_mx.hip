@@ -163,6 +163,8 @@ hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, i
     a.M = (int)M;
     a.N = (int)N;
     a.K = K;
+    if (M > 512)
+        return mx_tile<256, 256, 4, 2, 1, 4>(a, s);
     return mx_tile<64, 64, 4, 1, 2, 4>(a, s);
 }
 
