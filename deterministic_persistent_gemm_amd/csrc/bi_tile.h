@@ -259,7 +259,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
         }
     }
 
-    auto issue_one = [&](int st, int t) {
+    auto issue_one = [&](int st, int t) __attribute__((always_inline)) {
         const uint32_t base = lds0 + (uint32_t)(st % R) * kStage;
         if (t < LA + LB) {
             const bool is_a = t < LA;
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
                    rg * 64 < BM ? p.sa + (int64_t)m0 * p.ldsa : p.sb + (int64_t)n0 * p.ldsb, dst);
         }
     };
-    auto issue = [&](int st) {
+    auto issue = [&](int st) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < LS; ++t)
             issue_one(st, t);
@@ -310,15 +310,15 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
     }
     const unsigned char* sarow = ring + A::kBytes + B::kBytes + (wm * FM * 16 + r) * 4 + g;
     const unsigned char* sbrow = ring + A::kBytes + B::kBytes + (BM + wn * FN * 16 + r) * 4 + g;
-    auto at = [&](int s) { return ((s / KB) % R) * kStage; };       // stage of slice s
-    auto frag_a = [&](int s, int f) {
+    auto at = [&](int s) __attribute__((always_inline)) { return ((s / KB) % R) * kStage; };       // stage of slice s
+    auto frag_a = [&](int s, int f) __attribute__((always_inline)) {
         return A::read((CA ? arow[CA ? f : 0] : arow[0] + f * 1024) + at(s) + (s % KB) * A::kSliceBytes);
     };
-    auto frag_b = [&](int s, int f) {
+    auto frag_b = [&](int s, int f) __attribute__((always_inline)) {
         return B::read((CB ? brow[CB ? f : 0] : brow[0] + f * 1024) + at(s) + (s % KB) * B::kSliceBytes);
     };
-    auto scale_a = [&](int s, int f) -> int { return sarow[at(s) + (s % KB) * (BM + BN) * 4 + f * 64]; };
-    auto scale_b = [&](int s, int f) -> int { return sbrow[at(s) + (s % KB) * (BM + BN) * 4 + f * 64]; };
+    auto scale_a = [&](int s, int f) __attribute__((always_inline)) -> int { return sarow[at(s) + (s % KB) * (BM + BN) * 4 + f * 64]; };
+    auto scale_b = [&](int s, int f) __attribute__((always_inline)) -> int { return sbrow[at(s) + (s % KB) * (BM + BN) * 4 + f * 64]; };
 
     f32x4 acc[FM][FN];
 #pragma unroll
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
 
     u32x4 xa[FM], xb[FM], wf[FN];
     int sxa[FP4 ? FM : 1], sxb[FP4 ? FM : 1], swf[FP4 ? FN : 1];
-    auto mfma = [&](const u32x4& x, const u32x4& wv, int sx, int sw, f32x4& c) {
+    auto mfma = [&](const u32x4& x, const u32x4& wv, int sx, int sw, f32x4& c) __attribute__((always_inline)) {
         if constexpr (FP4) {
             const i32x8 xv = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
             const i32x8 bv = {(int)wv[0], (int)wv[1], (int)wv[2], (int)wv[3], 0, 0, 0, 0};
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
     // once its MFMAs have issued.  Past the last slice, loads and reads touch
     // re-read data that nothing uses.
     auto step = [&](auto tail, int s, int j, u32x4 (&xc)[FM], int (&sxc)[FP4 ? FM : 1], u32x4 (&xn)[FM],
-                    int (&sxn)[FP4 ? FM : 1]) {
+                    int (&sxn)[FP4 ? FM : 1]) __attribute__((always_inline)) {
         const bool stage_end = j % KB == KB - 1;                   // compile-time after unrolling
         if (stage_end) {
             async_wait<(R - 3) * LS>();
@@ -410,7 +410,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
             }
         }
     };
-    auto body = [&](auto tail, int s) {
+    auto body = [&](auto tail, int s) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < U; j += 2) {
             step(tail, s + j, j, xa, sxa, xb, sxb);
