@@ -385,28 +385,32 @@ def bi_indexer_topk(scores, topk: int, row_start=None, row_end=None, out=None):
 BI_GATE_SILU, BI_GATE_GELU_TANH = 0, 1
 
 
-def _rows(t, dtype, shape, device, name, what, align=16):
-    """Row pitch (in elements) of a 2-D tensor the kernels take as rows of
-    contiguous elements, after checking it; a single row's pitch is its width
-    rounded up to `align` bytes, whatever stride torch reports for it."""
+_ELEM = {torch.bfloat16: 2, torch.float32: 4, torch.uint8: 1}
+
+
+def _rows(t, dtype, rows, cols, dev, name, what, align=16, transposed=False):
+    """Row pitch (in elements) of a 2-D tensor the kernels take as `rows` rows
+    of `cols` contiguous elements, after checking it; `transposed`: t is the
+    .t() view of that matrix.  A single row's pitch is its width rounded up to
+    `align` bytes, whatever stride torch reports for it."""
+    shape, stride = t.shape, t.stride()
+    if transposed and len(shape) == 2:
+        shape, stride = (shape[1], shape[0]), (stride[1], stride[0])
+    es = _ELEM[dtype]
+    if t.dtype == dtype and shape == (rows, cols) and dev >= 0 and t.get_device() == dev and t.data_ptr() % align == 0 \
+            and (stride[1] == 1 or cols == 1):
+        if rows <= 1:
+            return -(-cols * es // align) * align // es
+        if stride[0] >= cols and stride[0] * es % align == 0:
+            return stride[0]
     if t.dtype != dtype:
         raise TypeError(f"{name}: {what} must be {dtype}, got {t.dtype}")
-    if t.device != device or device.type != "cuda":
+    if dev < 0 or t.get_device() != dev:
         raise ValueError(f"{name}: tensors must be on one GPU; {what} is on {t.device}")
-    if t.dim() != 2 or (t.shape[0], t.shape[1]) != shape:
-        raise ValueError(f"{name}: {what} must have shape {shape}, got {tuple(t.shape)}")
-    es = t.element_size()
-    if shape[0] > 1:
-        ld = t.stride(0)
-        if ld < shape[1] or ld * es % align:
-            raise ValueError(f"{name}: {what} needs a row pitch >= {shape[1]} that is a multiple of {align} bytes")
-    else:
-        ld = -(-shape[1] * es // align) * align // es
-    if shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: rows of {what} must be contiguous")
-    if t.data_ptr() % align:
-        raise ValueError(f"{name}: {what} must be {align}-byte aligned")
-    return ld
+    if shape != (rows, cols):
+        raise ValueError(f"{name}: {what} must have shape {(rows, cols)}, got {tuple(shape)}")
+    raise ValueError(f"{name}: {what} needs contiguous rows at a pitch >= {cols} that is a multiple of {align} bytes, "
+                     f"{align}-byte aligned; its strides are {tuple(stride)}")
 
 
 def _sizes(name, N, K):
@@ -426,14 +430,13 @@ def _scratch(nbytes, device, given, name):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
-def _call(fn, name, device, *args):
-    """Enqueue on the tensors' device and its current stream."""
-    s = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, s)
+def _call(fn, name, dev, *args):
+    """Enqueue on GPU `dev`, on its current stream."""
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, s)
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != BI_OK:
         raise BIError(st, name)
 
@@ -463,13 +466,13 @@ def bi_gated_linear_bf16(x: torch.Tensor, w13t: torch.Tensor, gate: int = BI_GAT
     M, H = x.shape
     I = w13t.shape[1] // 2
     _sizes(name, I, H)
-    dev = x.device
-    ldx = _rows(x, torch.bfloat16, (M, H), dev, name, "x")
-    ldw = _rows(w13t.t(), torch.bfloat16, (2 * I, H), dev, name, "w13t.t()")
+    dev = x.get_device()
+    ldx = _rows(x, torch.bfloat16, M, H, dev, name, "x")
+    ldw = _rows(w13t, torch.bfloat16, 2 * I, H, dev, name, "w13t.t()", transposed=True)
     if out is None:
-        out = torch.empty((M, I), dtype=torch.bfloat16, device=dev)
-    ldy = _rows(out, torch.bfloat16, (M, I), dev, name, "out")
-    h = torch.empty((M, 2 * I), dtype=torch.bfloat16, device=dev) if save_h else None
+        out = x.new_empty((M, I))
+    ldy = _rows(out, torch.bfloat16, M, I, dev, name, "out")
+    h = x.new_empty((M, 2 * I)) if save_h else None
     _call(_lib.bi_gated_linear_bf16, name, dev, x.data_ptr(), ldx, w13t.data_ptr(), ldw, int(gate), out.data_ptr(), ldy,
           _dp(h), 2 * I, M, I, H)
     return (out, h) if save_h else out
@@ -488,18 +491,18 @@ def bi_gated_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, w13t: tor
     H = w13t.shape[0] if need_dx else x.shape[1] if need_dw else 32
     code = _dtype_code(dw_dtype, name, "dw_dtype")
     _sizes(name, I, H)
-    dev = dy.device
-    lddy = _rows(dy, torch.bfloat16, (M, I), dev, name, "dy")
-    ldh = _rows(h, torch.bfloat16, (M, 2 * I), dev, name, "h")
+    dev = dy.get_device()
+    lddy = _rows(dy, torch.bfloat16, M, I, dev, name, "dy")
+    ldh = _rows(h, torch.bfloat16, M, 2 * I, dev, name, "h")
     dx = dw = None
     ldx = ldw = 0
     if need_dx:
-        ldw = _rows(w13t.t(), torch.bfloat16, (2 * I, H), dev, name, "w13t.t()")
-        dx = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+        ldw = _rows(w13t, torch.bfloat16, 2 * I, H, dev, name, "w13t.t()", transposed=True)
+        dx = dy.new_empty((M, H))
     if need_dw:
-        ldx = _rows(x, torch.bfloat16, (M, H), dev, name, "x")
-        dw = torch.empty((2 * I, H), dtype=dw_dtype, device=dev)
-    ws = _scratch(_lib.bi_gated_linear_bwd_workspace_size(M, I), dev, ws, name)
+        ldx = _rows(x, torch.bfloat16, M, H, dev, name, "x")
+        dw = dy.new_empty((2 * I, H), dtype=dw_dtype)
+    ws = _scratch(_lib.bi_gated_linear_bwd_workspace_size(M, I), dy.device, ws, name)
     _call(_lib.bi_gated_linear_bf16_bwd, name, dev, dy.data_ptr(), lddy, _dp(x) if need_dw else None, ldx,
           _dp(w13t) if need_dx else None, ldw, h.data_ptr(), ldh, int(gate), _dp(dx), H, _dp(dw), code, H, M, I, H,
           _dp(ws), 0 if ws is None else ws.numel())
@@ -519,36 +522,38 @@ def bi_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tenso
     K = wt.shape[0] if need_dx else x.shape[1] if need_dw else 32
     code = _dtype_code(dw_dtype, name, "dw_dtype")
     _sizes(name, N, K)
-    dev = dy.device
-    lddy = _rows(dy, torch.bfloat16, (M, N), dev, name, "dy")
+    dev = dy.get_device()
+    lddy = _rows(dy, torch.bfloat16, M, N, dev, name, "dy")
     dx = dw = db = None
     ldx = ldw = 0
     if need_dx:
-        ldw = _rows(wt.t(), torch.bfloat16, (N, K), dev, name, "wt.t()")
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        ldw = _rows(wt, torch.bfloat16, N, K, dev, name, "wt.t()", transposed=True)
+        dx = dy.new_empty((M, K))
     if need_dw:
-        ldx = _rows(x, torch.bfloat16, (M, K), dev, name, "x")
-        dw = torch.empty((N, K), dtype=dw_dtype, device=dev)
+        ldx = _rows(x, torch.bfloat16, M, K, dev, name, "x")
+        dw = dy.new_empty((N, K), dtype=dw_dtype)
     if need_db:
-        db = torch.empty((N,), dtype=torch.float32, device=dev)
-    ws = _scratch(_lib.bi_linear_bwd_workspace_size(M, N, K), dev, ws, name)
+        db = dy.new_empty((N,), dtype=torch.float32)
+    ws = _scratch(_lib.bi_linear_bwd_workspace_size(M, N, K), dy.device, ws, name)
     _call(_lib.bi_linear_bf16_bwd, name, dev, dy.data_ptr(), lddy, _dp(x) if need_dw else None, ldx,
           _dp(wt) if need_dx else None, ldw, _dp(dx), K, _dp(dw), code, K, _dp(db), M, N, K, _dp(ws),
           0 if ws is None else ws.numel())
     return dx, dw, db
 
 
-def _mx_operand(q, s, device, name, what):
+def _mx_operand(q, s, dev, name, codes, scales):
     """Pitches (bytes) of an MXFP4 operand's codes [rows, K/2] and scales
     [rows, K/32], and its shape (rows, K)."""
     if q.dim() != 2:
-        raise ValueError(f"{name}: {what} codes are [rows, K/2]")
-    rows, K = q.shape[0], 2 * q.shape[1]
+        raise ValueError(f"{name}: {codes} is [rows, K/2]")
+    rows, half = q.shape
+    K = 2 * half
     _sizes(name, 16, K)
-    ldq = _rows(q, torch.uint8, (rows, K // 2), device, name, f"{what} codes")
-    lds = _rows(s, torch.uint8, (rows, K // 32), device, name, f"{what} scales", align=4)
-    if rows and s.storage_offset() + (rows - 1) * lds + (K // 32 + 3) // 4 * 4 > s.untyped_storage().nbytes():
-        raise ValueError(f"{name}: {what} scales must be readable in whole 32-bit words up to the last row's end")
+    kb = K // 32
+    ldq = _rows(q, torch.uint8, rows, half, dev, name, codes)
+    lds = _rows(s, torch.uint8, rows, kb, dev, name, scales, align=4)
+    if kb % 4 and rows and s.storage_offset() + (rows - 1) * lds + (kb + 3) // 4 * 4 > s.untyped_storage().nbytes():
+        raise ValueError(f"{name}: {scales} must be readable in whole 32-bit words up to the last row's end")
     return ldq, lds, rows, K
 
 
@@ -563,11 +568,11 @@ def bi_quantize_mxfp4(x: torch.Tensor):
         raise ValueError(f"{name}: x is [rows, K]")
     rows, K = x.shape
     _sizes(name, 16, K)
-    dev = x.device
-    ldx = _rows(x, x.dtype, (rows, K), dev, name, "x")
-    q = torch.empty((rows, K // 2), dtype=torch.uint8, device=dev)
+    dev = x.get_device()
+    ldx = _rows(x, x.dtype, rows, K, dev, name, "x")
+    q = x.new_empty((rows, K // 2), dtype=torch.uint8)
     lds = (K // 32 + 3) // 4 * 4
-    s = torch.empty((rows, lds), dtype=torch.uint8, device=dev)
+    s = x.new_empty((rows, lds), dtype=torch.uint8)
     _call(_lib.bi_quantize_mxfp4, name, dev, x.data_ptr(), code, ldx, q.data_ptr(), K // 2, s.data_ptr(), lds, rows, K)
     return q, s if lds == K // 32 else s[:, :K // 32]
 
@@ -576,9 +581,9 @@ def bi_dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, out_dtype: torch.dtype
     """The values [rows, K] (bf16 or fp32) that MXFP4 codes and scales stand for."""
     name = "bi_dequantize_mxfp4"
     code = _dtype_code(out_dtype, name, "out_dtype")
-    dev = q.device
-    ldq, lds, rows, K = _mx_operand(q, s, dev, name, "q")
-    y = torch.empty((rows, K), dtype=out_dtype, device=dev)
+    dev = q.get_device()
+    ldq, lds, rows, K = _mx_operand(q, s, dev, name, "q", "s")
+    y = q.new_empty((rows, K), dtype=out_dtype)
     _call(_lib.bi_dequantize_mxfp4, name, dev, q.data_ptr(), ldq, s.data_ptr(), lds, y.data_ptr(), code, K, rows, K)
     return y
 
@@ -591,16 +596,16 @@ def bi_linear_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: to
     batch-invariant."""
     name = "bi_linear_mxfp4"
     code = _dtype_code(out_dtype if out is None else out.dtype, name, "out")
-    dev = xq.device
-    ldxq, ldxs, M, K = _mx_operand(xq, xs, dev, name, "x")
-    ldwq, ldws, N, Kw = _mx_operand(wq, ws, dev, name, "w")
+    dev = xq.get_device()
+    ldxq, ldxs, M, K = _mx_operand(xq, xs, dev, name, "xq", "xs")
+    ldwq, ldws, N, Kw = _mx_operand(wq, ws, dev, name, "wq", "ws")
     if K != Kw:
         raise ValueError(f"{name}: x has k = {K} and w has k = {Kw}")
     _sizes(name, N, K)
-    _check_bias(bias, N, dev, name)
+    _check_bias(bias, N, xq.device, name)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    ldy = _rows(out, out.dtype, (M, N), dev, name, "out")
+        out = xq.new_empty((M, N), dtype=out_dtype)
+    ldy = _rows(out, out.dtype, M, N, dev, name, "out")
     _call(_lib.bi_linear_mxfp4, name, dev, xq.data_ptr(), ldxq, xs.data_ptr(), ldxs, wq.data_ptr(), ldwq, ws.data_ptr(),
           ldws, _dp(bias), out.data_ptr(), code, ldy, M, N, K)
     return out

@@ -180,16 +180,16 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
     using A = TileOperand<BM, KB, CA, false, FP4>;
     using B = TileOperand<BN, KB, CB, true, FP4>;
     constexpr int kSliceK = FP4 ? 128 : 32;
-    constexpr int kScaleStage = FP4 ? (BM + BN) * 4 * KB : 0;      // [slice][row][4 scale bytes]
+    constexpr int kScaleRows = (BM + BN + 63) / 64 * 64;           // A's, then B's; 64 rows per load
+    constexpr int kScaleStage = FP4 ? kScaleRows * 4 * KB : 0;     // [slice][row][4 scale bytes]
     constexpr int kStage = A::kBytes + B::kBytes + kScaleStage;
     constexpr int LA = A::kLoads / NW, LB = B::kLoads / NW;
-    constexpr int kScaleLoads = FP4 ? (BM + BN) / 64 * KB : 0;     // 64 rows of 4 bytes each
+    constexpr int kScaleLoads = FP4 ? kScaleRows / 64 * KB : 0;    // fewer than waves: some load the same twice
     constexpr int LSC = FP4 ? (kScaleLoads + NW - 1) / NW : 0;
     constexpr int LS = LA + LB + LSC;                              // loads per wave and stage
     constexpr int U = KB < 2 ? 2 : KB;                             // slices per loop body
     static_assert(LA * NW == A::kLoads && LB * NW == B::kLoads, "loads split evenly over the waves");
     static_assert(FN % (EPI == kEpiGated ? 4 : 2) == 0, "fragment pairs");
-    static_assert(!FP4 || (BM % 64 == 0 && BN % 64 == 0 && kScaleLoads % NW == 0), "scale loads");
     static_assert(R >= 3 && (R - 2) * LS < 64, "ring depth");
     static_assert(U % 2 == 0 && U % KB == 0, "whole stages per body");
     __shared__ __attribute__((aligned(1024))) unsigned char ring[R * kStage];
@@ -249,13 +249,13 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
     const int kbytes = (int)(FP4 ? p.K / 2 : p.K * 2);             // row operands
     const unsigned char* abase = p.a + (CA ? (int64_t)m0 * 2 : (int64_t)m0 * p.lda);
     const unsigned char* bbase = p.b + (CB ? (int64_t)n0 * 2 : (int64_t)n0 * p.ldb);
-    uint32_t soff[FP4 ? LSC : 1];
+    const unsigned char* srow[FP4 ? LSC : 1];                      // this lane's row of scales
     if constexpr (FP4) {
 #pragma unroll
         for (int t = 0; t < LSC; ++t) {
-            const int row = ((w * LSC + t) % ((BM + BN) / 64)) * 64 + lane;
-            soff[t] = row < BM ? (uint32_t)((int64_t)(min(m0 + row, p.M - 1) - m0) * p.ldsa)
-                               : (uint32_t)((int64_t)(min(n0 + B::paired(row - BM), p.N - 1) - n0) * p.ldsb);
+            const int row = ((w * LSC + t) % (kScaleRows / 64)) * 64 + lane;
+            srow[t] = row < BM ? p.sa + (int64_t)min(m0 + row, p.M - 1) * p.ldsa
+                               : p.sb + (int64_t)min(n0 + B::paired(min(row - BM, BN - 1)), p.N - 1) * p.ldsb;
         }
     }
 
@@ -277,12 +277,9 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
                 async16(voff[t] + (uint32_t)min(slice * 64 + kch[t] * 16, kbytes - 16), is_a ? abase : bbase, dst);
             }
         } else if constexpr (FP4) {
-            const int load = w * LSC + (t - LA - LB);
-            const int rg = load % ((BM + BN) / 64);                // group of 64 rows
-            const int slice = st * KB + load / ((BM + BN) / 64);
-            const uint32_t dst = uniform(base + A::kBytes + B::kBytes + load * 256);
-            async4(soff[t - LA - LB] + (uint32_t)min(slice, ns - 1) * 4u,
-                   rg * 64 < BM ? p.sa + (int64_t)m0 * p.ldsa : p.sb + (int64_t)n0 * p.ldsb, dst);
+            const int load = (w * LSC + (t - LA - LB)) % kScaleLoads;
+            const int slice = st * KB + load / (kScaleRows / 64);
+            async4(srow[t - LA - LB] + min(slice, ns - 1) * 4, uniform(base + A::kBytes + B::kBytes + load * 256));
         }
     };
     auto issue = [&](int st) __attribute__((always_inline)) {
@@ -317,8 +314,8 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
     auto frag_b = [&](int s, int f) __attribute__((always_inline)) {
         return B::read((CB ? brow[CB ? f : 0] : brow[0] + f * 1024) + at(s) + (s % KB) * B::kSliceBytes);
     };
-    auto scale_a = [&](int s, int f) __attribute__((always_inline)) -> int { return sarow[at(s) + (s % KB) * (BM + BN) * 4 + f * 64]; };
-    auto scale_b = [&](int s, int f) __attribute__((always_inline)) -> int { return sbrow[at(s) + (s % KB) * (BM + BN) * 4 + f * 64]; };
+    auto scale_a = [&](int s, int f) __attribute__((always_inline)) -> int { return sarow[at(s) + (s % KB) * kScaleRows * 4 + f * 64]; };
+    auto scale_b = [&](int s, int f) __attribute__((always_inline)) -> int { return sbrow[at(s) + (s % KB) * kScaleRows * 4 + f * 64]; };
 
     f32x4 acc[FM][FN];
 #pragma unroll
