@@ -68,13 +68,13 @@ __device__ __forceinline__ void async_wait_later(int later)
     }
 }
 
-// s_waitcnt lgkmcnt(0), other counters untouched
-__device__ __forceinline__ void lds_wait() { __builtin_amdgcn_s_waitcnt(0xF | (0x7 << 4) | (0x3 << 14)); }
-
 // A workgroup barrier without the fence of __syncthreads (whose release would
 // wait for every outstanding load); callers wait for exactly what the other
 // side needs first.
 __device__ __forceinline__ void wg_barrier() { asm volatile("s_barrier" : : : "memory"); }
+
+// The same after this wave's LDS reads have landed in registers.
+__device__ __forceinline__ void wg_barrier_reads_done() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
 
 // Transposing LDS read: in each group of 16 lanes, lane i points at 8 bytes
 // (four bf16) of row i / 4 of a 4-row block, and receives the four rows'

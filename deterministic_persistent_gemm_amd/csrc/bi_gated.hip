@@ -17,10 +17,10 @@ bool gated_fits(int64_t ldx, int64_t ldw, int64_t M, int64_t I, int64_t H)
 template <int BM, int BN, int WM, int WN, int KB, int R>
 static hipError_t gated_tile(TileArgs a, hipStream_t s)
 {
+    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, false, kEpiGated>;
     a.tiles_m = (a.M + BM - 1) / BM;
-    a.tiles_n = (a.N + BN / 2 - 1) / (BN / 2);
-    k_tile<BM, BN, WM, WN, KB, R, false, false, false, kEpiGated>
-        <<<(unsigned)(a.tiles_m * a.tiles_n), WM * WN * 64, 0, s>>>(a);
+    a.tiles_n = (a.N + C::kOutN - 1) / C::kOutN;
+    k_tile<C><<<(unsigned)(a.tiles_m * a.tiles_n), C::NW * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 

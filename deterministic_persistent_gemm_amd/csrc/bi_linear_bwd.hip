@@ -17,10 +17,10 @@ bool linear_bwd_fits(int64_t lddy, int64_t ldx, int64_t ldw, int64_t M, int64_t 
 template <int BM, int BN, int WM, int WN, int KB, int R, bool CA>
 static hipError_t bwd_tile(TileArgs a, hipStream_t s)
 {
+    using C = TileCfg<BM, BN, WM, WN, KB, R, CA, true, false, kEpiLinear>;
     a.tiles_m = (a.M + BM - 1) / BM;
     a.tiles_n = (a.N + BN - 1) / BN;
-    k_tile<BM, BN, WM, WN, KB, R, CA, true, false, kEpiLinear>
-        <<<(unsigned)(a.tiles_m * a.tiles_n), WM * WN * 64, 0, s>>>(a);
+    k_tile<C><<<(unsigned)(a.tiles_m * a.tiles_n), C::NW * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 

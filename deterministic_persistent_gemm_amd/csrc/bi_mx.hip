@@ -136,10 +136,10 @@ bool mx_fits(int64_t ldx, int64_t ldxs, int64_t ldw, int64_t ldws, int64_t M, in
 template <int BM, int BN, int WM, int WN, int KB, int R>
 static hipError_t mx_tile(TileArgs a, hipStream_t s)
 {
+    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, true, kEpiLinear>;
     a.tiles_m = (a.M + BM - 1) / BM;
     a.tiles_n = (a.N + BN - 1) / BN;
-    k_tile<BM, BN, WM, WN, KB, R, false, false, true, kEpiLinear>
-        <<<(unsigned)(a.tiles_m * a.tiles_n), WM * WN * 64, 0, s>>>(a);
+    k_tile<C><<<(unsigned)(a.tiles_m * a.tiles_n), C::NW * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -92,39 +92,60 @@ __device__ __forceinline__ int tile_of(int w, int tiles_m, int tiles_n, int& tn)
     return m0 + in % rows;
 }
 
+// How the weight side's output columns are dealt to fragment rows.  kPairs:
+// within each 32, register q of fragment f of lane group g is column
+// 8 g + 4 f + q (eight consecutive columns per lane); kSingle: one fragment,
+// columns in order.  Gated: kGated4 holds 32 gate rows, dealt as pairs, then the
+// 32 up rows of the same outputs; kGated2 16 and 16, kGated1 8 and 8, in order.
+enum TileDeal { kPairs, kSingle, kGated4, kGated2, kGated1 };
+
+template <int FN, int EPI> constexpr TileDeal tile_deal()
+{
+    if (EPI == kEpiGated)
+        return FN % 4 == 0 ? kGated4 : FN == 2 ? kGated2 : kGated1;
+    return FN % 2 == 0 ? kPairs : kSingle;
+}
+
+// The tile output a weight-side LDS row belongs to, and whether it is the up row.
+template <TileDeal D> __device__ __forceinline__ int deal_out(int p)
+{
+    const int pair = 8 * ((p >> 2) & 3) + 4 * ((p >> 4) & 1) + (p & 3);
+    return D == kPairs ? (p & ~31) + pair : D == kSingle ? p : D == kGated4 ? (p >> 6) * 32 + pair
+         : D == kGated2 ? (p >> 5) * 16 + (p & 15) : (p >> 4) * 8 + (p & 7);
+}
+template <TileDeal D> __device__ __forceinline__ int deal_up(int p)
+{
+    return D == kGated4 ? (p >> 5) & 1 : D == kGated2 ? (p >> 4) & 1 : D == kGated1 ? (p >> 3) & 1 : 0;
+}
+
 // One operand's place in a stage and how its lanes load and read it.
-//   ROWS output rows per tile, KB slices per stage, FP4: 128 k per slice.
+//   ROWS output rows per tile, KB slices per stage.
 // Row operands: [slice][row][64 bytes], the row's four 16-byte chunks permuted
 // by (row / 2) & 3 (free of bank conflicts for the 16-row fragment reads).
 // Column operands: [slice][32 k][ROWS bf16], 32-byte units of a k row permuted
-// by a key of the k row, so that the four k rows a transposing read touches
-// fall on different banks.  PAIR: the columns of a fragment pair are dealt out
-// as described above (the weight side).
-template <int ROWS, int KB, bool COL, bool PAIR, bool FP4>
+// by a key of the k row where four k rows span more than the 256 bytes of all
+// banks, so that the four k rows a transposing read touches fall on different
+// banks.  PAIR: the weight side's columns are dealt as kPairs.
+template <int ROWS, int KB, bool COL, bool PAIR>
 struct TileOperand {
-    static_assert(!(COL && FP4), "4-bit operands are stored by rows");
     static constexpr int kSliceBytes = ROWS * 64;
     static constexpr int kBytes = KB * kSliceBytes;
     static constexpr int kLoads = kBytes / 1024;        // 1 KiB wave loads per stage
     static constexpr int kPitch = COL ? ROWS * 2 : 64;
     static constexpr int kUnits = ROWS / 16;            // column operands: 32-byte units per k row
+    static_assert(ROWS % 16 == 0 && (!COL || kUnits == 1 || kUnits == 2 || kUnits == 4 || kUnits % 8 == 0), "tile rows");
 
     __device__ __forceinline__ static int col_key(int krow)
     {
         if constexpr (kUnits >= 8)
             return PAIR ? (krow & 3) << 1 : (krow & 3) | ((krow >> 3) & 1) << 2;
-        else
+        else if constexpr (kUnits == 4)
             return PAIR ? ((krow >> 1) & 1) << 1 : ((krow >> 1) & 1) | ((krow >> 3) & 1) << 1;
+        else
+            return 0;
     }
 
-    // The tile row a weight-side LDS row holds: within each 32, fragment f,
-    // row i is column 8 (i / 4) + 4 f + i % 4.
-    __device__ __forceinline__ static int paired(int p)
-    {
-        return (p & ~31) + 8 * ((p >> 2) & 3) + 4 * ((p >> 4) & 1) + (p & 3);
-    }
-
-    // LDS address of fragment f (16 rows), slice j, for lane (r, g); column
+    // LDS address of fragment f (16 rows), slice 0, for lane (r, g); column
     // operands: the first of two reads, the second 4 kPitch further.
     __device__ __forceinline__ static int frag_at(int f, int r, int g)
     {
@@ -154,6 +175,177 @@ struct TileOperand {
     }
 };
 
+// A tile: BM x BN outputs (gated: BN weight rows, BN / 2 outputs) on WM x WN
+// computing waves, R ring stages of KB slices.  CA, CB: operand A / B stored by
+// columns.
+template <int BM_, int BN_, int WM_, int WN_, int KB_, int R_, bool CA_, bool CB_, bool FP4_, int EPI_>
+struct TileCfg {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, R = R_, EPI = EPI_;
+    static constexpr bool CA = CA_, CB = CB_, FP4 = FP4_;
+    static constexpr int NW = WM * WN;
+    static constexpr int FM = BM / (WM * 16), FN = BN / (WN * 16);
+    static constexpr TileDeal kDeal = tile_deal<FN, EPI>();
+    using A = TileOperand<BM, KB, CA, false>;
+    using B = TileOperand<BN, KB, CB, kDeal == kPairs || kDeal == kGated4>;
+    static constexpr int kOutN = EPI == kEpiGated ? BN / 2 : BN;       // output columns per tile
+    static constexpr int kSliceK = FP4 ? 128 : 32;
+    static constexpr int kScaleRows = (BM + BN + 63) / 64 * 64;        // A's, then B's; 64 rows per load
+    static constexpr int kScaleAt = A::kBytes + B::kBytes;             // [slice][row][4 scale bytes]
+    static constexpr int kScaleLoads = FP4 ? kScaleRows / 64 * KB : 0;
+    static constexpr int kStage = kScaleAt + (FP4 ? kScaleRows * 4 * KB : 0);
+    static constexpr int kRing = R * kStage;
+    static_assert(FM * WM * 16 == BM && FN * WN * 16 == BN, "whole fragments per wave");
+    static_assert(!(FP4 && (CA || CB)), "4-bit operands are stored by rows");
+    static_assert(EPI != kEpiGated || !CB, "the gated weight is stored by rows");
+};
+
+// The loads of a stage, spread over NL loading waves (this one is `wl`).
+// Row operands: a load covers 16 tile rows of one slice; lane i lands at row
+// i / 4, chunk position i % 4 and fetches the chunk that belongs there.  Rows
+// past the end read the last row, chunks past the end of k the last chunk:
+// neither reaches a stored result.  Column operands: a load covers 1024 / pitch
+// k rows of one slice, columns past the end read the last eight.
+template <typename C, int NL>
+struct TileLoads {
+    using A = typename C::A;
+    using B = typename C::B;
+    static constexpr int LA = A::kLoads / NL, LB = B::kLoads / NL;
+    static constexpr int LSC = (C::kScaleLoads + NL - 1) / NL;         // past the last: the same loads again
+    static constexpr int LS = LA + LB + LSC;                           // loads per wave and stage
+    static_assert(LA * NL == A::kLoads && LB * NL == B::kLoads, "loads split evenly over the waves");
+
+    uint32_t voff[LA + LB];                                            // row operands: row offset; column: first column's
+    int kch[LA + LB];                                                  // row operands: chunk; column: k row in the slice
+    const unsigned char* srow[LSC > 0 ? LSC : 1];                      // this lane's row of scales
+    const unsigned char *abase, *bbase;
+    int64_t lda, ldb, K;
+    int ns, kbytes, wl;
+    uint32_t lds0;
+
+    __device__ __forceinline__ void init(const TileArgs& p, unsigned char* ring, int wl_, int lane, int m0, int n0)
+    {
+        wl = wl_;
+        lds0 = lds_byte(ring);
+        K = p.K;
+        ns = (int)((p.K + C::kSliceK - 1) / C::kSliceK);
+        kbytes = (int)(C::FP4 ? p.K / 2 : p.K * 2);                    // row operands
+        lda = p.lda;
+        ldb = p.ldb;
+        abase = p.a + (C::CA ? (int64_t)m0 * 2 : (int64_t)m0 * p.lda);
+        bbase = p.b + (C::CB ? (int64_t)n0 * 2 : (int64_t)n0 * p.ldb);
+#pragma unroll
+        for (int t = 0; t < LA + LB; ++t) {
+            const bool is_a = t < LA;
+            const int load = is_a ? wl * LA + t : wl * LB + (t - LA);
+            if (is_a ? C::CA : C::CB) {
+                const int pitch = is_a ? A::kPitch : B::kPitch;
+                const int cpr = pitch / 16;                            // chunks per k row
+                const int per = 1024 / pitch;                          // k rows per load
+                const int krow = (load * per) % 32 + lane / cpr;
+                const int pos = lane % cpr;
+                const int key = is_a ? A::col_key(krow) : B::col_key(krow);
+                const int chunk = (((pos >> 1) ^ key) << 1) | (pos & 1);
+                const int first = is_a ? m0 : n0, total = is_a ? p.M : p.N;
+                voff[t] = (uint32_t)(min(first + chunk * 8, total - 8) - first) * 2u;
+                kch[t] = krow;
+            } else {
+                const int row = (load * 16) % (is_a ? C::BM : C::BN) + (lane >> 2);
+                kch[t] = (lane & 3) ^ ((row >> 1) & 3);
+                if (is_a) {
+                    voff[t] = (uint32_t)((int64_t)(min(m0 + row, p.M - 1) - m0) * p.lda);
+                } else {
+                    const int out = min(n0 + deal_out<C::kDeal>(row), p.N - 1);
+                    voff[t] = (uint32_t)((int64_t)(out - n0 + deal_up<C::kDeal>(row) * p.N) * p.ldb);
+                }
+            }
+        }
+        if constexpr (C::FP4) {
+#pragma unroll
+            for (int t = 0; t < LSC; ++t) {
+                const int row = ((wl * LSC + t) % (C::kScaleRows / 64)) * 64 + lane;
+                srow[t] = row < C::BM
+                              ? p.sa + (int64_t)min(m0 + row, p.M - 1) * p.ldsa
+                              : p.sb + (int64_t)min(n0 + deal_out<C::kDeal>(min(row - C::BM, C::BN - 1)), p.N - 1) * p.ldsb;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void issue_one(int st, int t) const
+    {
+        const uint32_t base = lds0 + (uint32_t)(st % C::R) * C::kStage;
+        if (t < LA + LB) {
+            const bool is_a = t < LA;
+            const int load = is_a ? wl * LA + t : wl * LB + (t - LA);
+            const uint32_t dst = uniform(base + (is_a ? 0 : A::kBytes) + load * 1024);
+            if (is_a ? C::CA : C::CB) {
+                const int pitch = is_a ? A::kPitch : B::kPitch;
+                const int slice = min(st * C::KB + load / (32 * pitch / 1024), ns - 1);
+                const int64_t ld = is_a ? lda : ldb;
+                const int64_t k0 = (int64_t)slice * 32;
+                const int krow = min(kch[t], (int)min((int64_t)31, K - 1 - k0));
+                async16(voff[t] + (uint32_t)krow * (uint32_t)ld, (is_a ? abase : bbase) + k0 * ld, dst);
+            } else {
+                const int slice = st * C::KB + load / ((is_a ? C::BM : C::BN) / 16);
+                async16(voff[t] + (uint32_t)min(slice * 64 + kch[t] * 16, kbytes - 16), is_a ? abase : bbase, dst);
+            }
+        } else if constexpr (C::FP4) {
+            const int load = (wl * LSC + (t - LA - LB)) % C::kScaleLoads;
+            const int slice = st * C::KB + load / (C::kScaleRows / 64);
+            async4(srow[t - LA - LB] + min(slice, ns - 1) * 4, uniform(base + C::kScaleAt + load * 256));
+        }
+    }
+
+    __device__ __forceinline__ void issue(int st) const
+    {
+#pragma unroll
+        for (int t = 0; t < LS; ++t)
+            issue_one(st, t);
+    }
+};
+
+// A computing wave's fragment and scale addresses.
+template <typename C>
+struct TileFrags {
+    const unsigned char* arow[C::CA ? C::FM : 1];
+    const unsigned char* brow[C::CB ? C::FN : 1];
+    const unsigned char *sarow, *sbrow;
+
+    __device__ __forceinline__ void init(const unsigned char* ring, int wm, int wn, int r, int g)
+    {
+#pragma unroll
+        for (int f = 0; f < (C::CA ? C::FM : 1); ++f)
+            arow[f] = ring + C::A::frag_at(wm * C::FM + f, r, g);
+#pragma unroll
+        for (int f = 0; f < (C::CB ? C::FN : 1); ++f)
+            brow[f] = ring + C::A::kBytes + C::B::frag_at(wn * C::FN + f, r, g);
+        sarow = ring + C::kScaleAt + (wm * C::FM * 16 + r) * 4 + g;
+        sbrow = ring + C::kScaleAt + (C::BM + wn * C::FN * 16 + r) * 4 + g;
+    }
+    // fragment f of slice j of the stage in slot `at` (a byte offset)
+    __device__ __forceinline__ u32x4 a(int at, int j, int f) const
+    {
+        return C::A::read((C::CA ? arow[C::CA ? f : 0] : arow[0] + f * 1024) + at + j * C::A::kSliceBytes);
+    }
+    __device__ __forceinline__ u32x4 b(int at, int j, int f) const
+    {
+        return C::B::read((C::CB ? brow[C::CB ? f : 0] : brow[0] + f * 1024) + at + j * C::B::kSliceBytes);
+    }
+    __device__ __forceinline__ int sa(int at, int j, int f) const { return C::FP4 ? sarow[at + j * C::kScaleRows * 4 + f * 64] : 0; }
+    __device__ __forceinline__ int sb(int at, int j, int f) const { return C::FP4 ? sbrow[at + j * C::kScaleRows * 4 + f * 64] : 0; }
+};
+
+template <bool FP4>
+__device__ __forceinline__ void tile_mfma(const u32x4& x, const u32x4& w, int sx, int sw, f32x4& c)
+{
+    if constexpr (FP4) {
+        const i32x8 xv = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
+        const i32x8 wv = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv, c, 4, 4, 0, sw, 0, sx);
+    } else {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), c, 0, 0, 0);
+    }
+}
+
 // Zero what lies past the end of k: `valid` k values of this lane's eight
 // (bf16) or 32 (4-bit) belong to the problem.
 template <bool FP4>
@@ -170,152 +362,131 @@ __device__ __forceinline__ u32x4 mask_k(u32x4 v, int64_t valid)
     }
 }
 
-// BM x BN tile on WM x WN waves, KB slices per ring stage, R stages.  CA, CB:
-// operand A / B stored by columns.
-template <int BM, int BN, int WM, int WN, int KB, int R, bool CA, bool CB, bool FP4, int EPI>
-__global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
+// Stores a wave's outputs: row r of fragment fm, columns as dealt.
+template <typename C>
+__device__ __forceinline__ void tile_store(const TileArgs& p, const f32x4 (&acc)[C::FM][C::FN], int m0, int n0, int wm, int wn,
+                                           int r, int g)
 {
-    constexpr int NW = WM * WN;
-    constexpr int FM = BM / (WM * 16), FN = BN / (WN * 16);
-    using A = TileOperand<BM, KB, CA, false, FP4>;
-    using B = TileOperand<BN, KB, CB, true, FP4>;
-    constexpr int kSliceK = FP4 ? 128 : 32;
-    constexpr int kScaleRows = (BM + BN + 63) / 64 * 64;           // A's, then B's; 64 rows per load
-    constexpr int kScaleStage = FP4 ? kScaleRows * 4 * KB : 0;     // [slice][row][4 scale bytes]
-    constexpr int kStage = A::kBytes + B::kBytes + kScaleStage;
-    constexpr int LA = A::kLoads / NW, LB = B::kLoads / NW;
-    constexpr int kScaleLoads = FP4 ? kScaleRows / 64 * KB : 0;    // fewer than waves: some load the same twice
-    constexpr int LSC = FP4 ? (kScaleLoads + NW - 1) / NW : 0;
-    constexpr int LS = LA + LB + LSC;                              // loads per wave and stage
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    auto gated = [&](float gv, float uv) __attribute__((always_inline)) { return gv * gate_sigma(gv, p.gate) * uv; };
+#pragma unroll
+    for (int fm = 0; fm < C::FM; ++fm) {
+        const int m = m0 + (wm * C::FM + fm) * 16 + r;
+        if constexpr (C::kDeal == kGated4) {
+#pragma unroll
+            for (int q4 = 0; q4 < C::FN / 4; ++q4) {
+                const int n = n0 + (wn * (C::FN / 4) + q4) * 32 + 8 * g;
+                if (m < p.M && n < p.N) {
+                    u32x4 yv, gv, uv;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int f = i >> 1, q = (i & 1) * 2;
+                        const float g0 = acc[fm][q4 * 4 + f][q], g1 = acc[fm][q4 * 4 + f][q + 1];
+                        const float u0 = acc[fm][q4 * 4 + 2 + f][q], u1 = acc[fm][q4 * 4 + 2 + f][q + 1];
+                        yv[i] = pack_bf16(gated(g0, u0), gated(g1, u1));
+                        gv[i] = pack_bf16(g0, g1);
+                        uv[i] = pack_bf16(u0, u1);
+                    }
+                    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p.y) + (int64_t)m * p.ldy + n) = yv;
+                    if (p.h) {
+                        *reinterpret_cast<u32x4*>(p.h + (int64_t)m * p.ldh + n) = gv;
+                        *reinterpret_cast<u32x4*>(p.h + (int64_t)m * p.ldh + p.N + n) = uv;
+                    }
+                }
+            }
+        } else if constexpr (C::kDeal == kGated2 || C::kDeal == kGated1) {
+            // kGated2: gate and up columns 4 g .. 4 g + 3 in the lane's two fragments.
+            // kGated1: lane groups 0, 1 hold gate columns 4 g .., groups 2, 3 the
+            // up columns of groups 0, 1, which the lanes 32 apart exchange.
+            const f32x4 gv = acc[fm][0];
+            f32x4 uv = acc[fm][C::FN - 1];
+            int n = n0 + wn * 16 + 4 * g;
+            bool owner = true, second = false;
+            if constexpr (C::kDeal == kGated1) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    uv[q] = __shfl_xor(gv[q], 32);
+                n = n0 + wn * 8 + 4 * (g & 1);
+                owner = g < 2;
+                second = g >= 2;
+            }
+            if (m < p.M && n < p.N) {
+                const u32x2 hv = {pack_bf16(gv[0], gv[1]), pack_bf16(gv[2], gv[3])};
+                if (owner) {
+                    const u32x2 yv = {pack_bf16(gated(gv[0], uv[0]), gated(gv[1], uv[1])),
+                                      pack_bf16(gated(gv[2], uv[2]), gated(gv[3], uv[3]))};
+                    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(p.y) + (int64_t)m * p.ldy + n) = yv;
+                }
+                if (p.h) {
+                    *reinterpret_cast<u32x2*>(p.h + (int64_t)m * p.ldh + (second ? p.N : 0) + n) = hv;
+                    if constexpr (C::kDeal == kGated2)
+                        *reinterpret_cast<u32x2*>(p.h + (int64_t)m * p.ldh + p.N + n) =
+                            u32x2{pack_bf16(uv[0], uv[1]), pack_bf16(uv[2], uv[3])};
+                }
+            }
+        } else {
+            // kPairs: eight columns from two fragments; kSingle: four from one
+            constexpr int PF = C::kDeal == kPairs ? 2 : 1;
+#pragma unroll
+            for (int q2 = 0; q2 < C::FN / PF; ++q2) {
+                const int n = n0 + (wn * (C::FN / PF) + q2) * 16 * PF + 4 * PF * g;
+                if (m < p.M && n < p.N) {
+                    f32x4 v[PF];
+#pragma unroll
+                    for (int f = 0; f < PF; ++f) {
+                        v[f] = acc[fm][q2 * PF + f];
+                        if (p.bias)
+                            v[f] += *reinterpret_cast<const f32x4*>(p.bias + n + 4 * f);
+                    }
+                    if (p.y_bf16) {
+                        uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + (int64_t)m * p.ldy + n;
+                        const u32x2 lo = {pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3])};
+                        if constexpr (PF == 2)
+                            *reinterpret_cast<u32x4*>(y) =
+                                u32x4{lo[0], lo[1], pack_bf16(v[PF - 1][0], v[PF - 1][1]), pack_bf16(v[PF - 1][2], v[PF - 1][3])};
+                        else
+                            *reinterpret_cast<u32x2*>(y) = lo;
+                    } else {
+                        float* y = reinterpret_cast<float*>(p.y) + (int64_t)m * p.ldy + n;
+#pragma unroll
+                        for (int f = 0; f < PF; ++f)
+                            *reinterpret_cast<f32x4*>(y + 4 * f) = v[f];
+                    }
+                }
+            }
+        }
+    }
+}
+
+// Large tiles: every wave loads and computes.  A wave holds the fragments of
+// two slices: while the MFMAs of slice s issue, the fragments of slice s + 1
+// are read -- the A fragments first, then one B fragment after each group of
+// MFMAs that used slice s's fragment at that position, which is then free --
+// and the loads of a later stage are issued between the groups.
+template <typename C>
+__device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring, int block)
+{
+    constexpr int FM = C::FM, FN = C::FN, KB = C::KB, R = C::R;
+    constexpr bool FP4 = C::FP4;
+    constexpr int kSliceK = C::kSliceK;
+    using Loads = TileLoads<C, C::NW>;
+    constexpr int LS = Loads::LS;
     constexpr int U = KB < 2 ? 2 : KB;                             // slices per loop body
-    static_assert(LA * NW == A::kLoads && LB * NW == B::kLoads, "loads split evenly over the waves");
-    static_assert(FN % (EPI == kEpiGated ? 4 : 2) == 0, "fragment pairs");
     static_assert(R >= 3 && (R - 2) * LS < 64, "ring depth");
     static_assert(U % 2 == 0 && U % KB == 0, "whole stages per body");
-    __shared__ __attribute__((aligned(1024))) unsigned char ring[R * kStage];
 
     const int lane = threadIdx.x & 63, w = (int)uniform(threadIdx.x >> 6);
-    const int wm = w / WN, wn = w % WN;
+    const int wm = w / C::WN, wn = w % C::WN;
     const int r = lane & 15, g = lane >> 4;
     int tn;
-    const int tm = tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tn);
-    const int m0 = tm * BM;
-    constexpr int kOutN = EPI == kEpiGated ? BN / 2 : BN;          // output columns per tile
-    const int n0 = tn * kOutN;
+    const int tm = tile_of(block, p.tiles_m, p.tiles_n, tn);
+    const int m0 = tm * C::BM, n0 = tn * C::kOutN;
     const int ns = (int)((p.K + kSliceK - 1) / kSliceK);           // slices
-    const uint32_t lds0 = lds_byte(ring);
-
-    // ---- loads.  Row operands: load t of a wave covers 16 tile rows of one
-    // slice; lane i lands at row i / 4, chunk position i % 4 and fetches the
-    // chunk that belongs there.  Rows past the end read the last row, chunks
-    // past the end of k the last chunk: neither reaches a stored result.
-    // Column operands: a load covers 1024 / pitch k rows of one slice.
-    uint32_t voff[LA + LB];                                        // row operands: row offset
-    int kch[LA + LB];                                              // row: chunk; column: k row in slice
-#pragma unroll
-    for (int t = 0; t < LA + LB; ++t) {
-        const bool is_a = t < LA;
-        const int load = is_a ? w * LA + t : w * LB + (t - LA);
-        if (is_a ? CA : CB) {
-            const int pitch = is_a ? A::kPitch : B::kPitch;
-            const int cpr = pitch / 16;                            // chunks per k row
-            const int per = 1024 / pitch;                          // k rows per load
-            const int krow = (load * per) % 32 + lane / cpr;
-            const int pos = lane % cpr;
-            const int key = is_a ? A::col_key(krow) : B::col_key(krow);
-            const int chunk = (((pos >> 1) ^ key) << 1) | (pos & 1);
-            const int first = is_a ? m0 : n0, total = is_a ? p.M : p.N;
-            voff[t] = (uint32_t)(min(first + chunk * 8, total - 8) - first) * 2u;
-            kch[t] = krow;
-        } else {
-            const int rows = is_a ? BM : BN;
-            const int row = (load * 16) % rows + (lane >> 2);
-            kch[t] = (lane & 3) ^ ((row >> 1) & 3);
-            if (is_a) {
-                voff[t] = (uint32_t)((int64_t)(min(m0 + row, p.M - 1) - m0) * p.lda);
-            } else {
-                int q = B::paired(row);
-                if constexpr (EPI == kEpiGated) {
-                    // 64 LDS rows: 32 gate rows, then the 32 up rows of the same outputs
-                    const int out = min(n0 + (q >> 6) * 32 + (q & 31), p.N - 1);
-                    q = out - n0 + ((q >> 5) & 1) * p.N;
-                } else {
-                    q = min(n0 + q, p.N - 1) - n0;
-                }
-                voff[t] = (uint32_t)((int64_t)q * p.ldb);
-            }
-        }
-    }
-    const int kbytes = (int)(FP4 ? p.K / 2 : p.K * 2);             // row operands
-    const unsigned char* abase = p.a + (CA ? (int64_t)m0 * 2 : (int64_t)m0 * p.lda);
-    const unsigned char* bbase = p.b + (CB ? (int64_t)n0 * 2 : (int64_t)n0 * p.ldb);
-    const unsigned char* srow[FP4 ? LSC : 1];                      // this lane's row of scales
-    if constexpr (FP4) {
-#pragma unroll
-        for (int t = 0; t < LSC; ++t) {
-            const int row = ((w * LSC + t) % (kScaleRows / 64)) * 64 + lane;
-            srow[t] = row < BM ? p.sa + (int64_t)min(m0 + row, p.M - 1) * p.ldsa
-                               : p.sb + (int64_t)min(n0 + B::paired(min(row - BM, BN - 1)), p.N - 1) * p.ldsb;
-        }
-    }
-
-    auto issue_one = [&](int st, int t) __attribute__((always_inline)) {
-        const uint32_t base = lds0 + (uint32_t)(st % R) * kStage;
-        if (t < LA + LB) {
-            const bool is_a = t < LA;
-            const int load = is_a ? w * LA + t : w * LB + (t - LA);
-            const uint32_t dst = uniform(base + (is_a ? 0 : A::kBytes) + load * 1024);
-            if (is_a ? CA : CB) {
-                const int pitch = is_a ? A::kPitch : B::kPitch;
-                const int slice = st * KB + load / (32 * pitch / 1024);
-                const int64_t ld = is_a ? p.lda : p.ldb;
-                const int64_t k0 = (int64_t)min(slice, ns - 1) * 32;
-                const int krow = (int)min((int64_t)kch[t], p.K - 1 - k0);
-                async16(voff[t] + (uint32_t)krow * (uint32_t)ld, (is_a ? abase : bbase) + k0 * ld, dst);
-            } else {
-                const int slice = st * KB + load / ((is_a ? BM : BN) / 16);
-                async16(voff[t] + (uint32_t)min(slice * 64 + kch[t] * 16, kbytes - 16), is_a ? abase : bbase, dst);
-            }
-        } else if constexpr (FP4) {
-            const int load = (w * LSC + (t - LA - LB)) % kScaleLoads;
-            const int slice = st * KB + load / (kScaleRows / 64);
-            async4(srow[t - LA - LB] + min(slice, ns - 1) * 4, uniform(base + A::kBytes + B::kBytes + load * 256));
-        }
-    };
-    auto issue = [&](int st) __attribute__((always_inline)) {
-#pragma unroll
-        for (int t = 0; t < LS; ++t)
-            issue_one(st, t);
-    };
-
-    // ---- fragments
-    const unsigned char* arow[CA ? FM : 1];
-    const unsigned char* brow[CB ? FN : 1];
-    if constexpr (CA) {
-#pragma unroll
-        for (int f = 0; f < FM; ++f)
-            arow[f] = ring + A::frag_at(wm * FM + f, r, g);
-    } else {
-        arow[0] = ring + A::frag_at(wm * FM, r, g);
-    }
-    if constexpr (CB) {
-#pragma unroll
-        for (int f = 0; f < FN; ++f)
-            brow[f] = ring + A::kBytes + B::frag_at(wn * FN + f, r, g);
-    } else {
-        brow[0] = ring + A::kBytes + B::frag_at(wn * FN, r, g);
-    }
-    const unsigned char* sarow = ring + A::kBytes + B::kBytes + (wm * FM * 16 + r) * 4 + g;
-    const unsigned char* sbrow = ring + A::kBytes + B::kBytes + (BM + wn * FN * 16 + r) * 4 + g;
-    auto at = [&](int s) __attribute__((always_inline)) { return ((s / KB) % R) * kStage; };       // stage of slice s
-    auto frag_a = [&](int s, int f) __attribute__((always_inline)) {
-        return A::read((CA ? arow[CA ? f : 0] : arow[0] + f * 1024) + at(s) + (s % KB) * A::kSliceBytes);
-    };
-    auto frag_b = [&](int s, int f) __attribute__((always_inline)) {
-        return B::read((CB ? brow[CB ? f : 0] : brow[0] + f * 1024) + at(s) + (s % KB) * B::kSliceBytes);
-    };
-    auto scale_a = [&](int s, int f) __attribute__((always_inline)) -> int { return sarow[at(s) + (s % KB) * kScaleRows * 4 + f * 64]; };
-    auto scale_b = [&](int s, int f) __attribute__((always_inline)) -> int { return sbrow[at(s) + (s % KB) * kScaleRows * 4 + f * 64]; };
+    Loads loads;
+    loads.init(p, ring, w, lane, m0, n0);
+    TileFrags<C> frags;
+    frags.init(ring, wm, wn, r, g);
+    auto at = [&](int s) __attribute__((always_inline)) { return ((s / KB) % R) * C::kStage; };
 
     f32x4 acc[FM][FN];
 #pragma unroll
@@ -323,87 +494,70 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn)
             acc[fm][fn] = f32x4{0.f, 0.f, 0.f, 0.f};
-
     u32x4 xa[FM], xb[FM], wf[FN];
-    int sxa[FP4 ? FM : 1], sxb[FP4 ? FM : 1], swf[FP4 ? FN : 1];
-    auto mfma = [&](const u32x4& x, const u32x4& wv, int sx, int sw, f32x4& c) __attribute__((always_inline)) {
-        if constexpr (FP4) {
-            const i32x8 xv = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
-            const i32x8 bv = {(int)wv[0], (int)wv[1], (int)wv[2], (int)wv[3], 0, 0, 0, 0};
-            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, xv, c, 4, 4, 0, sw, 0, sx);
-        } else {
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv), __builtin_bit_cast(bf16x8, x),
-                                                        c, 0, 0, 0);
-        }
-    };
+    int sxa[FM], sxb[FM], swf[FN];
 
-    // ---- prologue: R - 1 stages in flight, the first one landed
+    // R - 1 stages in flight, the first one landed
 #pragma unroll
     for (int st = 0; st < R - 1; ++st)
-        issue(st);
+        loads.issue(st);
     async_wait<(R - 2) * LS>();
     wg_barrier();
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
-        xa[f] = frag_a(0, f);
-        if constexpr (FP4)
-            sxa[f] = scale_a(0, f);
+        xa[f] = frags.a(0, 0, f);
+        sxa[f] = frags.sa(0, 0, f);
     }
 #pragma unroll
     for (int f = 0; f < FN; ++f) {
-        wf[f] = frag_b(0, f);
-        if constexpr (FP4)
-            swf[f] = scale_b(0, f);
+        wf[f] = frags.b(0, 0, f);
+        swf[f] = frags.sb(0, 0, f);
     }
 
     // Slice s: where it is a stage's last, make the next stage visible (this
     // wave's loads of it waited for, then the barrier, which also tells that
     // every wave is done with the stage before this one, whose slot the loads
     // of this step refill); then the MFMAs of slice s with the reads of slice
-    // s + 1's fragments between them, each weight fragment replaced in place
-    // once its MFMAs have issued.  Past the last slice, loads and reads touch
-    // re-read data that nothing uses.
-    auto step = [&](auto tail, int s, int j, u32x4 (&xc)[FM], int (&sxc)[FP4 ? FM : 1], u32x4 (&xn)[FM],
-                    int (&sxn)[FP4 ? FM : 1]) __attribute__((always_inline)) {
+    // s + 1's fragments between them.  Past the last slice, loads and reads
+    // touch re-read data that nothing uses.
+    auto step = [&](auto tail, int s, int j, u32x4 (&xc)[FM], int (&sxc)[FM], u32x4 (&xn)[FM], int (&sxn)[FM])
+                    __attribute__((always_inline)) {
         const bool stage_end = j % KB == KB - 1;                   // compile-time after unrolling
         if (stage_end) {
             async_wait<(R - 3) * LS>();
             wg_barrier();
         }
         if constexpr (decltype(tail)::value) {
-            // this lane's slot: k values s * kSliceK + slot g
+            // this lane's slot: k values from s * kSliceK + g * kSliceK / 4 on
             const int64_t valid = p.K - (int64_t)s * kSliceK - g * (kSliceK / 4);
 #pragma unroll
             for (int f = 0; f < FM; ++f) {
                 xc[f] = mask_k<FP4>(xc[f], valid);
-                if constexpr (FP4)
-                    sxc[f] = valid > 0 ? sxc[f] : 127;
+                sxc[f] = valid > 0 ? sxc[f] : 127;
             }
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
                 wf[f] = mask_k<FP4>(wf[f], valid);
-                if constexpr (FP4)
-                    swf[f] = valid > 0 ? swf[f] : 127;
+                swf[f] = valid > 0 ? swf[f] : 127;
             }
         }
+        const int nat = at(s + 1), nj = (j + 1) % KB;
 #pragma unroll
         for (int f = 0; f < FM; ++f) {
-            xn[f] = frag_a(s + 1, f);
-            if constexpr (FP4)
-                sxn[f] = scale_a(s + 1, f);
+            xn[f] = frags.a(nat, nj, f);
+            sxn[f] = frags.sa(nat, nj, f);
         }
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn) {
 #pragma unroll
             for (int fm = 0; fm < FM; ++fm)
-                mfma(xc[fm], wf[fn], FP4 ? sxc[FP4 ? fm : 0] : 0, FP4 ? swf[FP4 ? fn : 0] : 0, acc[fm][fn]);
-            wf[fn] = frag_b(s + 1, fn);
-            if constexpr (FP4)
-                swf[fn] = scale_b(s + 1, fn);
+                tile_mfma<FP4>(xc[fm], wf[fn], sxc[fm], swf[fn], acc[fm][fn]);
+            wf[fn] = frags.b(nat, nj, fn);
+            swf[fn] = frags.sb(nat, nj, fn);
             if (stage_end) {
 #pragma unroll
                 for (int t = fn * LS / FN; t < (fn + 1) * LS / FN; ++t)
-                    issue_one(s / KB + R - 1, t);
+                    loads.issue_one(s / KB + R - 1, t);
             }
         }
     };
@@ -421,56 +575,117 @@ __global__ __launch_bounds__(WM * WN * 64) void k_tile(TileArgs p)
         body(std::true_type{}, whole);
     // the loads still in flight land before the workgroup's LDS is given away
     async_wait<0>();
+    tile_store<C>(p, acc, m0, n0, wm, wn, r, g);
+}
 
-    // ---- epilogue: rows m, eight consecutive columns per fragment pair
+// Small tiles, where a wave has too few MFMAs per slice to hide the latency of
+// its LDS reads and loads behind them: NL waves only load, up to R - 1 stages
+// ahead, and the computing waves read all fragments of a stage at once.  One
+// barrier per stage hands it over: a loading wave waits for its own loads of
+// the stage first, a computing wave for its reads of the stage before, whose
+// slot is refilled next.
+template <typename C, int NL>
+__device__ __forceinline__ void stream_body(const TileArgs& p, unsigned char* ring, int block)
+{
+    constexpr int FM = C::FM, FN = C::FN, KB = C::KB, R = C::R;
+    constexpr bool FP4 = C::FP4;
+    constexpr int kSliceK = C::kSliceK;
+    using Loads = TileLoads<C, NL>;
+    constexpr int LS = Loads::LS;
+    static_assert(R >= 2 && (R - 2) * LS < 64, "ring depth");
+
+    const int lane = threadIdx.x & 63, w = (int)uniform(threadIdx.x >> 6);
+    int tn;
+    const int tm = tile_of(block, p.tiles_m, p.tiles_n, tn);
+    const int m0 = tm * C::BM, n0 = tn * C::kOutN;
+    const int ns = (int)((p.K + kSliceK - 1) / kSliceK);
+    const int nst = (ns + KB - 1) / KB;                            // stages
+
+    if (w >= C::NW) {
+        Loads loads;
+        loads.init(p, ring, w - C::NW, lane, m0, n0);
+        for (int st = 0; st < R - 1 && st < nst; ++st)
+            loads.issue(st);
+        for (int st = 0; st < nst; ++st) {
+            async_wait_later<LS, R - 2>(min(R - 2, nst - 1 - st));
+            wg_barrier();
+            if (st + R - 1 < nst)
+                loads.issue(st + R - 1);
+        }
+        return;
+    }
+
+    const int wm = w / C::WN, wn = w % C::WN;
+    const int r = lane & 15, g = lane >> 4;
+    TileFrags<C> frags;
+    frags.init(ring, wm, wn, r, g);
+    f32x4 acc[FM][FN];
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
-        const int m = m0 + (wm * FM + fm) * 16 + r;
-        if constexpr (EPI == kEpiGated) {
+    for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-            for (int q4 = 0; q4 < FN / 4; ++q4) {
-                const int n = n0 + (wn * (FN / 4) + q4) * 32 + 8 * g;
-                if (m < p.M && n < p.N) {
-                    u32x4 yv, gv, uv;
+        for (int fn = 0; fn < FN; ++fn)
+            acc[fm][fn] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    auto stage = [&](auto tail, int st) __attribute__((always_inline)) {
+        wg_barrier_reads_done();
+        const int at = (st % R) * C::kStage;
+        u32x4 x[KB][FM], wf[KB][FN];
+        int sx[KB][FM], sw[KB][FN];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int f = i >> 1, q = (i & 1) * 2;
-                        const float g0 = acc[fm][q4 * 4 + f][q], g1 = acc[fm][q4 * 4 + f][q + 1];
-                        const float u0 = acc[fm][q4 * 4 + 2 + f][q], u1 = acc[fm][q4 * 4 + 2 + f][q + 1];
-                        yv[i] = pack_bf16(g0 * gate_sigma(g0, p.gate) * u0, g1 * gate_sigma(g1, p.gate) * u1);
-                        gv[i] = pack_bf16(g0, g1);
-                        uv[i] = pack_bf16(u0, u1);
-                    }
-                    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p.y) + (int64_t)m * p.ldy + n) = yv;
-                    if (p.h) {
-                        *reinterpret_cast<u32x4*>(p.h + (int64_t)m * p.ldh + n) = gv;
-                        *reinterpret_cast<u32x4*>(p.h + (int64_t)m * p.ldh + p.N + n) = uv;
-                    }
-                }
+        for (int j = 0; j < KB; ++j) {
+#pragma unroll
+            for (int f = 0; f < FM; ++f) {
+                x[j][f] = frags.a(at, j, f);
+                sx[j][f] = frags.sa(at, j, f);
             }
-        } else {
 #pragma unroll
-            for (int q2 = 0; q2 < FN / 2; ++q2) {
-                const int n = n0 + (wn * (FN / 2) + q2) * 32 + 8 * g;
-                if (m < p.M && n < p.N) {
-                    f32x4 lo = acc[fm][q2 * 2], hi = acc[fm][q2 * 2 + 1];
-                    if (p.bias) {
-                        lo += *reinterpret_cast<const f32x4*>(p.bias + n);
-                        hi += *reinterpret_cast<const f32x4*>(p.bias + n + 4);
-                    }
-                    if (p.y_bf16) {
-                        const u32x4 v = {pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]), pack_bf16(hi[0], hi[1]),
-                                         pack_bf16(hi[2], hi[3])};
-                        *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p.y) + (int64_t)m * p.ldy + n) = v;
-                    } else {
-                        float* y = reinterpret_cast<float*>(p.y) + (int64_t)m * p.ldy + n;
-                        *reinterpret_cast<f32x4*>(y) = lo;
-                        *reinterpret_cast<f32x4*>(y + 4) = hi;
-                    }
-                }
+            for (int f = 0; f < FN; ++f) {
+                wf[j][f] = frags.b(at, j, f);
+                sw[j][f] = frags.sb(at, j, f);
             }
         }
-    }
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            if constexpr (decltype(tail)::value) {
+                const int64_t valid = p.K - (int64_t)(st * KB + j) * kSliceK - g * (kSliceK / 4);
+#pragma unroll
+                for (int f = 0; f < FM; ++f) {
+                    x[j][f] = mask_k<FP4>(x[j][f], valid);
+                    sx[j][f] = valid > 0 ? sx[j][f] : 127;
+                }
+#pragma unroll
+                for (int f = 0; f < FN; ++f) {
+                    wf[j][f] = mask_k<FP4>(wf[j][f], valid);
+                    sw[j][f] = valid > 0 ? sw[j][f] : 127;
+                }
+            }
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+                for (int fm = 0; fm < FM; ++fm)
+                    tile_mfma<FP4>(x[j][fm], wf[j][fn], sx[j][fm], sw[j][fn], acc[fm][fn]);
+        }
+    };
+    const int whole = (int)(p.K / (kSliceK * KB));
+    for (int st = 0; st < whole; ++st)
+        stage(std::false_type{}, st);
+    if (whole < nst)
+        stage(std::true_type{}, whole);
+    tile_store<C>(p, acc, m0, n0, wm, wn, r, g);
+}
+
+template <typename C>
+__global__ __launch_bounds__(C::NW * 64) void k_tile(TileArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char ring[C::kRing];
+    tile_body<C>(p, ring, (int)blockIdx.x);
+}
+
+template <typename C, int NL>
+__global__ __launch_bounds__((C::NW + NL) * 64) void k_stream(TileArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char ring[C::kRing];
+    stream_body<C, NL>(p, ring, (int)blockIdx.x);
 }
 
 }  // namespace bi
