@@ -74,13 +74,11 @@ _lib.bi_linear_f32_noalloc.argtypes = [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _
 _lib.bi_gated_linear_bf16.argtypes = [_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _I64, _I64, _I64, _P]
 _lib.bi_gated_linear_bf16_bwd.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _I32, _I64,
                                           _I64, _I64, _I64, _P, _SZ, _P]
-_lib.bi_linear_bf16_bwd.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _P, _I64, _I64, _I64,
-                                    _P, _SZ, _P]
+_lib.bi_linear_bf16_bwd.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _P, _I64, _I64, _I64, _P]
 _lib.bi_quantize_mxfp4.argtypes = [_P, _I32, _I64, _P, _I64, _P, _I64, _I64, _I64, _P]
 _lib.bi_dequantize_mxfp4.argtypes = [_P, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64, _P]
 _lib.bi_linear_mxfp4.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _I64, _I64, _I64, _I64, _P]
 _lib.bi_gated_linear_bwd_workspace_size.argtypes = [_I64, _I64]
-_lib.bi_linear_bwd_workspace_size.argtypes = [_I64, _I64, _I64]
 for _f in (_lib.bi_linear_f32, _lib.bi_linear_bf16, _lib.bi_negctl_linear_f32, _lib.bi_lab_linear,
            _lib.bi_gated_linear_bf16, _lib.bi_gated_linear_bf16_bwd, _lib.bi_linear_bf16_bwd,
            _lib.bi_quantize_mxfp4, _lib.bi_dequantize_mxfp4, _lib.bi_linear_mxfp4,
@@ -90,7 +88,7 @@ for _f in (_lib.bi_linear_f32, _lib.bi_linear_bf16, _lib.bi_negctl_linear_f32, _
            _lib.bi_lab_lds_read, _lib.bi_lab_mfma_rate, _lib.bi_lab_l2_read):
     _f.restype = _I32
 for _f in (_lib.bi_linear_workspace_size, _lib.bi_lab_workspace_size, _lib.bi_moe_workspace_size,
-           _lib.bi_gated_linear_bwd_workspace_size, _lib.bi_linear_bwd_workspace_size):
+           _lib.bi_gated_linear_bwd_workspace_size):
     _f.restype = _SZ
 _lib.bi_status_str.restype = ctypes.c_char_p
 
@@ -510,8 +508,7 @@ def bi_gated_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, w13t: tor
 
 
 def bi_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tensor | None, need_dx: bool = True,
-                       need_dw: bool = True, need_db: bool = True, dw_dtype: torch.dtype = torch.bfloat16,
-                       ws: torch.Tensor | None = None):
+                       need_dw: bool = True, need_db: bool = True, dw_dtype: torch.dtype = torch.bfloat16):
     """Gradients of bi_linear_bf16: (dx [M, K] bf16, dw [N, K] of dw_dtype, db
     [N] fp32), each None if not wanted.  dy [M, N] bf16; x [M, K] is read for
     dw only and wt = weight.t() [K, N] for dx only; either may be None."""
@@ -534,10 +531,8 @@ def bi_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tenso
         dw = dy.new_empty((N, K), dtype=dw_dtype)
     if need_db:
         db = dy.new_empty((N,), dtype=torch.float32)
-    ws = _scratch(_lib.bi_linear_bwd_workspace_size(M, N, K), dy.device, ws, name)
     _call(_lib.bi_linear_bf16_bwd, name, dev, dy.data_ptr(), lddy, _dp(x) if need_dw else None, ldx,
-          _dp(wt) if need_dx else None, ldw, _dp(dx), K, _dp(dw), code, K, _dp(db), M, N, K, _dp(ws),
-          0 if ws is None else ws.numel())
+          _dp(wt) if need_dx else None, ldw, _dp(dx), K, _dp(dw), code, K, _dp(db), M, N, K)
     return dx, dw, db
 
 

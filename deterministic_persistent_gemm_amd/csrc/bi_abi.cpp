@@ -89,19 +89,23 @@ bool mx_ok(const void* q, int64_t ldq, const void* sc, int64_t lds, int64_t K)
 
 size_t dh_bytes(int64_t M, int64_t I) { return (size_t)M * 2 * (size_t)I * 2; }
 
-// dx = dy W, dw = dy^T x; the operands have been checked
-bi_status_t run_bwd_products(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
-                             int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int32_t dw_dtype, int64_t lddw,
-                             int64_t M, int64_t N, int64_t K, hipStream_t stream)
+// The gradients of a linear layer; the operands have been checked.  An empty
+// batch has no dx, and zero dw and db.
+bi_status_t run_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
+                           int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int32_t dw_dtype, int64_t lddw, float* db,
+                           int64_t M, int64_t N, int64_t K, hipStream_t stream)
 {
-    if (dx && M > 0 && launch_dgrad(dy, lddy, w, ldw, dx, lddx, M, N, K, stream) != hipSuccess)
-        return BI_EHIP;
-    if (!dw)
-        return BI_OK;
+    if (M > 0)
+        return launch_linear_bwd(dy, lddy, x, ldx, w, ldw, dx, lddx, dw, dw_dtype == BI_BF16, lddw, db, M, N, K,
+                                 stream) == hipSuccess
+                   ? BI_OK
+                   : BI_EHIP;
     const int64_t es = dtype_bytes(dw_dtype);
-    const hipError_t e = M == 0 ? launch_zero_rows(dw, lddw * es, N, K * es, stream)
-                                : launch_wgrad(dy, lddy, x, ldx, dw, dw_dtype == BI_BF16, lddw, M, N, K, stream);
-    return e == hipSuccess ? BI_OK : BI_EHIP;
+    if (dw && launch_zero_rows(dw, lddw * es, N, K * es, stream) != hipSuccess)
+        return BI_EHIP;
+    if (db && launch_zero_rows(db, N * 4, 1, N * 4, stream) != hipSuccess)
+        return BI_EHIP;
+    return BI_OK;
 }
 
 }  // namespace
@@ -417,21 +421,12 @@ bi_status_t bi_gated_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uin
     uint16_t* dh = M > 0 ? reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(ws) + kDecodeCounterBytes) : nullptr;
     if (M > 0 && launch_gate_bwd(dy, lddy, h, ldh, gate, dh, 2 * I, M, I, stream) != hipSuccess)
         return BI_EHIP;
-    return run_bwd_products(dh, 2 * I, x, ldx, w13, ldw, dx, lddx, dw, dw_dtype, lddw, M, 2 * I, H, stream);
-}
-
-size_t bi_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K)
-{
-    if (check_sizes(M, N, K) != BI_OK || M == 0)
-        return 0;
-    const size_t need = colsum_ws_bytes(M, N);
-    return need ? kDecodeCounterBytes + need : 0;
+    return run_linear_bwd(dh, 2 * I, x, ldx, w13, ldw, dx, lddx, dw, dw_dtype, lddw, nullptr, M, 2 * I, H, stream);
 }
 
 bi_status_t bi_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
                                int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int32_t dw_dtype, int64_t lddw,
-                               float* db, int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
-                               hipStream_t stream)
+                               float* db, int64_t M, int64_t N, int64_t K, hipStream_t stream)
 {
     if (!dtype_ok(dw_dtype))
         return BI_EINVAL;
@@ -449,17 +444,8 @@ bi_status_t bi_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uint16_t*
             return BI_EINVAL;
         if (!linear_bwd_fits(lddy, dw ? ldx : 0, dx ? ldw : 0, M, N, K))
             return BI_EUNSUPPORTED;
-        const size_t need = bi_linear_bwd_workspace_size(M, N, K);
-        if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws)))
-            return BI_EWORKSPACE;
     }
-    st = run_bwd_products(dy, lddy, x, ldx, w, ldw, dx, lddx, dw, dw_dtype, lddw, M, N, K, stream);
-    if (st != BI_OK || !db)
-        return st;
-    char* scratch = ws ? reinterpret_cast<char*>(ws) + kDecodeCounterBytes : nullptr;
-    const hipError_t e = M == 0 ? launch_zero_rows(db, N * 4, 1, N * 4, stream)
-                                : launch_colsum(dy, lddy, db, M, N, scratch, stream);
-    return e == hipSuccess ? BI_OK : BI_EHIP;
+    return run_linear_bwd(dy, lddy, x, ldx, w, ldw, dx, lddx, dw, dw_dtype, lddw, db, M, N, K, stream);
 }
 
 bi_status_t bi_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t ldx, uint8_t* q, int64_t ldq, uint8_t* sc,

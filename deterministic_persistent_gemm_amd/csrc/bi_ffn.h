@@ -20,15 +20,11 @@ hipError_t launch_gate_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* h, 
 
 // bi_linear_bwd.hip
 bool linear_bwd_fits(int64_t lddy, int64_t ldx, int64_t ldw, int64_t M, int64_t N, int64_t K);
-// dx [M, K] = dy [M, N] . w [N, K]
-hipError_t launch_dgrad(const uint16_t* dy, int64_t lddy, const uint16_t* w, int64_t ldw, uint16_t* dx, int64_t lddx,
-                        int64_t M, int64_t N, int64_t K, hipStream_t s);
-// dw [N, K] = dy [M, N]^T . x [M, K]; M >= 1
-hipError_t launch_wgrad(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, void* dw, int dw_bf16,
-                        int64_t lddw, int64_t M, int64_t N, int64_t K, hipStream_t s);
-// db [N] = sum of dy's rows, in fp32; ws: colsum_ws_bytes
-size_t colsum_ws_bytes(int64_t M, int64_t N);
-hipError_t launch_colsum(const uint16_t* dy, int64_t lddy, float* db, int64_t M, int64_t N, void* ws, hipStream_t s);
+// dx [M, K] = dy [M, N] . w [N, K], dw [N, K] = dy^T . x [M, K] and db [N] = the
+// sum of dy's rows, each where its output is not null; M >= 1
+hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
+                             int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int dw_bf16, int64_t lddw, float* db,
+                             int64_t M, int64_t N, int64_t K, hipStream_t s);
 // rows of `bytes` (a multiple of 4) at a pitch of `pitch` bytes, set to zero
 hipError_t launch_zero_rows(void* p, int64_t pitch, int64_t rows, int64_t bytes, hipStream_t s);
 

@@ -1,7 +1,9 @@
 // bi_gated.hip -- the gated linear layer, y = act(x Wg^T) * (x Wu^T), and the
 // elementwise part of its backward pass.
 #include "bi_ffn.h"
+#include "bi_plan.h"
 #include "bi_tile.h"
+#include "bi_tile_rule.h"
 
 namespace bi {
 
@@ -14,15 +16,26 @@ bool gated_fits(int64_t ldx, int64_t ldw, int64_t M, int64_t I, int64_t H)
            ((M + 15) / 16) * ((I + 7) / 8) < (int64_t(1) << 31);
 }
 
-template <int BM, int BN, int WM, int WN, int KB, int R>
+template <int BM, int BN, int WM, int WN, int KB, int R, int NL>
 static hipError_t gated_tile(TileArgs a, hipStream_t s)
 {
     using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, false, kEpiGated>;
     a.tiles_m = (a.M + BM - 1) / BM;
     a.tiles_n = (a.N + C::kOutN - 1) / C::kOutN;
-    k_tile<C><<<(unsigned)(a.tiles_m * a.tiles_n), C::NW * 64, 0, s>>>(a);
+    const unsigned grid = (unsigned)(a.tiles_m * a.tiles_n);
+    if constexpr (NL > 0)
+        k_stream<C, NL><<<grid, (C::NW + NL) * 64, 0, s>>>(a);
+    else
+        k_tile<C><<<grid, C::NW * 64, 0, s>>>(a);
     return hipGetLastError();
 }
+
+// bm x (weight rows / 2); the costs are explained in bi_tile_rule.h
+static const TileShape kGatedShapes[] = {
+    {16, 8, 0.69f, 0.041f, 1.00f},   {16, 16, 0.32f, 0.066f, 1.00f}, {32, 16, 0.61f, 0.075f, 1.10f},
+    {64, 16, 1.10f, 0.090f, 0.f},    {64, 32, 0.53f, 0.159f, 1.10f}, {128, 64, 1.20f, 0.289f, 0.f},
+    {128, 128, 0.82f, 0.547f, 0.f},  {256, 128, 4.28f, 0.651f, 0.f},
+};
 
 hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int64_t ldw, int gate, uint16_t* y,
                         int64_t ldy, uint16_t* h, int64_t ldh, int64_t M, int64_t I, int64_t H, hipStream_t s)
@@ -41,9 +54,16 @@ hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int
     a.M = (int)M;
     a.N = (int)I;
     a.K = H;
-    if (M > 512)
-        return gated_tile<256, 256, 4, 2, 1, 4>(a, s);
-    return gated_tile<64, 64, 4, 1, 2, 4>(a, s);
+    switch (pick_tile(kGatedShapes, 8, M, I, (H + 31) / 32, device_cu_count())) {
+    case 0: return gated_tile<16, 16, 1, 1, 8, 4, 4>(a, s);
+    case 1: return gated_tile<16, 32, 1, 1, 4, 4, 4>(a, s);
+    case 2: return gated_tile<32, 32, 2, 1, 4, 4, 4>(a, s);
+    case 3: return gated_tile<64, 32, 4, 1, 4, 4, 4>(a, s);
+    case 4: return gated_tile<64, 64, 4, 1, 2, 4, 0>(a, s);
+    case 5: return gated_tile<128, 128, 4, 2, 2, 4, 0>(a, s);
+    case 6: return gated_tile<128, 256, 2, 4, 1, 4, 0>(a, s);
+    default: return gated_tile<256, 256, 4, 2, 1, 4, 0>(a, s);
+    }
 }
 
 // One thread per eight columns of a row: dy, the gate half and the up half of

@@ -1,100 +1,44 @@
-// bi_linear_bwd.hip -- the products of the backward passes: dx = dy W (the
-// weight read by columns), dw = dy^T x (both operands read by columns) and the
-// column sums of dy.
+// bi_linear_bwd.hip -- the products of the backward passes in one launch:
+// dx = dy W (the weight read by columns), dw = dy^T x (both operands read by
+// columns) and the column sums of dy.
 #include "bi_ffn.h"
+#include "bi_plan.h"
 #include "bi_tile.h"
+#include "bi_tile_rule.h"
 
 namespace bi {
 
 bool linear_bwd_fits(int64_t lddy, int64_t ldx, int64_t ldw, int64_t M, int64_t N, int64_t K)
 {
-    const int64_t lim = int64_t(1) << 32;
+    const int64_t lim = int64_t(1) << 32, grid = int64_t(1) << 29;
     return 255 * lddy * 2 + N * 2 < lim && 32 * lddy * 2 + 512 < lim && 32 * ldw * 2 + 512 < lim &&
-           32 * ldx * 2 + 512 < lim && N < (int64_t(1) << 29) && ((M + 15) / 16) * ((K + 15) / 16) < (int64_t(1) << 31) &&
-           ((N + 15) / 16) * ((K + 15) / 16) < (int64_t(1) << 31);
+           32 * ldx * 2 + 512 < lim && N < (int64_t(1) << 29) && ((M + 31) / 32) * ((K + 31) / 32) < grid &&
+           ((N + 63) / 64) * ((K + 63) / 64) < grid;
 }
 
-template <int BM, int BN, int WM, int WN, int KB, int R, bool CA>
-static hipError_t bwd_tile(TileArgs a, hipStream_t s)
-{
-    using C = TileCfg<BM, BN, WM, WN, KB, R, CA, true, false, kEpiLinear>;
-    a.tiles_m = (a.M + BM - 1) / BM;
-    a.tiles_n = (a.N + BN - 1) / BN;
-    k_tile<C><<<(unsigned)(a.tiles_m * a.tiles_n), C::NW * 64, 0, s>>>(a);
-    return hipGetLastError();
-}
+// Column sums of dy: a workgroup takes 64 columns and all rows; thread (row
+// lane, group of 8 columns) adds its rows in ascending order in fp32, and the 64
+// row lanes are added in order.  No split over rows, so nothing is left to fold:
+// the workgroups run beside the products' tiles, whose time grows with M too.
+struct SumArgs {
+    const uint16_t* dy;
+    int64_t lddy;
+    float* db;
+    int64_t M;
+    int N;
+};
+constexpr int kSumCols = 64, kBwdThreads = 512, kSumLanes = kBwdThreads / 8;
 
-hipError_t launch_dgrad(const uint16_t* dy, int64_t lddy, const uint16_t* w, int64_t ldw, uint16_t* dx, int64_t lddx,
-                        int64_t M, int64_t N, int64_t K, hipStream_t s)
+__device__ __forceinline__ void colsum_body(const SumArgs& p, unsigned char* lds, int block)
 {
-    TileArgs a{};
-    a.a = reinterpret_cast<const unsigned char*>(dy);
-    a.b = reinterpret_cast<const unsigned char*>(w);
-    a.lda = lddy * 2;
-    a.ldb = ldw * 2;
-    a.y = dx;
-    a.ldy = lddx;
-    a.y_bf16 = 1;
-    a.M = (int)M;
-    a.N = (int)K;
-    a.K = N;
-    if (M > 512)
-        return bwd_tile<256, 256, 4, 2, 1, 4, false>(a, s);
-    return bwd_tile<64, 64, 4, 1, 2, 4, false>(a, s);
-}
-
-hipError_t launch_wgrad(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, void* dw, int dw_bf16,
-                        int64_t lddw, int64_t M, int64_t N, int64_t K, hipStream_t s)
-{
-    TileArgs a{};
-    a.a = reinterpret_cast<const unsigned char*>(dy);
-    a.b = reinterpret_cast<const unsigned char*>(x);
-    a.lda = lddy * 2;
-    a.ldb = ldx * 2;
-    a.y = dw;
-    a.ldy = lddw;
-    a.y_bf16 = dw_bf16;
-    a.M = (int)N;
-    a.N = (int)K;
-    a.K = M;
-    if (M > 512)
-        return bwd_tile<256, 256, 4, 2, 1, 4, true>(a, s);
-    return bwd_tile<64, 64, 4, 1, 2, 4, true>(a, s);
-}
-
-// Column sums: a workgroup takes 64 columns and a contiguous part of the rows;
-// thread (row lane, column group of 8) adds its rows in ascending order, the 32
-// row lanes are added in order, and a second launch adds the parts in order.
-// The split follows from (M, N) alone, so the bits repeat.
-constexpr int kSumCols = 64, kSumLanes = 32;
-
-static int64_t colsum_parts(int64_t M, int64_t N)
-{
-    const int64_t groups = (N + kSumCols - 1) / kSumCols;
-    int64_t parts = (512 + groups - 1) / groups;
-    const int64_t most = (M + 4 * kSumLanes - 1) / (4 * kSumLanes);
-    parts = parts < most ? parts : most;
-    return parts < 1 ? 1 : parts;
-}
-
-size_t colsum_ws_bytes(int64_t M, int64_t N)
-{
-    const int64_t parts = colsum_parts(M, N);
-    return parts > 1 ? (size_t)parts * (size_t)N * 4 : 0;
-}
-
-__global__ __launch_bounds__(256) void k_colsum(const uint16_t* __restrict__ dy, int64_t lddy, float* __restrict__ out,
-                                                int64_t M, int N, int64_t rows_per)
-{
-    __shared__ float part[kSumLanes][kSumCols + 1];
+    float(*part)[kSumCols + 1] = reinterpret_cast<float(*)[kSumCols + 1]>(lds);
     const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
-    const int c = blockIdx.x * kSumCols + cg * 8;
-    const int64_t lo = (int64_t)blockIdx.y * rows_per;
-    const int64_t hi = lo + rows_per < M ? lo + rows_per : M;
+    const int c = block * kSumCols + cg * 8;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (c < N) {
-        for (int64_t m = lo + rl; m < hi; m += kSumLanes) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(dy + m * lddy + c);
+    if (c < p.N) {
+#pragma unroll 4
+        for (int64_t m = rl; m < p.M; m += kSumLanes) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(p.dy + m * p.lddy + c);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 acc[2 * j] += __uint_as_float(v[j] << 16);
@@ -106,39 +50,169 @@ __global__ __launch_bounds__(256) void k_colsum(const uint16_t* __restrict__ dy,
     for (int j = 0; j < 8; ++j)
         part[rl][cg * 8 + j] = acc[j];
     __syncthreads();
-    const int col = blockIdx.x * kSumCols + threadIdx.x;
-    if (threadIdx.x < kSumCols && col < N) {
+    const int col = block * kSumCols + (int)threadIdx.x;
+    if (threadIdx.x < kSumCols && col < p.N) {
         float t = part[0][threadIdx.x];
         for (int l = 1; l < kSumLanes; ++l)
             t += part[l][threadIdx.x];
-        out[(int64_t)blockIdx.y * N + col] = t;
+        p.db[col] = t;
     }
 }
 
-__global__ __launch_bounds__(256) void k_colsum_fold(const float* __restrict__ parts, float* __restrict__ db, int N,
-                                                     int nparts)
+// Tile shapes of the two products, all on 512 threads so that any two can share
+// a launch: S32 streams (short batches: few tiles and a long sum over N),
+// the others load and compute in every wave.
+template <int SHAPE, bool CA> struct BwdShape;
+template <bool CA> struct BwdShape<0, CA> {
+    using C = TileCfg<32, 32, 2, 2, 4, 4, CA, true, false, kEpiLinear>;
+    static constexpr int NL = 4;
+};
+template <bool CA> struct BwdShape<1, CA> {
+    using C = TileCfg<64, 64, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
+    static constexpr int NL = 0;
+};
+template <bool CA> struct BwdShape<2, CA> {
+    using C = TileCfg<128, 128, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
+    static constexpr int NL = 0;
+};
+template <bool CA> struct BwdShape<3, CA> {
+    using C = TileCfg<256, 256, 4, 2, 1, 4, CA, true, false, kEpiLinear>;
+    static constexpr int NL = 0;
+};
+
+template <typename S>
+__device__ __forceinline__ void bwd_body(const TileArgs& p, unsigned char* ring, int block)
 {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= N)
-        return;
-    float t = parts[c];
-    for (int i = 1; i < nparts; ++i)
-        t += parts[(int64_t)i * N + c];
-    db[c] = t;
+    static_assert((S::C::NW + S::NL) * 64 == kBwdThreads, "one workgroup size");
+    if constexpr (S::NL > 0)
+        stream_body<typename S::C, S::NL>(p, ring, block);
+    else
+        tile_body<typename S::C>(p, ring, block);
 }
 
-hipError_t launch_colsum(const uint16_t* dy, int64_t lddy, float* db, int64_t M, int64_t N, void* ws, hipStream_t s)
+// Workgroups 0 .. ndx-1 tile dx, the next ndw dw, the rest sum columns.
+template <int DX, int DW>
+__global__ __launch_bounds__(kBwdThreads) void k_bwd(TileArgs dx, TileArgs dw, SumArgs sum, int ndx, int ndw)
 {
-    const int64_t parts = colsum_parts(M, N);
-    const int64_t rows_per = (M + parts - 1) / parts;
-    float* out = parts > 1 ? reinterpret_cast<float*>(ws) : db;
-    k_colsum<<<dim3((unsigned)((N + kSumCols - 1) / kSumCols), (unsigned)parts), 256, 0, s>>>(dy, lddy, out, M, (int)N,
-                                                                                          rows_per);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || parts == 1)
-        return e;
-    k_colsum_fold<<<(unsigned)((N + 255) / 256), 256, 0, s>>>(out, db, (int)N, (int)parts);
+    using SX = BwdShape<DX, false>;
+    using SW = BwdShape<DW, true>;
+    constexpr int kRing = SX::C::kRing > SW::C::kRing ? SX::C::kRing : SW::C::kRing;
+    static_assert(kRing >= kSumLanes * (kSumCols + 1) * 4, "column sums fit the ring");
+    __shared__ __attribute__((aligned(1024))) unsigned char ring[kRing];
+    const int b = (int)blockIdx.x;
+    if (b < ndx)
+        bwd_body<SX>(dx, ring, b);
+    else if (b < ndx + ndw)
+        bwd_body<SW>(dw, ring, b - ndx);
+    else
+        colsum_body(sum, ring, b - ndx - ndw);
+}
+
+// the costs are explained in bi_tile_rule.h
+static const TileShape kDxShapes[] = {{32, 32, 0.70f, 0.084f, 0.83f}, {64, 64, 0.73f, 0.134f, 1.10f},
+                                      {128, 128, 1.40f, 0.255f, 0.f}, {256, 256, 2.82f, 0.655f, 0.f}};
+static const TileShape kDwShapes[] = {{0, 0, 0.f, 0.f, 0.f},          {64, 64, 1.42f, 0.119f, 1.10f},
+                                      {128, 128, 2.91f, 0.263f, 0.f}, {256, 256, 6.41f, 0.658f, 0.f}};
+
+// The shape pairs that are built; a product alone may use its side of any.
+static const int kBwdPairs[][2] = {{0, 1}, {1, 1}, {2, 1}, {0, 2}, {1, 2}, {2, 2}, {2, 3}, {3, 3}};
+constexpr int kNumBwdPairs = (int)(sizeof(kBwdPairs) / sizeof(kBwdPairs[0]));
+
+// Both products in one launch: the longer of one tile's time and of all tiles'
+// times spread over the compute units, the last round half empty.
+static float pair_time(const TileShape& a, const TileShape& b, int64_t M, int64_t N, int64_t K, int cus)
+{
+    const float ta = tile_once(a, (N + 31) / 32), tb = tile_once(b, (M + 31) / 32);
+    const int64_t na = tile_count(a, M, K), nb = tile_count(b, N, K);
+    const float longest = ta > tb ? ta : tb, shortest = ta > tb ? tb : ta;
+    const float all = ((float)na * ta + (float)nb * tb) / (float)cus + (na + nb > cus ? 0.5f * shortest : 0.f);
+    return kTileLaunch + (all > longest ? all : longest);
+}
+
+template <int DX, int DW>
+static hipError_t bwd_launch(TileArgs dx, TileArgs dw, const SumArgs& sum, hipStream_t s)
+{
+    using CX = typename BwdShape<DX, false>::C;
+    using CW = typename BwdShape<DW, true>::C;
+    dx.tiles_m = (dx.M + CX::BM - 1) / CX::BM;
+    dx.tiles_n = (dx.N + CX::BN - 1) / CX::BN;
+    dw.tiles_m = (dw.M + CW::BM - 1) / CW::BM;
+    dw.tiles_n = (dw.N + CW::BN - 1) / CW::BN;
+    const int ndx = dx.y ? dx.tiles_m * dx.tiles_n : 0, ndw = dw.y ? dw.tiles_m * dw.tiles_n : 0;
+    const int nsum = sum.db ? (sum.N + kSumCols - 1) / kSumCols : 0;
+    k_bwd<DX, DW><<<(unsigned)(ndx + ndw + nsum), kBwdThreads, 0, s>>>(dx, dw, sum, ndx, ndw);
     return hipGetLastError();
+}
+
+static hipError_t bwd_launch_pair(int pair, const TileArgs& dx, const TileArgs& dw, const SumArgs& sum, hipStream_t s)
+{
+    switch (pair) {
+    case 0: return bwd_launch<0, 1>(dx, dw, sum, s);
+    case 1: return bwd_launch<1, 1>(dx, dw, sum, s);
+    case 2: return bwd_launch<2, 1>(dx, dw, sum, s);
+    case 3: return bwd_launch<0, 2>(dx, dw, sum, s);
+    case 4: return bwd_launch<1, 2>(dx, dw, sum, s);
+    case 5: return bwd_launch<2, 2>(dx, dw, sum, s);
+    case 6: return bwd_launch<2, 3>(dx, dw, sum, s);
+    default: return bwd_launch<3, 3>(dx, dw, sum, s);
+    }
+}
+
+hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
+                             int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int dw_bf16, int64_t lddw, float* db,
+                             int64_t M, int64_t N, int64_t K, hipStream_t s)
+{
+    TileArgs a{}, b{};
+    SumArgs sum{dy, lddy, db, M, (int)N};
+    a.a = b.a = reinterpret_cast<const unsigned char*>(dy);
+    a.lda = b.lda = lddy * 2;
+    a.b = reinterpret_cast<const unsigned char*>(w);
+    a.ldb = ldw * 2;
+    a.y = dx;
+    a.ldy = lddx;
+    a.y_bf16 = 1;
+    a.M = (int)M;
+    a.N = (int)K;
+    a.K = N;
+    b.b = reinterpret_cast<const unsigned char*>(x);
+    b.ldb = ldx * 2;
+    b.y = dw;
+    b.ldy = lddw;
+    b.y_bf16 = dw_bf16;
+    b.M = (int)N;
+    b.N = (int)K;
+    b.K = M;
+    const int cus = device_cu_count();
+    // each product's own best shape, and the best pair for one launch
+    const int bx = pick_tile(kDxShapes, 4, M, K, (N + 31) / 32, cus);
+    const int bw = 1 + pick_tile(kDwShapes + 1, 3, N, K, (M + 31) / 32, cus);
+    auto pair_with = [](int side, int shape) {
+        for (int i = 0; i < kNumBwdPairs; ++i)
+            if (kBwdPairs[i][side] == shape)
+                return i;
+        return 0;
+    };
+    if (!dw)
+        return bwd_launch_pair(pair_with(0, dx ? bx : 1), a, b, sum, s);
+    if (!dx)
+        return bwd_launch_pair(pair_with(1, bw), a, b, sum, s);
+    int best = 0;
+    float best_time = 0.f;
+    for (int i = 0; i < kNumBwdPairs; ++i) {
+        const float t = pair_time(kDxShapes[kBwdPairs[i][0]], kDwShapes[kBwdPairs[i][1]], M, N, K, cus);
+        if (i == 0 || t < best_time) {
+            best = i;
+            best_time = t;
+        }
+    }
+    const float apart = tile_time(kDxShapes[bx], M, K, (N + 31) / 32, cus) +
+                        tile_time(kDwShapes[bw], N, K, (M + 31) / 32, cus);
+    if (best_time <= apart)
+        return bwd_launch_pair(best, a, b, sum, s);
+    TileArgs none{};
+    SumArgs nosum{};
+    const hipError_t e = bwd_launch_pair(pair_with(0, bx), a, none, sum, s);
+    return e != hipSuccess ? e : bwd_launch_pair(pair_with(1, bw), none, b, nosum, s);
 }
 
 __global__ __launch_bounds__(256) void k_zero_rows(unsigned char* __restrict__ p, int64_t pitch, int64_t rows, int64_t words)

@@ -6,7 +6,9 @@
 // with the even element in the low half, and one scale byte s standing for
 // 2^(s - 127); s = 255 makes the block NaN.
 #include "bi_ffn.h"
+#include "bi_plan.h"
 #include "bi_tile.h"
+#include "bi_tile_rule.h"
 
 namespace bi {
 
@@ -133,15 +135,25 @@ bool mx_fits(int64_t ldx, int64_t ldxs, int64_t ldw, int64_t ldws, int64_t M, in
            K < (int64_t(1) << 30) && ((M + 15) / 16) * ((N + 15) / 16) < (int64_t(1) << 31);
 }
 
-template <int BM, int BN, int WM, int WN, int KB, int R>
+template <int BM, int BN, int WM, int WN, int KB, int R, int NL>
 static hipError_t mx_tile(TileArgs a, hipStream_t s)
 {
     using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, true, kEpiLinear>;
     a.tiles_m = (a.M + BM - 1) / BM;
     a.tiles_n = (a.N + BN - 1) / BN;
-    k_tile<C><<<(unsigned)(a.tiles_m * a.tiles_n), C::NW * 64, 0, s>>>(a);
+    const unsigned grid = (unsigned)(a.tiles_m * a.tiles_n);
+    if constexpr (NL > 0)
+        k_stream<C, NL><<<grid, (C::NW + NL) * 64, 0, s>>>(a);
+    else
+        k_tile<C><<<grid, C::NW * 64, 0, s>>>(a);
     return hipGetLastError();
 }
+
+// the costs are explained in bi_tile_rule.h; a slice is 128 k
+static const TileShape kMxShapes[] = {
+    {16, 16, 0.75f, 0.031f, 1.10f},   {16, 32, 0.60f, 0.043f, 1.06f}, {64, 64, 1.10f, 0.173f, 1.10f},
+    {128, 128, 1.84f, 0.451f, 1.10f}, {256, 128, 1.97f, 0.647f, 0.f}, {256, 256, 3.32f, 0.890f, 0.f},
+};
 
 hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, int64_t ldxs, const uint8_t* wq,
                             int64_t ldw, const uint8_t* wsc, int64_t ldws, const float* bias, void* y, int y_bf16,
@@ -163,9 +175,14 @@ hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, i
     a.M = (int)M;
     a.N = (int)N;
     a.K = K;
-    if (M > 512)
-        return mx_tile<256, 256, 4, 2, 1, 4>(a, s);
-    return mx_tile<64, 64, 4, 1, 2, 4>(a, s);
+    switch (pick_tile(kMxShapes, 6, M, N, (K + 127) / 128, device_cu_count())) {
+    case 0: return mx_tile<16, 16, 1, 1, 8, 4, 4>(a, s);
+    case 1: return mx_tile<16, 32, 1, 1, 4, 4, 4>(a, s);
+    case 2: return mx_tile<64, 64, 4, 1, 2, 4, 0>(a, s);
+    case 3: return mx_tile<128, 128, 2, 2, 1, 4, 0>(a, s);
+    case 4: return mx_tile<256, 128, 4, 2, 1, 4, 0>(a, s);
+    default: return mx_tile<256, 256, 4, 2, 1, 4, 0>(a, s);
+    }
 }
 
 }  // namespace bi

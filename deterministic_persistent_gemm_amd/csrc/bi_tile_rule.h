@@ -1,0 +1,66 @@
+// bi_tile_rule.h -- how a feed-forward product picks its tile shape (host).
+//
+// The shapes of one product differ only in time, never in bits, so the rule may
+// look at everything, M included.  A shape's time is estimated as
+//
+//   launch + rounds * (per_tile + slices * per_slice)
+//
+// with the two costs of one workgroup fitted to timings of 26 to 33 problems
+// drawn over M 1 .. 4096, widths 128 .. 12288 and k 256 .. 4096 on an MI355X
+// (fit within 5 to 20 percent).  rounds: workgroups per compute unit, counted
+// whole where a shape's LDS ring leaves room for one workgroup per compute unit
+// and as a fraction where several share it.  Over those problems the shapes
+// chosen this way come within 1 to 5 percent of the fastest of 18 shapes on
+// average; always taking 64 x 64 costs 1.33 to 1.48 times as much, always
+// 256 x 256 2.4 to 3.7 times.
+#pragma once
+
+#include <stdint.h>
+
+namespace bi {
+
+struct TileShape {
+    int bm, bn;            // outputs per tile: rows, columns
+    float per_tile;        // us
+    float per_slice;       // us
+    float share;           // several workgroups per compute unit: cost of each against alone; 0: one
+};
+
+constexpr float kTileLaunch = 1.7f;    // us
+
+inline int64_t tile_count(const TileShape& t, int64_t M, int64_t N)
+{
+    return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+}
+
+inline float tile_once(const TileShape& t, int64_t slices) { return t.per_tile + t.per_slice * (float)slices; }
+
+inline float tile_time(const TileShape& t, int64_t M, int64_t N, int64_t slices, int cus)
+{
+    const int64_t tiles = tile_count(t, M, N);
+    float rounds;
+    if (t.share > 0.f) {
+        rounds = (float)tiles / (float)cus * t.share;
+        rounds = rounds < 1.f ? 1.f : rounds;
+    } else {
+        rounds = (float)((tiles + cus - 1) / cus);
+    }
+    return kTileLaunch + rounds * tile_once(t, slices);
+}
+
+// The index of the fastest of n shapes.
+inline int pick_tile(const TileShape* t, int n, int64_t M, int64_t N, int64_t slices, int cus)
+{
+    int best = 0;
+    float best_time = tile_time(t[0], M, N, slices, cus);
+    for (int i = 1; i < n; ++i) {
+        const float time = tile_time(t[i], M, N, slices, cus);
+        if (time < best_time) {
+            best = i;
+            best_time = time;
+        }
+    }
+    return best;
+}
+
+}  // namespace bi

@@ -274,17 +274,15 @@ size_t bi_gated_linear_bwd_workspace_size(int64_t M, int64_t I);
 /* Gradients of bi_linear_bf16: dx[M,K] = bf16( dy[M,N] . w[N,K] ),
  * dw[N,K] = dy^T . x (bf16 or fp32), db[N] = sum of dy's rows (fp32).  Any of
  * dx, dw, db may be NULL, and w (read for dx only) and x (for dw only) with
- * them.  M == 0 clears dw and db.  Requires N % 16 == 0, K % 32 == 0.  ws holds
- * partial sums: bi_linear_bwd_workspace_size(M, N, K) bytes (0: none needed). */
+ * them.  M == 0 clears dw and db.  Requires N % 16 == 0, K % 32 == 0.  No
+ * workspace. */
 bi_status_t bi_linear_bf16_bwd(const uint16_t* dy, int64_t lddy,
                                const uint16_t* x, int64_t ldx,
                                const uint16_t* w, int64_t ldw,
                                uint16_t* dx, int64_t lddx,
                                void* dw, int32_t dw_dtype, int64_t lddw,
                                float* db,
-                               int64_t M, int64_t N, int64_t K,
-                               void* ws, size_t ws_bytes, hipStream_t stream);
-size_t bi_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
+                               int64_t M, int64_t N, int64_t K, hipStream_t stream);
 
 /* Rows of x (bf16 or fp32) to MXFP4: blocks of 32 values along a row share the
  * scale 2^(s - 127), s = max(exponent byte of the block's largest magnitude
