@@ -35,10 +35,11 @@ __device__ __forceinline__ void async16(uint32_t voff, const void* sbase, uint32
                  : "memory", "m0");
 }
 
-// 4 bytes per lane, a whole address per lane.
-__device__ __forceinline__ void async4(const void* g, uint32_t lds)
+// 4 bytes per lane.
+__device__ __forceinline__ void async4(uint32_t voff, const void* sbase, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" : : "v"(g), "s"(lds) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(uniform_ptr(sbase)), "s"(lds)
+                 : "memory", "m0");
 }
 
 __device__ __forceinline__ uint32_t lds_byte(const void* p)

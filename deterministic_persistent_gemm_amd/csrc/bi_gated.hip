@@ -62,7 +62,7 @@ hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int
     case 4: return gated_tile<64, 64, 4, 1, 2, 4, 0>(a, s);
     case 5: return gated_tile<128, 128, 4, 2, 2, 4, 0>(a, s);
     case 6: return gated_tile<128, 256, 2, 4, 1, 4, 0>(a, s);
-    default: return gated_tile<256, 256, 4, 2, 1, 4, 0>(a, s);
+    default: return gated_tile<256, 256, 2, 4, 1, 4, 0>(a, s);
     }
 }
 

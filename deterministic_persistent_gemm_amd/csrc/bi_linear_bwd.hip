@@ -76,7 +76,7 @@ template <bool CA> struct BwdShape<2, CA> {
     static constexpr int NL = 0;
 };
 template <bool CA> struct BwdShape<3, CA> {
-    using C = TileCfg<256, 256, 4, 2, 1, 4, CA, true, false, kEpiLinear>;
+    using C = TileCfg<256, 256, 2, 4, 1, 4, CA, true, false, kEpiLinear>;
     static constexpr int NL = 0;
 };
 

@@ -181,7 +181,7 @@ hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, i
     case 2: return mx_tile<64, 64, 4, 1, 2, 4, 0>(a, s);
     case 3: return mx_tile<128, 128, 2, 2, 1, 4, 0>(a, s);
     case 4: return mx_tile<256, 128, 4, 2, 1, 4, 0>(a, s);
-    default: return mx_tile<256, 256, 4, 2, 1, 4, 0>(a, s);
+    default: return mx_tile<256, 256, 2, 4, 1, 4, 0>(a, s);
     }
 }
 

@@ -189,11 +189,20 @@ struct TileCfg {
     using B = TileOperand<BN, KB, CB, kDeal == kPairs || kDeal == kGated4>;
     static constexpr int kOutN = EPI == kEpiGated ? BN / 2 : BN;       // output columns per tile
     static constexpr int kSliceK = FP4 ? 128 : 32;
-    static constexpr int kScaleRows = (BM + BN + 63) / 64 * 64;        // A's, then B's; 64 rows per load
-    static constexpr int kScaleAt = A::kBytes + B::kBytes;             // [slice][row][4 scale bytes]
-    static constexpr int kScaleLoads = FP4 ? kScaleRows / 64 * KB : 0;
-    static constexpr int kStage = kScaleAt + (FP4 ? kScaleRows * 4 * KB : 0);
-    static constexpr int kRing = R * kStage;
+    static constexpr int kStage = A::kBytes + B::kBytes;
+    // Scales travel in groups of four slices, [row][16 bytes], A's rows then B's:
+    // a 4-byte load then takes 16 bytes of each of 16 rows (a load of one slice's
+    // four bytes of 64 rows touches 64 cache lines, which cost the 256 x 256
+    // tile 30 percent of its time).  A stage of a whole number of groups brings
+    // its own; smaller stages each bring a part of the group after theirs, in a
+    // ring of three groups.
+    static constexpr int kGroup = (BM + BN) * 16;
+    static constexpr bool kGroupInStage = KB % 4 == 0;
+    static constexpr int kGroups = !FP4 ? 0 : kGroupInStage ? R * (KB / 4) : 3;
+    static constexpr int kScaleAt = R * kStage;
+    static constexpr int kScaleLoads = !FP4 ? 0 : (BM + BN) / 16 * KB / 4;     // per stage, 16 rows each
+    static constexpr int kRing = kScaleAt + kGroups * kGroup;
+    static_assert(!FP4 || kGroupInStage || ((BM + BN) / 16 * KB) % 4 == 0, "equal parts of a group per stage");
     static_assert(FM * WM * 16 == BM && FN * WN * 16 == BN, "whole fragments per wave");
     static_assert(!(FP4 && (CA || CB)), "4-bit operands are stored by rows");
     static_assert(EPI != kEpiGated || !CB, "the gated weight is stored by rows");
@@ -212,19 +221,28 @@ struct TileLoads {
     static constexpr int LA = A::kLoads / NL, LB = B::kLoads / NL;
     static constexpr int LSC = (C::kScaleLoads + NL - 1) / NL;         // past the last: the same loads again
     static constexpr int LS = LA + LB + LSC;                           // loads per wave and stage
+    static constexpr int kParts = C::FP4 && !C::kGroupInStage ? 4 / C::KB : 1;  // stages a scale group is spread over
+    static constexpr int PA = C::BM / 16 / kParts, PB = C::BN / 16 / kParts;    // loads of a part, by operand
+    static_assert(kParts == 1 || (PA * kParts * 16 == C::BM && PB * kParts * 16 == C::BN && PB % 2 == 0), "equal parts");
     static_assert(LA * NL == A::kLoads && LB * NL == B::kLoads, "loads split evenly over the waves");
 
     uint32_t voff[LA + LB];                                            // row operands: row offset; column: first column's
     int kch[LA + LB];                                                  // row operands: chunk; column: k row in the slice
-    const unsigned char* srow[LSC > 0 ? LSC : 1];                      // this lane's row of scales
+    // scales, per load: the operand's first row of the tile, its pitch, the lane's
+    // row in part 0, rows to the operand's end and per part, the place in a group
+    const unsigned char* sbase[LSC > 0 ? LSC : 1];
+    uint32_t sld[LSC > 0 ? LSC : 1];
+    int srow[LSC > 0 ? LSC : 1], slast[LSC > 0 ? LSC : 1], sstep[LSC > 0 ? LSC : 1], sgroup[LSC > 0 ? LSC : 1];
+    uint32_t sdst[LSC > 0 ? LSC : 1];
     const unsigned char *abase, *bbase;
     int64_t lda, ldb, K;
-    int ns, kbytes, wl;
+    int ns, kbytes, wl, lane;
     uint32_t lds0;
 
-    __device__ __forceinline__ void init(const TileArgs& p, unsigned char* ring, int wl_, int lane, int m0, int n0)
+    __device__ __forceinline__ void init(const TileArgs& p, unsigned char* ring, int wl_, int lane_, int m0, int n0)
     {
         wl = wl_;
+        lane = lane_;
         lds0 = lds_byte(ring);
         K = p.K;
         ns = (int)((p.K + C::kSliceK - 1) / C::kSliceK);
@@ -262,11 +280,40 @@ struct TileLoads {
         if constexpr (C::FP4) {
 #pragma unroll
             for (int t = 0; t < LSC; ++t) {
-                const int row = ((wl * LSC + t) % (C::kScaleRows / 64)) * 64 + lane;
-                srow[t] = row < C::BM
-                              ? p.sa + (int64_t)min(m0 + row, p.M - 1) * p.ldsa
-                              : p.sb + (int64_t)min(n0 + deal_out<C::kDeal>(min(row - C::BM, C::BN - 1)), p.N - 1) * p.ldsb;
+                const int load = (wl * LSC + t) % C::kScaleLoads;      // past the last: the same again
+                const int j = load % (PA + PB);
+                const bool is_a = j < PA;
+                const int row = (is_a ? j : j - PA) * 16 + (lane >> 2);
+                sbase[t] = is_a ? p.sa + (int64_t)m0 * p.ldsa : p.sb + (int64_t)n0 * p.ldsb;
+                sld[t] = (uint32_t)(is_a ? p.ldsa : p.ldsb);
+                srow[t] = is_a ? row : deal_out<C::kDeal>(row);
+                slast[t] = (is_a ? p.M - m0 : p.N - n0) - 1;
+                sstep[t] = (is_a ? PA : PB) * 16;
+                sgroup[t] = load / (PA + PB);
+                sdst[t] = lds0 + C::kScaleAt + (is_a ? j : C::BM / 16 + j - PA) * 256;
             }
+        }
+    }
+
+    // Load t of the scales of group `grp` (the first of a stage's groups), part
+    // `part` where a group is spread over stages.
+    __device__ __forceinline__ void issue_scale(int grp, int part, int t) const
+    {
+        const int group = grp + sgroup[t];
+        const uint32_t off = (uint32_t)min(srow[t] + part * sstep[t], slast[t]) * sld[t];
+        async4(off + (uint32_t)min(group * 4 + (lane & 3), ns - 1) * 4u, sbase[t],
+               uniform(sdst[t] + (uint32_t)(group % (C::kGroups > 0 ? C::kGroups : 1)) * C::kGroup + part * sstep[t] * 16));
+    }
+
+    // The first scale group, where stages bring the group after theirs.
+    __device__ __forceinline__ void issue_first_scales() const
+    {
+        if constexpr (C::FP4 && !C::kGroupInStage) {
+#pragma unroll
+            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                for (int t = 0; t < LSC; ++t)
+                    issue_scale(0, part, t);
         }
     }
 
@@ -289,9 +336,10 @@ struct TileLoads {
                 async16(voff[t] + (uint32_t)min(slice * 64 + kch[t] * 16, kbytes - 16), is_a ? abase : bbase, dst);
             }
         } else if constexpr (C::FP4) {
-            const int load = (wl * LSC + (t - LA - LB)) % C::kScaleLoads;
-            const int slice = st * C::KB + load / (C::kScaleRows / 64);
-            async4(srow[t - LA - LB] + min(slice, ns - 1) * 4, uniform(base + C::kScaleAt + load * 256));
+            if constexpr (C::kGroupInStage)
+                issue_scale(st * (C::KB / 4), 0, t - LA - LB);
+            else
+                issue_scale(st / kParts + 1, st % kParts, t - LA - LB);
         }
     }
 
@@ -318,8 +366,8 @@ struct TileFrags {
 #pragma unroll
         for (int f = 0; f < (C::CB ? C::FN : 1); ++f)
             brow[f] = ring + C::A::kBytes + C::B::frag_at(wn * C::FN + f, r, g);
-        sarow = ring + C::kScaleAt + (wm * C::FM * 16 + r) * 4 + g;
-        sbrow = ring + C::kScaleAt + (C::BM + wn * C::FN * 16 + r) * 4 + g;
+        sarow = ring + C::kScaleAt + (wm * C::FM * 16 + r) * 16 + g;
+        sbrow = ring + C::kScaleAt + (C::BM + wn * C::FN * 16 + r) * 16 + g;
     }
     // fragment f of slice j of the stage in slot `at` (a byte offset)
     __device__ __forceinline__ u32x4 a(int at, int j, int f) const
@@ -330,8 +378,13 @@ struct TileFrags {
     {
         return C::B::read((C::CB ? brow[C::CB ? f : 0] : brow[0] + f * 1024) + at + j * C::B::kSliceBytes);
     }
-    __device__ __forceinline__ int sa(int at, int j, int f) const { return C::FP4 ? sarow[at + j * C::kScaleRows * 4 + f * 64] : 0; }
-    __device__ __forceinline__ int sb(int at, int j, int f) const { return C::FP4 ? sbrow[at + j * C::kScaleRows * 4 + f * 64] : 0; }
+    // scale byte of fragment f in slice s
+    __device__ __forceinline__ int sa(int s, int f) const { return C::FP4 ? sarow[group_at(s) + f * 256] : 0; }
+    __device__ __forceinline__ int sb(int s, int f) const { return C::FP4 ? sbrow[group_at(s) + f * 256] : 0; }
+    __device__ __forceinline__ static int group_at(int s)
+    {
+        return (s / 4) % (C::kGroups > 0 ? C::kGroups : 1) * C::kGroup + s % 4 * 4;
+    }
 };
 
 template <bool FP4>
@@ -498,6 +551,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
     int sxa[FM], sxb[FM], swf[FN];
 
     // R - 1 stages in flight, the first one landed
+    loads.issue_first_scales();
 #pragma unroll
     for (int st = 0; st < R - 1; ++st)
         loads.issue(st);
@@ -506,12 +560,12 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
         xa[f] = frags.a(0, 0, f);
-        sxa[f] = frags.sa(0, 0, f);
+        sxa[f] = frags.sa(0, f);
     }
 #pragma unroll
     for (int f = 0; f < FN; ++f) {
         wf[f] = frags.b(0, 0, f);
-        swf[f] = frags.sb(0, 0, f);
+        swf[f] = frags.sb(0, f);
     }
 
     // Slice s: where it is a stage's last, make the next stage visible (this
@@ -545,7 +599,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
 #pragma unroll
         for (int f = 0; f < FM; ++f) {
             xn[f] = frags.a(nat, nj, f);
-            sxn[f] = frags.sa(nat, nj, f);
+            sxn[f] = frags.sa(s + 1, f);
         }
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn) {
@@ -553,7 +607,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
             for (int fm = 0; fm < FM; ++fm)
                 tile_mfma<FP4>(xc[fm], wf[fn], sxc[fm], swf[fn], acc[fm][fn]);
             wf[fn] = frags.b(nat, nj, fn);
-            swf[fn] = frags.sb(nat, nj, fn);
+            swf[fn] = frags.sb(s + 1, fn);
             if (stage_end) {
 #pragma unroll
                 for (int t = fn * LS / FN; t < (fn + 1) * LS / FN; ++t)
@@ -590,6 +644,7 @@ __device__ __forceinline__ void stream_body(const TileArgs& p, unsigned char* ri
     constexpr int FM = C::FM, FN = C::FN, KB = C::KB, R = C::R;
     constexpr bool FP4 = C::FP4;
     constexpr int kSliceK = C::kSliceK;
+    static_assert(!FP4 || C::kGroupInStage, "a stage brings its own scales");
     using Loads = TileLoads<C, NL>;
     constexpr int LS = Loads::LS;
     static_assert(R >= 2 && (R - 2) * LS < 64, "ring depth");
@@ -636,12 +691,12 @@ __device__ __forceinline__ void stream_body(const TileArgs& p, unsigned char* ri
 #pragma unroll
             for (int f = 0; f < FM; ++f) {
                 x[j][f] = frags.a(at, j, f);
-                sx[j][f] = frags.sa(at, j, f);
+                sx[j][f] = frags.sa(st * KB + j, f);
             }
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
                 wf[j][f] = frags.b(at, j, f);
-                sw[j][f] = frags.sb(at, j, f);
+                sw[j][f] = frags.sb(st * KB + j, f);
             }
         }
 #pragma unroll
