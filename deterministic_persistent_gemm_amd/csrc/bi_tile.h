@@ -226,7 +226,7 @@ struct TileLoads {
     static_assert(kParts == 1 || (PA * kParts * 16 == C::BM && PB * kParts * 16 == C::BN && PB % 2 == 0), "equal parts");
     static_assert(LA * NL == A::kLoads && LB * NL == B::kLoads, "loads split evenly over the waves");
 
-    uint32_t voff[LA + LB];                                            // row operands: row offset; column: first column's
+    uint32_t voff[LA + LB];                                            // this lane's bytes from the slice's first
     int kch[LA + LB];                                                  // row operands: chunk; column: k row in the slice
     // scales, per load: the operand's first row of the tile, its pitch, the lane's
     // row in part 0, rows to the operand's end and per part, the place in a group
@@ -264,16 +264,16 @@ struct TileLoads {
                 const int key = is_a ? A::col_key(krow) : B::col_key(krow);
                 const int chunk = (((pos >> 1) ^ key) << 1) | (pos & 1);
                 const int first = is_a ? m0 : n0, total = is_a ? p.M : p.N;
-                voff[t] = (uint32_t)(min(first + chunk * 8, total - 8) - first) * 2u;
+                voff[t] = (uint32_t)(min(first + chunk * 8, total - 8) - first) * 2u + (uint32_t)krow * (uint32_t)(is_a ? p.lda : p.ldb);
                 kch[t] = krow;
             } else {
                 const int row = (load * 16) % (is_a ? C::BM : C::BN) + (lane >> 2);
                 kch[t] = (lane & 3) ^ ((row >> 1) & 3);
                 if (is_a) {
-                    voff[t] = (uint32_t)((int64_t)(min(m0 + row, p.M - 1) - m0) * p.lda);
+                    voff[t] = (uint32_t)((int64_t)(min(m0 + row, p.M - 1) - m0) * p.lda) + kch[t] * 16;
                 } else {
                     const int out = min(n0 + deal_out<C::kDeal>(row), p.N - 1);
-                    voff[t] = (uint32_t)((int64_t)(out - n0 + deal_up<C::kDeal>(row) * p.N) * p.ldb);
+                    voff[t] = (uint32_t)((int64_t)(out - n0 + deal_up<C::kDeal>(row) * p.N) * p.ldb) + kch[t] * 16;
                 }
             }
         }
@@ -317,6 +317,9 @@ struct TileLoads {
         }
     }
 
+    // Load t of stage st.  WHOLE: every slice of the stage lies inside k, so
+    // that only the scalar base moves; otherwise k is clamped.
+    template <bool WHOLE>
     __device__ __forceinline__ void issue_one(int st, int t) const
     {
         const uint32_t base = lds0 + (uint32_t)(st % C::R) * C::kStage;
@@ -324,16 +327,24 @@ struct TileLoads {
             const bool is_a = t < LA;
             const int load = is_a ? wl * LA + t : wl * LB + (t - LA);
             const uint32_t dst = uniform(base + (is_a ? 0 : A::kBytes) + load * 1024);
+            const unsigned char* from = is_a ? abase : bbase;
             if (is_a ? C::CA : C::CB) {
                 const int pitch = is_a ? A::kPitch : B::kPitch;
-                const int slice = min(st * C::KB + load / (32 * pitch / 1024), ns - 1);
+                const int slice = st * C::KB + load / (32 * pitch / 1024);
                 const int64_t ld = is_a ? lda : ldb;
-                const int64_t k0 = (int64_t)slice * 32;
-                const int krow = min(kch[t], (int)min((int64_t)31, K - 1 - k0));
-                async16(voff[t] + (uint32_t)krow * (uint32_t)ld, (is_a ? abase : bbase) + k0 * ld, dst);
+                if constexpr (WHOLE) {
+                    async16(voff[t], from + (int64_t)slice * 32 * ld, dst);
+                } else {
+                    const int64_t k0 = (int64_t)min(slice, ns - 1) * 32;
+                    const int past = max(kch[t] - (int)min((int64_t)31, K - 1 - k0), 0);
+                    async16(voff[t] - (uint32_t)past * (uint32_t)ld, from + k0 * ld, dst);
+                }
             } else {
                 const int slice = st * C::KB + load / ((is_a ? C::BM : C::BN) / 16);
-                async16(voff[t] + (uint32_t)min(slice * 64 + kch[t] * 16, kbytes - 16), is_a ? abase : bbase, dst);
+                if constexpr (WHOLE)
+                    async16(voff[t], from + slice * 64, dst);
+                else
+                    async16(voff[t] + (uint32_t)(min(slice * 64, kbytes - 16 - kch[t] * 16)), from, dst);
             }
         } else if constexpr (C::FP4) {
             if constexpr (C::kGroupInStage)
@@ -345,9 +356,15 @@ struct TileLoads {
 
     __device__ __forceinline__ void issue(int st) const
     {
+        if ((int64_t)(st + 1) * C::KB * C::kSliceK <= K) {
 #pragma unroll
-        for (int t = 0; t < LS; ++t)
-            issue_one(st, t);
+            for (int t = 0; t < LS; ++t)
+                issue_one<true>(st, t);
+        } else {
+#pragma unroll
+            for (int t = 0; t < LS; ++t)
+                issue_one<false>(st, t);
+        }
     }
 };
 
@@ -574,7 +591,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
     // of this step refill); then the MFMAs of slice s with the reads of slice
     // s + 1's fragments between them.  Past the last slice, loads and reads
     // touch re-read data that nothing uses.
-    auto step = [&](auto tail, int s, int j, u32x4 (&xc)[FM], int (&sxc)[FM], u32x4 (&xn)[FM], int (&sxn)[FM])
+    auto step = [&](auto whole_loads, auto tail, int s, int j, u32x4 (&xc)[FM], int (&sxc)[FM], u32x4 (&xn)[FM], int (&sxn)[FM])
                     __attribute__((always_inline)) {
         const bool stage_end = j % KB == KB - 1;                   // compile-time after unrolling
         if (stage_end) {
@@ -611,22 +628,27 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
             if (stage_end) {
 #pragma unroll
                 for (int t = fn * LS / FN; t < (fn + 1) * LS / FN; ++t)
-                    loads.issue_one(s / KB + R - 1, t);
+                    loads.template issue_one<decltype(whole_loads)::value>(s / KB + R - 1, t);
             }
         }
     };
-    auto body = [&](auto tail, int s) __attribute__((always_inline)) {
+    auto body = [&](auto whole_loads, auto tail, int s) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < U; j += 2) {
-            step(tail, s + j, j, xa, sxa, xb, sxb);
-            step(tail, s + j + 1, j + 1, xb, sxb, xa, sxa);
+            step(whole_loads, tail, s + j, j, xa, sxa, xb, sxb);
+            step(whole_loads, tail, s + j + 1, j + 1, xb, sxb, xa, sxa);
         }
     };
-    const int whole = (int)(p.K / (kSliceK * U)) * U;               // slices of bodies without a ragged end
-    for (int s = 0; s < whole; s += U)
-        body(std::false_type{}, s);
+    const int inside = (int)(p.K / kSliceK);                        // slices without a ragged end
+    const int whole = inside / U * U;                               // of bodies of such slices
+    const int ahead = (inside / KB - (R - 1)) * KB;                 // bodies up to here load only such slices
+    int s = 0;
+    for (; s + U <= ahead; s += U)
+        body(std::true_type{}, std::false_type{}, s);
+    for (; s < whole; s += U)
+        body(std::false_type{}, std::false_type{}, s);
     if (whole < ns)
-        body(std::true_type{}, whole);
+        body(std::false_type{}, std::true_type{}, whole);
     // the loads still in flight land before the workgroup's LDS is given away
     async_wait<0>();
     tile_store<C>(p, acc, m0, n0, wm, wn, r, g);
