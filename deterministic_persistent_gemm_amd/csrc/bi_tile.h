@@ -120,8 +120,10 @@ template <TileDeal D> __device__ __forceinline__ int deal_up(int p)
 
 // One operand's place in a stage and how its lanes load and read it.
 //   ROWS output rows per tile, KB slices per stage.
-// Row operands: [slice][row][64 bytes], the row's four 16-byte chunks permuted
-// by (row / 2) & 3 (free of bank conflicts for the 16-row fragment reads).
+// Row operands: slices in pairs where a stage has an even number, so that a load
+// asks for whole 128-byte lines: [pair][row][128 bytes], the row's eight 16-byte
+// chunks permuted by (row / 2) & 7; else [row][64 bytes], four chunks permuted by
+// (row / 2) & 3 (both free of bank conflicts for the 16-row fragment reads).
 // Column operands: [slice][32 k][ROWS bf16], 32-byte units of a k row permuted
 // by a key of the k row where four k rows span more than the 256 bytes of all
 // banks, so that the four k rows a transposing read touches fall on different
@@ -131,7 +133,10 @@ struct TileOperand {
     static constexpr int kSliceBytes = ROWS * 64;
     static constexpr int kBytes = KB * kSliceBytes;
     static constexpr int kLoads = kBytes / 1024;        // 1 KiB wave loads per stage
-    static constexpr int kPitch = COL ? ROWS * 2 : 64;
+    static constexpr int kSpan = KB % 2 == 0 ? 2 : 1;   // row operands: slices side by side in a row
+    static constexpr int kPitch = COL ? ROWS * 2 : 64 * kSpan;
+    static constexpr int kChunks = kPitch / 16;
+    static constexpr int kLoadRows = 1024 / kPitch;     // rows (column operands: k rows) per load
     static constexpr int kUnits = ROWS / 16;            // column operands: 32-byte units per k row
     static_assert(ROWS % 16 == 0 && (!COL || kUnits == 1 || kUnits == 2 || kUnits == 4 || kUnits % 8 == 0), "tile rows");
 
@@ -145,12 +150,14 @@ struct TileOperand {
             return 0;
     }
 
+    __device__ __forceinline__ static int row_key(int row) { return (row >> 1) & (kChunks - 1); }
+
     // LDS address of fragment f (16 rows), slice 0, for lane (r, g); column
     // operands: the first of two reads, the second 4 kPitch further.
     __device__ __forceinline__ static int frag_at(int f, int r, int g)
     {
         if constexpr (!COL) {
-            return f * 1024 + r * 64 + ((g ^ ((r >> 1) & 3)) << 4);
+            return (f * 16 + r) * kPitch + ((g ^ row_key(r)) << 4);
         } else {
             const int krow = 8 * g + (r >> 2), c = r & 3;
             if constexpr (PAIR) {
@@ -160,6 +167,16 @@ struct TileOperand {
                 return krow * kPitch + ((f ^ col_key(krow)) << 5) + (c << 3);
             }
         }
+    }
+
+    // The same in slice j (the second slice of a pair lies four chunks further,
+    // under the same permutation).
+    __device__ __forceinline__ static int in_slice(int at, int j)
+    {
+        if constexpr (COL)
+            return at + j * kSliceBytes;
+        else
+            return (j % kSpan == 0 ? at : at ^ 64) + j / kSpan * kSpan * kSliceBytes;
     }
 
     __device__ __forceinline__ static u32x4 read(const unsigned char* p)
@@ -267,8 +284,9 @@ struct TileLoads {
                 voff[t] = (uint32_t)(min(first + chunk * 8, total - 8) - first) * 2u + (uint32_t)krow * (uint32_t)(is_a ? p.lda : p.ldb);
                 kch[t] = krow;
             } else {
-                const int row = (load * 16) % (is_a ? C::BM : C::BN) + (lane >> 2);
-                kch[t] = (lane & 3) ^ ((row >> 1) & 3);
+                const int chunks = is_a ? A::kChunks : B::kChunks;
+                const int row = (load * (is_a ? A::kLoadRows : B::kLoadRows)) % (is_a ? C::BM : C::BN) + lane / chunks;
+                kch[t] = (lane % chunks) ^ (is_a ? A::row_key(row) : B::row_key(row));
                 if (is_a) {
                     voff[t] = (uint32_t)((int64_t)(min(m0 + row, p.M - 1) - m0) * p.lda) + kch[t] * 16;
                 } else {
@@ -340,7 +358,8 @@ struct TileLoads {
                     async16(voff[t] - (uint32_t)past * (uint32_t)ld, from + k0 * ld, dst);
                 }
             } else {
-                const int slice = st * C::KB + load / ((is_a ? C::BM : C::BN) / 16);
+                const int rows = is_a ? C::BM / A::kLoadRows : C::BN / B::kLoadRows;
+                const int slice = st * C::KB + load / rows * A::kSpan;
                 if constexpr (WHOLE)
                     async16(voff[t], from + slice * 64, dst);
                 else
@@ -368,36 +387,38 @@ struct TileLoads {
     }
 };
 
-// A computing wave's fragment and scale addresses.
+// A computing wave's fragment and scale addresses (byte offsets in the ring).
 template <typename C>
 struct TileFrags {
-    const unsigned char* arow[C::CA ? C::FM : 1];
-    const unsigned char* brow[C::CB ? C::FN : 1];
-    const unsigned char *sarow, *sbrow;
+    const unsigned char* ring;
+    int arow[C::CA ? C::FM : 1];
+    int brow[C::CB ? C::FN : 1];
+    int sarow, sbrow;
 
-    __device__ __forceinline__ void init(const unsigned char* ring, int wm, int wn, int r, int g)
+    __device__ __forceinline__ void init(const unsigned char* ring_, int wm, int wn, int r, int g)
     {
+        ring = ring_;
 #pragma unroll
         for (int f = 0; f < (C::CA ? C::FM : 1); ++f)
-            arow[f] = ring + C::A::frag_at(wm * C::FM + f, r, g);
+            arow[f] = C::A::frag_at(wm * C::FM + f, r, g);
 #pragma unroll
         for (int f = 0; f < (C::CB ? C::FN : 1); ++f)
-            brow[f] = ring + C::A::kBytes + C::B::frag_at(wn * C::FN + f, r, g);
-        sarow = ring + C::kScaleAt + (wm * C::FM * 16 + r) * 16 + g;
-        sbrow = ring + C::kScaleAt + (C::BM + wn * C::FN * 16 + r) * 16 + g;
+            brow[f] = C::A::kBytes + C::B::frag_at(wn * C::FN + f, r, g);
+        sarow = C::kScaleAt + (wm * C::FM * 16 + r) * 16 + g;
+        sbrow = C::kScaleAt + (C::BM + wn * C::FN * 16 + r) * 16 + g;
     }
     // fragment f of slice j of the stage in slot `at` (a byte offset)
     __device__ __forceinline__ u32x4 a(int at, int j, int f) const
     {
-        return C::A::read((C::CA ? arow[C::CA ? f : 0] : arow[0] + f * 1024) + at + j * C::A::kSliceBytes);
+        return C::A::read(ring + C::A::in_slice(arow[C::CA ? f : 0], j) + at + (C::CA ? 0 : f * 16 * C::A::kPitch));
     }
     __device__ __forceinline__ u32x4 b(int at, int j, int f) const
     {
-        return C::B::read((C::CB ? brow[C::CB ? f : 0] : brow[0] + f * 1024) + at + j * C::B::kSliceBytes);
+        return C::B::read(ring + C::B::in_slice(brow[C::CB ? f : 0], j) + at + (C::CB ? 0 : f * 16 * C::B::kPitch));
     }
     // scale byte of fragment f in slice s
-    __device__ __forceinline__ int sa(int s, int f) const { return C::FP4 ? sarow[group_at(s) + f * 256] : 0; }
-    __device__ __forceinline__ int sb(int s, int f) const { return C::FP4 ? sbrow[group_at(s) + f * 256] : 0; }
+    __device__ __forceinline__ int sa(int s, int f) const { return C::FP4 ? ring[sarow + group_at(s) + f * 256] : 0; }
+    __device__ __forceinline__ int sb(int s, int f) const { return C::FP4 ? ring[sbrow + group_at(s) + f * 256] : 0; }
     __device__ __forceinline__ static int group_at(int s)
     {
         return (s / 4) % (C::kGroups > 0 ? C::kGroups : 1) * C::kGroup + s % 4 * 4;
@@ -654,6 +675,114 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
     tile_store<C>(p, acc, m0, n0, wm, wn, r, g);
 }
 
+// The largest tile: two groups of four waves, one wave of each per SIMD, take
+// turns.  While one group's MFMAs of a slice run back to back, the other reads
+// its fragments of the next from LDS and issues its loads; then they swap, one
+// barrier per turn.  The matrix unit always has one wave that needs nothing but
+// registers, and neither the LDS latency nor the issue of loads is in its way.
+//
+// A wave's turn in memory at slice s: read the fragments of s; issue its loads
+// of stage s + R - 1 into the slot of stage s - 1, whose last readers (the
+// other group) finished before the barrier this turn began with; wait for
+// its own reads and for its loads of stage s + 1, which the next barriers make
+// visible to everyone before that stage's first reader.
+template <typename C>
+__device__ __forceinline__ void turns_body(const TileArgs& p, unsigned char* ring, int block)
+{
+    constexpr int FM = C::FM, FN = C::FN, R = C::R;
+    constexpr bool FP4 = C::FP4;
+    constexpr int kSliceK = C::kSliceK;
+    using Loads = TileLoads<C, C::NW>;
+    constexpr int LS = Loads::LS;
+    constexpr int kEvery = FM * FN / LS;                           // MFMAs between loads
+    static_assert(C::KB == 1 && C::NW == 8 && R >= 3 && (R - 1) * LS < 64, "eight waves, one slice per stage");
+
+    const int lane = threadIdx.x & 63, w = (int)uniform(threadIdx.x >> 6);
+    const int wm = w / C::WN, wn = w % C::WN;
+    const int r = lane & 15, g = lane >> 4;
+    int tn;
+    const int tm = tile_of(block, p.tiles_m, p.tiles_n, tn);
+    const int m0 = tm * C::BM, n0 = tn * C::kOutN;
+    const int ns = (int)((p.K + kSliceK - 1) / kSliceK);
+    Loads loads;
+    loads.init(p, ring, w, lane, m0, n0);
+    TileFrags<C> frags;
+    frags.init(ring, wm, wn, r, g);
+
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+            acc[fm][fn] = f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 xf[FM], wf[FN];
+    int sx[FM], sw[FN];
+
+    loads.issue_first_scales();
+#pragma unroll
+    for (int st = 0; st < R - 1; ++st)
+        loads.issue(st);
+    async_wait<(R - 2) * LS>();
+    wg_barrier();
+    if (w >= 4)
+        wg_barrier();
+
+    auto slice = [&](auto whole_loads, auto tail, int s) __attribute__((always_inline)) {
+        const int at = (s % R) * C::kStage;
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+            wf[f] = frags.b(at, 0, f);
+            sw[f] = frags.sb(s, f);
+        }
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+            xf[f] = frags.a(at, 0, f);
+            sx[f] = frags.sa(s, f);
+        }
+        async_wait<(R - 3) * LS>();
+        wg_barrier_reads_done();
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (decltype(tail)::value) {
+            const int64_t valid = p.K - (int64_t)s * kSliceK - g * (kSliceK / 4);
+#pragma unroll
+            for (int f = 0; f < FM; ++f) {
+                xf[f] = mask_k<FP4>(xf[f], valid);
+                sx[f] = valid > 0 ? sx[f] : 127;
+            }
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                wf[f] = mask_k<FP4>(wf[f], valid);
+                sw[f] = valid > 0 ? sw[f] : 127;
+            }
+        }
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 0; i < FN * FM; ++i) {
+            tile_mfma<FP4>(xf[i % FM], wf[i / FM], sx[i % FM], sw[i / FM], acc[i % FM][i / FM]);
+            if (i % kEvery == kEvery / 2 && i / kEvery < LS) {
+                __builtin_amdgcn_sched_barrier(0);
+                loads.template issue_one<decltype(whole_loads)::value>(s + R - 1, i / kEvery);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        wg_barrier();
+    };
+    const int inside = (int)(p.K / kSliceK);
+    int s = 0;
+    for (; s + R <= inside; ++s)
+        slice(std::true_type{}, std::false_type{}, s);
+    for (; s < inside; ++s)
+        slice(std::false_type{}, std::false_type{}, s);
+    if (s < ns)
+        slice(std::false_type{}, std::true_type{}, s);
+    if (w < 4)
+        wg_barrier();
+    async_wait<0>();
+    tile_store<C>(p, acc, m0, n0, wm, wn, r, g);
+}
+
 // Small tiles, where a wave has too few MFMAs per slice to hide the latency of
 // its LDS reads and loads behind them: NL waves only load, up to R - 1 stages
 // ahead, and the computing waves read all fragments of a stage at once.  One
@@ -756,6 +885,13 @@ __global__ __launch_bounds__(C::NW * 64) void k_tile(TileArgs p)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char ring[C::kRing];
     tile_body<C>(p, ring, (int)blockIdx.x);
+}
+
+template <typename C>
+__global__ __launch_bounds__(C::NW * 64) void k_turns(TileArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char ring[C::kRing];
+    turns_body<C>(p, ring, (int)blockIdx.x);
 }
 
 template <typename C, int NL>
