@@ -25,6 +25,8 @@ static hipError_t gated_tile(TileArgs a, hipStream_t s)
     const unsigned grid = (unsigned)(a.tiles_m * a.tiles_n);
     if constexpr (NL > 0)
         k_stream<C, NL><<<grid, (C::NW + NL) * 64, 0, s>>>(a);
+    else if constexpr (R == 2)
+        k_turns<C><<<grid, C::NW * 64, 0, s>>>(a);
     else
         k_tile<C><<<grid, C::NW * 64, 0, s>>>(a);
     return hipGetLastError();
@@ -32,9 +34,8 @@ static hipError_t gated_tile(TileArgs a, hipStream_t s)
 
 // bm x (weight rows / 2); the costs are explained in bi_tile_rule.h
 static const TileShape kGatedShapes[] = {
-    {16, 8, 0.69f, 0.041f, 1.00f},   {16, 16, 0.32f, 0.066f, 1.00f}, {32, 16, 0.61f, 0.075f, 1.10f},
-    {64, 16, 1.10f, 0.090f, 0.f},    {64, 32, 0.53f, 0.159f, 1.10f}, {128, 64, 1.20f, 0.289f, 0.f},
-    {128, 128, 0.82f, 0.547f, 0.f},  {256, 128, 4.28f, 0.651f, 0.f},
+    {16, 8, 0.67f, 0.037f, 1.10f}, {16, 16, 0.29f, 0.063f, 1.10f}, {32, 16, 0.64f, 0.072f, 1.10f}, {64, 16, 0.90f, 0.088f, 0.f},
+    {128, 32, 0.65f, 0.204f, 0.f}, {128, 64, 0.72f, 0.277f, 0.f},  {256, 128, 1.87f, 0.688f, 0.f},
 };
 
 hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int64_t ldw, int gate, uint16_t* y,
@@ -54,15 +55,14 @@ hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int
     a.M = (int)M;
     a.N = (int)I;
     a.K = H;
-    switch (pick_tile(kGatedShapes, 8, M, I, (H + 31) / 32, device_cu_count())) {
+    switch (pick_tile(kGatedShapes, 7, M, I, (H + 31) / 32, device_cu_count())) {
     case 0: return gated_tile<16, 16, 1, 1, 8, 4, 4>(a, s);
     case 1: return gated_tile<16, 32, 1, 1, 4, 4, 4>(a, s);
     case 2: return gated_tile<32, 32, 2, 1, 4, 4, 4>(a, s);
     case 3: return gated_tile<64, 32, 4, 1, 4, 4, 4>(a, s);
-    case 4: return gated_tile<64, 64, 4, 1, 2, 4, 0>(a, s);
+    case 4: return gated_tile<128, 64, 4, 1, 2, 4, 0>(a, s);
     case 5: return gated_tile<128, 128, 4, 2, 2, 4, 0>(a, s);
-    case 6: return gated_tile<128, 256, 2, 4, 1, 4, 0>(a, s);
-    default: return gated_tile<256, 256, 2, 4, 1, 4, 0>(a, s);
+    default: return gated_tile<256, 256, 4, 2, 2, 2, 0>(a, s);
     }
 }
 

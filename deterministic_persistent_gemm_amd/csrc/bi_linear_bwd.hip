@@ -72,11 +72,15 @@ template <bool CA> struct BwdShape<1, CA> {
     static constexpr int NL = 0;
 };
 template <bool CA> struct BwdShape<2, CA> {
-    using C = TileCfg<128, 128, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
+    using C = TileCfg<128, 64, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
     static constexpr int NL = 0;
 };
 template <bool CA> struct BwdShape<3, CA> {
-    using C = TileCfg<256, 256, 2, 4, 1, 4, CA, true, false, kEpiLinear>;
+    using C = TileCfg<128, 128, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
+    static constexpr int NL = 0;
+};
+template <bool CA> struct BwdShape<4, CA> {
+    using C = TileCfg<256, 256, CA ? 4 : 2, CA ? 2 : 4, 2, 2, CA, true, false, kEpiLinear>;
     static constexpr int NL = 0;
 };
 
@@ -86,6 +90,8 @@ __device__ __forceinline__ void bwd_body(const TileArgs& p, unsigned char* ring,
     static_assert((S::C::NW + S::NL) * 64 == kBwdThreads, "one workgroup size");
     if constexpr (S::NL > 0)
         stream_body<typename S::C, S::NL>(p, ring, block);
+    else if constexpr (S::C::R == 2)
+        turns_body<typename S::C>(p, ring, block);
     else
         tile_body<typename S::C>(p, ring, block);
 }
@@ -109,13 +115,14 @@ __global__ __launch_bounds__(kBwdThreads) void k_bwd(TileArgs dx, TileArgs dw, S
 }
 
 // the costs are explained in bi_tile_rule.h
-static const TileShape kDxShapes[] = {{32, 32, 0.70f, 0.084f, 0.83f}, {64, 64, 0.73f, 0.134f, 1.10f},
-                                      {128, 128, 1.40f, 0.255f, 0.f}, {256, 256, 2.82f, 0.655f, 0.f}};
-static const TileShape kDwShapes[] = {{0, 0, 0.f, 0.f, 0.f},          {64, 64, 1.42f, 0.119f, 1.10f},
-                                      {128, 128, 2.91f, 0.263f, 0.f}, {256, 256, 6.41f, 0.658f, 0.f}};
+static const TileShape kDxShapes[] = {{32, 32, 0.74f, 0.086f, 0.76f}, {64, 64, 0.79f, 0.128f, 1.05f}, {128, 64, 0.99f, 0.171f, 0.f},
+                                      {128, 128, 1.37f, 0.238f, 0.f}, {256, 256, 2.47f, 0.649f, 0.f}};
+static const TileShape kDwShapes[] = {{0, 0, 0.f, 0.f, 0.f},          {64, 64, 1.51f, 0.110f, 1.01f}, {128, 64, 2.25f, 0.161f, 0.f},
+                                      {128, 128, 2.98f, 0.235f, 0.f}, {256, 256, 7.12f, 0.635f, 0.f}};
+constexpr int kNumDxShapes = 5, kNumDwShapes = 4;       // dw: shapes 1 .. 4
 
 // The shape pairs that are built; a product alone may use its side of any.
-static const int kBwdPairs[][2] = {{0, 1}, {1, 1}, {2, 1}, {0, 2}, {1, 2}, {2, 2}, {2, 3}, {3, 3}};
+static const int kBwdPairs[][2] = {{0, 1}, {1, 1}, {2, 1}, {0, 2}, {2, 2}, {0, 3}, {2, 3}, {3, 3}, {3, 4}, {4, 4}};
 constexpr int kNumBwdPairs = (int)(sizeof(kBwdPairs) / sizeof(kBwdPairs[0]));
 
 // Both products in one launch: the longer of one tile's time and of all tiles'
@@ -151,10 +158,12 @@ static hipError_t bwd_launch_pair(int pair, const TileArgs& dx, const TileArgs& 
     case 1: return bwd_launch<1, 1>(dx, dw, sum, s);
     case 2: return bwd_launch<2, 1>(dx, dw, sum, s);
     case 3: return bwd_launch<0, 2>(dx, dw, sum, s);
-    case 4: return bwd_launch<1, 2>(dx, dw, sum, s);
-    case 5: return bwd_launch<2, 2>(dx, dw, sum, s);
+    case 4: return bwd_launch<2, 2>(dx, dw, sum, s);
+    case 5: return bwd_launch<0, 3>(dx, dw, sum, s);
     case 6: return bwd_launch<2, 3>(dx, dw, sum, s);
-    default: return bwd_launch<3, 3>(dx, dw, sum, s);
+    case 7: return bwd_launch<3, 3>(dx, dw, sum, s);
+    case 8: return bwd_launch<3, 4>(dx, dw, sum, s);
+    default: return bwd_launch<4, 4>(dx, dw, sum, s);
     }
 }
 
@@ -184,8 +193,8 @@ hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x
     b.K = M;
     const int cus = device_cu_count();
     // each product's own best shape, and the best pair for one launch
-    const int bx = pick_tile(kDxShapes, 4, M, K, (N + 31) / 32, cus);
-    const int bw = 1 + pick_tile(kDwShapes + 1, 3, N, K, (M + 31) / 32, cus);
+    const int bx = pick_tile(kDxShapes, kNumDxShapes, M, K, (N + 31) / 32, cus);
+    const int bw = 1 + pick_tile(kDwShapes + 1, kNumDwShapes, N, K, (M + 31) / 32, cus);
     auto pair_with = [](int side, int shape) {
         for (int i = 0; i < kNumBwdPairs; ++i)
             if (kBwdPairs[i][side] == shape)

@@ -144,6 +144,8 @@ static hipError_t mx_tile(TileArgs a, hipStream_t s)
     const unsigned grid = (unsigned)(a.tiles_m * a.tiles_n);
     if constexpr (NL > 0)
         k_stream<C, NL><<<grid, (C::NW + NL) * 64, 0, s>>>(a);
+    else if constexpr (R == 2)
+        k_turns<C><<<grid, C::NW * 64, 0, s>>>(a);
     else
         k_tile<C><<<grid, C::NW * 64, 0, s>>>(a);
     return hipGetLastError();
@@ -151,8 +153,8 @@ static hipError_t mx_tile(TileArgs a, hipStream_t s)
 
 // the costs are explained in bi_tile_rule.h; a slice is 128 k
 static const TileShape kMxShapes[] = {
-    {16, 16, 0.75f, 0.031f, 1.10f},   {16, 32, 0.60f, 0.043f, 1.06f}, {64, 64, 1.10f, 0.173f, 1.10f},
-    {128, 128, 1.84f, 0.451f, 1.10f}, {256, 128, 1.97f, 0.647f, 0.f}, {256, 256, 3.32f, 0.890f, 0.f},
+    {16, 16, 0.87f, 0.032f, 1.10f}, {16, 32, 0.78f, 0.051f, 0.92f},   {32, 32, 0.97f, 0.068f, 1.10f},
+    {64, 64, 1.26f, 0.162f, 1.00f}, {128, 128, 2.25f, 0.393f, 1.10f}, {256, 256, 5.08f, 0.961f, 0.f},
 };
 
 hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, int64_t ldxs, const uint8_t* wq,
@@ -178,10 +180,10 @@ hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, i
     switch (pick_tile(kMxShapes, 6, M, N, (K + 127) / 128, device_cu_count())) {
     case 0: return mx_tile<16, 16, 1, 1, 8, 4, 4>(a, s);
     case 1: return mx_tile<16, 32, 1, 1, 4, 4, 4>(a, s);
-    case 2: return mx_tile<64, 64, 4, 1, 2, 4, 0>(a, s);
-    case 3: return mx_tile<128, 128, 2, 2, 1, 4, 0>(a, s);
-    case 4: return mx_tile<256, 128, 4, 2, 1, 4, 0>(a, s);
-    default: return mx_tile<256, 256, 2, 4, 1, 4, 0>(a, s);
+    case 2: return mx_tile<32, 32, 2, 1, 4, 4, 4>(a, s);
+    case 3: return mx_tile<64, 64, 4, 1, 2, 4, 0>(a, s);
+    case 4: return mx_tile<128, 128, 2, 2, 1, 4, 0>(a, s);
+    default: return mx_tile<256, 256, 2, 4, 2, 2, 0>(a, s);
     }
 }
 

@@ -57,11 +57,15 @@ constexpr float kGeluC2 = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
 // act(g) = g * gate_sigma(g).  exp overflows to +inf for very negative g,
-// where the quotient is 0 as it should be.
+// where the reciprocal is 0 as it should be.  The hardware exponential and
+// reciprocal (one ulp each, the argument's rounding times its magnitude of at
+// most 88 on top: below 2^-15 relative, far under the bf16 rounding of what is
+// stored) in place of expf and a full division, which made the epilogue of a
+// 256 x 256 tile 9 us long.
 __device__ __forceinline__ float gate_sigma(float g, int gate)
 {
     const float z = gate == kGateSilu ? g : kGeluC2 * (g + kGeluB * g * g * g);
-    return 1.0f / (1.0f + expf(-z));
+    return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
 }
 
 // two fp32 -> packed bf16, round to nearest even
@@ -120,20 +124,20 @@ template <TileDeal D> __device__ __forceinline__ int deal_up(int p)
 
 // One operand's place in a stage and how its lanes load and read it.
 //   ROWS output rows per tile, KB slices per stage.
-// Row operands: slices in pairs where a stage has an even number, so that a load
-// asks for whole 128-byte lines: [pair][row][128 bytes], the row's eight 16-byte
+// Row operands: WIDE, slices in pairs, so that a load asks for whole 128-byte
+// lines: [pair][row][128 bytes], the row's eight 16-byte
 // chunks permuted by (row / 2) & 7; else [row][64 bytes], four chunks permuted by
 // (row / 2) & 3 (both free of bank conflicts for the 16-row fragment reads).
 // Column operands: [slice][32 k][ROWS bf16], 32-byte units of a k row permuted
 // by a key of the k row where four k rows span more than the 256 bytes of all
 // banks, so that the four k rows a transposing read touches fall on different
 // banks.  PAIR: the weight side's columns are dealt as kPairs.
-template <int ROWS, int KB, bool COL, bool PAIR>
+template <int ROWS, int KB, bool COL, bool PAIR, bool WIDE>
 struct TileOperand {
     static constexpr int kSliceBytes = ROWS * 64;
     static constexpr int kBytes = KB * kSliceBytes;
     static constexpr int kLoads = kBytes / 1024;        // 1 KiB wave loads per stage
-    static constexpr int kSpan = KB % 2 == 0 ? 2 : 1;   // row operands: slices side by side in a row
+    static constexpr int kSpan = WIDE ? 2 : 1;          // row operands: slices side by side in a row
     static constexpr int kPitch = COL ? ROWS * 2 : 64 * kSpan;
     static constexpr int kChunks = kPitch / 16;
     static constexpr int kLoadRows = 1024 / kPitch;     // rows (column operands: k rows) per load
@@ -202,8 +206,12 @@ struct TileCfg {
     static constexpr int NW = WM * WN;
     static constexpr int FM = BM / (WM * 16), FN = BN / (WN * 16);
     static constexpr TileDeal kDeal = tile_deal<FN, EPI>();
-    using A = TileOperand<BM, KB, CA, false>;
-    using B = TileOperand<BN, KB, CB, kDeal == kPairs || kDeal == kGated4>;
+    // 128 bytes of a row at a time: 17 to 32 percent off a 128 x 128 bf16 tile's
+    // time, 9 off a 256 x 256 one's.  Short 4-bit streams (16 rows) take 5 percent
+    // longer with it and keep 64.
+    static constexpr bool kWide = KB % 2 == 0 && !(FP4 && BM < 64);
+    using A = TileOperand<BM, KB, CA, false, kWide>;
+    using B = TileOperand<BN, KB, CB, kDeal == kPairs || kDeal == kGated4, kWide>;
     static constexpr int kOutN = EPI == kEpiGated ? BN / 2 : BN;       // output columns per tile
     static constexpr int kSliceK = FP4 ? 128 : 32;
     static constexpr int kStage = A::kBytes + B::kBytes;
@@ -677,109 +685,149 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
 
 // The largest tile: two groups of four waves, one wave of each per SIMD, take
 // turns.  While one group's MFMAs of a slice run back to back, the other reads
-// its fragments of the next from LDS and issues its loads; then they swap, one
-// barrier per turn.  The matrix unit always has one wave that needs nothing but
-// registers, and neither the LDS latency nor the issue of loads is in its way.
+// its fragments of its next slice from LDS; then they swap, one barrier per
+// turn.  The matrix unit always has one wave that needs nothing but registers.
 //
-// A wave's turn in memory at slice s: read the fragments of s; issue its loads
-// of stage s + R - 1 into the slot of stage s - 1, whose last readers (the
-// other group) finished before the barrier this turn began with; wait for
-// its own reads and for its loads of stage s + 1, which the next barriers make
-// visible to everyone before that stage's first reader.
+// Stages of two slices in a ring of two.  Turns of stage S (group 0 computes on
+// odd turns, group 1 one turn later):
+//   4S      group 0 reads slice 2S         group 1 computes 2S - 1
+//   4S + 1  group 0 computes 2S            group 1 reads 2S
+//   4S + 2  group 0 reads 2S + 1           group 1 computes 2S
+//   4S + 3  group 0 computes 2S + 1        group 1 reads 2S + 1
+// The slot of stage S + 1 had its last reader in turn 4S - 1, so its loads are
+// issued in turns 4S and 4S + 1 and waited for at the end of turn 4S + 3.
+template <typename C, bool SECOND>
+__device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ring, const TileLoads<C, C::NW>& loads, int ns,
+                                            int wm, int wn, int r, int g, f32x4 (&acc)[C::FM][C::FN])
+{
+    constexpr int FM = C::FM, FN = C::FN;
+    constexpr bool FP4 = C::FP4;
+    constexpr int kSliceK = C::kSliceK;
+    constexpr int LS = TileLoads<C, C::NW>::LS, kFirst = LS / 2;   // group 0's loads: before and between its MFMAs
+    TileFrags<C> frags;
+    frags.init(ring, wm, wn, r, g);
+    u32x4 xf[FM], wf[FN];
+    int sx[FM], sw[FN];
+
+    auto read = [&](int st, int j) __attribute__((always_inline)) {
+        const int at = (st % 2) * C::kStage;
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+            wf[f] = frags.b(at, j, f);
+            sw[f] = frags.sb(2 * st + j, f);
+        }
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+            xf[f] = frags.a(at, j, f);
+            sx[f] = frags.sa(2 * st + j, f);
+        }
+    };
+    auto mask = [&](int s) __attribute__((always_inline)) {
+        const int64_t valid = p.K - (int64_t)s * kSliceK - g * (kSliceK / 4);
+#pragma unroll
+        for (int f = 0; f < FM; ++f) {
+            xf[f] = mask_k<FP4>(xf[f], valid);
+            sx[f] = valid > 0 ? sx[f] : 127;
+        }
+#pragma unroll
+        for (int f = 0; f < FN; ++f) {
+            wf[f] = mask_k<FP4>(wf[f], valid);
+            sw[f] = valid > 0 ? sw[f] : 127;
+        }
+    };
+    // the MFMAs of a slice with loads t0 .. t1-1 of stage st spread among them
+    auto compute = [&](auto whole_loads, int st, auto t0, auto t1) __attribute__((always_inline)) {
+        constexpr int kLoads = decltype(t1)::value - decltype(t0)::value;
+        constexpr int kEvery = kLoads > 0 ? FM * FN / kLoads : FM * FN + 1;
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 0; i < FN * FM; ++i) {
+            tile_mfma<FP4>(xf[i % FM], wf[i / FM], sx[i % FM], sw[i / FM], acc[i % FM][i / FM]);
+            if (i % kEvery == kEvery / 2 && i / kEvery < kLoads) {
+                __builtin_amdgcn_sched_barrier(0);
+                loads.template issue_one<decltype(whole_loads)::value>(st, decltype(t0)::value + i / kEvery);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    using None = std::integral_constant<int, 0>;
+    auto stage = [&](auto whole_loads, auto tail, int st) __attribute__((always_inline)) {
+        read(st, 0);
+        if constexpr (!SECOND) {
+#pragma unroll
+            for (int t = 0; t < kFirst; ++t)
+                loads.template issue_one<decltype(whole_loads)::value>(st + 1, t);
+        }
+        wg_barrier_reads_done();
+        if constexpr (decltype(tail)::value)
+            mask(2 * st);
+        if constexpr (!SECOND)
+            compute(whole_loads, st + 1, std::integral_constant<int, kFirst>{}, std::integral_constant<int, LS>{});
+        else
+            compute(whole_loads, st + 2, None{}, None{});
+        wg_barrier();
+        read(st, 1);
+        if constexpr (SECOND)
+            async_wait<0>();
+        wg_barrier_reads_done();
+        if constexpr (decltype(tail)::value)
+            mask(2 * st + 1);
+        if constexpr (!SECOND) {
+            compute(whole_loads, st + 1, None{}, None{});
+            async_wait<0>();
+        } else {
+            compute(whole_loads, st + 2, None{}, std::integral_constant<int, LS>{});
+        }
+        wg_barrier();
+    };
+    if constexpr (SECOND) {
+        loads.issue(1);
+        wg_barrier();
+    }
+    const int inside = (int)(p.K / (2 * kSliceK)), nst = (ns + 1) / 2;
+    constexpr int kAhead = SECOND ? 2 : 1;
+    int st = 0;
+    for (; st + kAhead < inside; ++st)
+        stage(std::true_type{}, std::false_type{}, st);
+    for (; st < inside; ++st)
+        stage(std::false_type{}, std::false_type{}, st);
+    if (st < nst)
+        stage(std::false_type{}, std::true_type{}, st);
+    if constexpr (!SECOND)
+        wg_barrier();
+    async_wait<0>();
+}
+
 template <typename C>
 __device__ __forceinline__ void turns_body(const TileArgs& p, unsigned char* ring, int block)
 {
-    constexpr int FM = C::FM, FN = C::FN, R = C::R;
-    constexpr bool FP4 = C::FP4;
-    constexpr int kSliceK = C::kSliceK;
-    using Loads = TileLoads<C, C::NW>;
-    constexpr int LS = Loads::LS;
-    constexpr int kEvery = FM * FN / LS;                           // MFMAs between loads
-    static_assert(C::KB == 1 && C::NW == 8 && R >= 3 && (R - 1) * LS < 64, "eight waves, one slice per stage");
-
+    static_assert(C::KB == 2 && C::R == 2 && C::NW == 8, "eight waves, two stages of two slices");
     const int lane = threadIdx.x & 63, w = (int)uniform(threadIdx.x >> 6);
     const int wm = w / C::WN, wn = w % C::WN;
     const int r = lane & 15, g = lane >> 4;
     int tn;
     const int tm = tile_of(block, p.tiles_m, p.tiles_n, tn);
     const int m0 = tm * C::BM, n0 = tn * C::kOutN;
-    const int ns = (int)((p.K + kSliceK - 1) / kSliceK);
-    Loads loads;
+    const int ns = (int)((p.K + C::kSliceK - 1) / C::kSliceK);
+    TileLoads<C, C::NW> loads;
     loads.init(p, ring, w, lane, m0, n0);
-    TileFrags<C> frags;
-    frags.init(ring, wm, wn, r, g);
-
-    f32x4 acc[FM][FN];
+    f32x4 acc[C::FM][C::FN];
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm)
+    for (int fm = 0; fm < C::FM; ++fm)
 #pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
+        for (int fn = 0; fn < C::FN; ++fn)
             acc[fm][fn] = f32x4{0.f, 0.f, 0.f, 0.f};
-    u32x4 xf[FM], wf[FN];
-    int sx[FM], sw[FN];
-
     loads.issue_first_scales();
-#pragma unroll
-    for (int st = 0; st < R - 1; ++st)
-        loads.issue(st);
-    async_wait<(R - 2) * LS>();
-    wg_barrier();
-    if (w >= 4)
-        wg_barrier();
-
-    auto slice = [&](auto whole_loads, auto tail, int s) __attribute__((always_inline)) {
-        const int at = (s % R) * C::kStage;
-#pragma unroll
-        for (int f = 0; f < FN; ++f) {
-            wf[f] = frags.b(at, 0, f);
-            sw[f] = frags.sb(s, f);
-        }
-#pragma unroll
-        for (int f = 0; f < FM; ++f) {
-            xf[f] = frags.a(at, 0, f);
-            sx[f] = frags.sa(s, f);
-        }
-        async_wait<(R - 3) * LS>();
-        wg_barrier_reads_done();
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (decltype(tail)::value) {
-            const int64_t valid = p.K - (int64_t)s * kSliceK - g * (kSliceK / 4);
-#pragma unroll
-            for (int f = 0; f < FM; ++f) {
-                xf[f] = mask_k<FP4>(xf[f], valid);
-                sx[f] = valid > 0 ? sx[f] : 127;
-            }
-#pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                wf[f] = mask_k<FP4>(wf[f], valid);
-                sw[f] = valid > 0 ? sw[f] : 127;
-            }
-        }
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int i = 0; i < FN * FM; ++i) {
-            tile_mfma<FP4>(xf[i % FM], wf[i / FM], sx[i % FM], sw[i / FM], acc[i % FM][i / FM]);
-            if (i % kEvery == kEvery / 2 && i / kEvery < LS) {
-                __builtin_amdgcn_sched_barrier(0);
-                loads.template issue_one<decltype(whole_loads)::value>(s + R - 1, i / kEvery);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-        __builtin_amdgcn_s_setprio(0);
-        __builtin_amdgcn_sched_barrier(0);
-        wg_barrier();
-    };
-    const int inside = (int)(p.K / kSliceK);
-    int s = 0;
-    for (; s + R <= inside; ++s)
-        slice(std::true_type{}, std::false_type{}, s);
-    for (; s < inside; ++s)
-        slice(std::false_type{}, std::false_type{}, s);
-    if (s < ns)
-        slice(std::false_type{}, std::true_type{}, s);
-    if (w < 4)
-        wg_barrier();
+    loads.issue(0);
     async_wait<0>();
+    wg_barrier();
+    if (w < 4)
+        turns_group<C, false>(p, ring, loads, ns, wm, wn, r, g, acc);
+    else
+        turns_group<C, true>(p, ring, loads, ns, wm, wn, r, g, acc);
     tile_store<C>(p, acc, m0, n0, wm, wn, r, g);
 }
 

@@ -5,14 +5,14 @@
 //
 //   launch + rounds * (per_tile + slices * per_slice)
 //
-// with the two costs of one workgroup fitted to timings of 26 to 33 problems
-// drawn over M 1 .. 4096, widths 128 .. 12288 and k 256 .. 4096 on an MI355X
-// (fit within 5 to 20 percent).  rounds: workgroups per compute unit, counted
-// whole where a shape's LDS ring leaves room for one workgroup per compute unit
-// and as a fraction where several share it.  Over those problems the shapes
-// chosen this way come within 1 to 5 percent of the fastest of 18 shapes on
-// average; always taking 64 x 64 costs 1.33 to 1.48 times as much, always
-// 256 x 256 2.4 to 3.7 times.
+// with the two costs of one workgroup fitted to timings of 32 to 34 problems per
+// product, drawn over M 1 .. 4096, widths 128 .. 12288 and k 256 .. 4096, on an
+// MI355X (fit within 5 to 20 percent).  rounds: workgroups per compute unit,
+// counted whole where a shape's LDS ring leaves room for one workgroup per
+// compute unit and as a fraction where several share it.  Over those problems
+// the shapes chosen this way come within 1 to 4 percent of the fastest of 6 to 14
+// shapes on average; always taking 64 x 64 costs 1.24 to 1.38 times the fastest,
+// always 128 x 128 1.40 to 1.70, always 256 x 256 2.0 to 3.4.
 #pragma once
 
 #include <stdint.h>
