@@ -21,12 +21,15 @@ TINY = 1e-30
 
 
 def act(g, gate):
-    """act(g) and act'(g); gate 0: silu, 1: gelu (tanh)."""
+    """act(g) and act'(g); gate 0: silu, 1: gelu (tanh).  The tanh form's
+    (1 + tanh z) / 2 is computed as the equal 1 / (1 + exp(-2 z)): in binary64
+    1 + tanh z is off by 2^-53, which for z = -16 is a hundredth of its value."""
     if gate == 0:
         s = torch.sigmoid(g)
         return g * s, s + g * s * (1 - s)
-    t = torch.tanh(C * (g + 0.044715 * g ** 3))
-    return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * C * (1 + 3 * 0.044715 * g * g)
+    z2 = 2 * C * (g + 0.044715 * g ** 3)
+    s, up = torch.sigmoid(z2), torch.sigmoid(-z2)
+    return g * s, s + g * s * up * 2 * C * (1 + 3 * 0.044715 * g * g)
 
 
 def mm(a, b):

@@ -97,6 +97,39 @@ def test_gated_large(M, H, I):
     same(y1, y[M - 1:], "the last row alone")
 
 
+# sizes that reach each tile shape of the gated layer with ragged rows, columns
+# and k (one slice, an odd number of slices, more slices than a ring holds)
+GATED_SHAPES = [(1, 480, 16), (1, 32, 16), (20, 96, 3536), (34, 96, 3024), (17, 32, 4560), (129, 544, 4560), (17, 32, 8496),
+                (300, 352, 8496), (387, 32, 8752), (387, 96, 8752), (515, 672, 8752), (1030, 2080, 2064)]
+
+
+@pytest.mark.parametrize("M,H,I", GATED_SHAPES)
+def test_gated_every_tile_shape(M, H, I):
+    """Integer operands: h is exact before its rounding, in every tile shape."""
+    banner(f"gated shapes M={M} H={H} I={I}")
+    g = gen(M + H + I)
+    x, w = ints(g, (M, H), -3, 3), ints(g, (2 * I, H), -2, 2)
+    xp, _ = padded(x)
+    wp, _ = padded(w)
+    y, h = bi.bi_gated_linear_bf16(xp, wp.t(), 1, save_h=True)
+    wh = ref.mm(x, w.t().contiguous())
+    same(h + 0.0, wh.to(BF) + 0.0, "h")
+    wy = ref.act(wh[:, :I], 1)[0] * wh[:, I:]
+    within(y, wy, (ref.HALF_BF16 + ref.ACT_REL) * (1 + ref.HALF_BF16) * wy.abs() + ref.TINY, "y")
+
+
+@pytest.mark.parametrize("N,K", [(4096, 1024), (1536, 768), (8192, 352)])
+def test_projections_equal_the_linear_layer(N, K):
+    """h is what bi_linear_bf16 computes, bit for bit, where that key's recipe is
+    fully chained: both thread one accumulator through k in the same order."""
+    assert bi.bi_describe_recipe(bi.BI_BF16, N, K).block_k == K
+    g = gen(N + K)
+    x, w = randn(g, (600, K)), randn(g, (N, K), 0.05)
+    for M in (1, 40, 600):
+        banner(f"h against bi_linear_bf16 M={M} N={N} K={K}")
+        same(bi.bi_gated_linear_bf16(x[:M], w.t(), save_h=True)[1], bi.bi_linear_bf16(x[:M], w.t()), f"M={M}")
+
+
 def test_gated_extreme_projections():
     """act over the whole range: projections of the diagonal layer are the inputs."""
     H = I = 64
@@ -140,7 +173,13 @@ BWD = [(1, 32, 32), (1, 544, 64), (7, 96, 64), (31, 64, 96), (32, 128, 128), (33
        (300, 2048, 768), (333, 1040, 544), (1000, 256, 512), (2050, 144, 96)]           # M, N, K
 
 
-@pytest.mark.parametrize("M,N,K", BWD)
+# sizes that reach every pair of tile shapes in one launch, and two launches
+BWD_SHAPES = [(1, 272, 2784), (1, 272, 4192), (1, 80, 4128), (89, 80, 4128), (1, 272, 3424), (1, 400, 4192), (133, 496, 4128),
+              (226, 1712, 4000), (1304, 1552, 3360), (135, 4016, 2016), (41, 3728, 3552), (235, 4048, 3872), (1442, 432, 2400),
+              (2569, 144, 4128), (807, 816, 4256), (996, 3184, 3616), (4100, 48, 8160)]
+
+
+@pytest.mark.parametrize("M,N,K", BWD + BWD_SHAPES)
 def test_linear_bwd_exact_on_integers(M, N, K):
     """Small integers: every product and sum is exact, so is the fp32 result."""
     banner(f"linear_bwd ints M={M} N={N} K={K}")
@@ -151,6 +190,10 @@ def test_linear_bwd_exact_on_integers(M, N, K):
     same(dw + 0.0, ref.mm(dy.t().contiguous(), x).float(), "dw")
     same(db + 0.0, dy.double().sum(0).float(), "db")
     same(bi.bi_linear_bf16_bwd(dy, x, w.t())[1] + 0.0, ref.mm(dy.t().contiguous(), x).to(BF), "dw bf16")
+    # each gradient alone takes its own shape
+    same(bi.bi_linear_bf16_bwd(dy, None, w.t(), need_dw=False, need_db=False)[0], dx, "dx alone")
+    same(bi.bi_linear_bf16_bwd(dy, x, None, need_dx=False, need_db=False, dw_dtype=torch.float32)[1], dw, "dw alone")
+    same(bi.bi_linear_bf16_bwd(dy, None, None, need_dx=False, need_dw=False)[2], db, "db alone")
 
 
 @pytest.mark.parametrize("M,N,K", BWD)
@@ -309,7 +352,8 @@ def test_quantize_ties_specials_and_range():
 
 
 MX = [(1, 16, 32), (1, 48, 96), (5, 32, 128), (16, 256, 544), (17, 272, 1024), (64, 64, 160), (65, 528, 416), (130, 1040, 256),
-      (300, 768, 2048), (1, 4096, 4096), (1030, 512, 672)]    # M, N, K
+      (300, 768, 2048), (1, 4096, 4096), (1030, 512, 672), (17, 6160, 32), (33, 5392, 32), (258, 6288, 32), (258, 6288, 416),
+      (915, 8720, 32), (915, 8720, 160), (700, 8720, 672), (900, 8720, 1184), (1030, 2064, 1184)]    # M, N, K
 
 
 @pytest.mark.parametrize("M,N,K", MX)
