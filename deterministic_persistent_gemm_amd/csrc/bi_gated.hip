@@ -55,7 +55,7 @@ hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int
     a.M = (int)M;
     a.N = (int)I;
     a.K = H;
-    switch (pick_tile(kGatedShapes, 7, M, I, (H + 31) / 32, device_cu_count())) {
+    switch (pick_tile(kGatedShapes, 7, M, I, (H + 31) / 32, false, device_cu_count())) {
     case 0: return gated_tile<16, 16, 1, 1, 8, 4, 4>(a, s);
     case 1: return gated_tile<16, 32, 1, 1, 4, 4, 4>(a, s);
     case 2: return gated_tile<32, 32, 2, 1, 4, 4, 4>(a, s);

@@ -127,9 +127,9 @@ constexpr int kNumBwdPairs = (int)(sizeof(kBwdPairs) / sizeof(kBwdPairs[0]));
 
 // Both products in one launch: the longer of one tile's time and of all tiles'
 // times spread over the compute units, the last round half empty.
-static float pair_time(const TileShape& a, const TileShape& b, int64_t M, int64_t N, int64_t K, int cus)
+static float pair_time(const TileShape& a, const TileShape& b, int64_t M, int64_t N, int64_t K, bool dw_f32, int cus)
 {
-    const float ta = tile_once(a, (N + 31) / 32), tb = tile_once(b, (M + 31) / 32);
+    const float ta = tile_once(a, (N + 31) / 32, false), tb = tile_once(b, (M + 31) / 32, dw_f32);
     const int64_t na = tile_count(a, M, K), nb = tile_count(b, N, K);
     const float longest = ta > tb ? ta : tb, shortest = ta > tb ? tb : ta;
     const float all = ((float)na * ta + (float)nb * tb) / (float)cus + (na + nb > cus ? 0.5f * shortest : 0.f);
@@ -193,8 +193,8 @@ hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x
     b.K = M;
     const int cus = device_cu_count();
     // each product's own best shape, and the best pair for one launch
-    const int bx = pick_tile(kDxShapes, kNumDxShapes, M, K, (N + 31) / 32, cus);
-    const int bw = 1 + pick_tile(kDwShapes + 1, kNumDwShapes, N, K, (M + 31) / 32, cus);
+    const int bx = pick_tile(kDxShapes, kNumDxShapes, M, K, (N + 31) / 32, false, cus);
+    const int bw = 1 + pick_tile(kDwShapes + 1, kNumDwShapes, N, K, (M + 31) / 32, !dw_bf16, cus);
     auto pair_with = [](int side, int shape) {
         for (int i = 0; i < kNumBwdPairs; ++i)
             if (kBwdPairs[i][side] == shape)
@@ -208,14 +208,14 @@ hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x
     int best = 0;
     float best_time = 0.f;
     for (int i = 0; i < kNumBwdPairs; ++i) {
-        const float t = pair_time(kDxShapes[kBwdPairs[i][0]], kDwShapes[kBwdPairs[i][1]], M, N, K, cus);
+        const float t = pair_time(kDxShapes[kBwdPairs[i][0]], kDwShapes[kBwdPairs[i][1]], M, N, K, !dw_bf16, cus);
         if (i == 0 || t < best_time) {
             best = i;
             best_time = t;
         }
     }
-    const float apart = tile_time(kDxShapes[bx], M, K, (N + 31) / 32, cus) +
-                        tile_time(kDwShapes[bw], N, K, (M + 31) / 32, cus);
+    const float apart = tile_time(kDxShapes[bx], M, K, (N + 31) / 32, false, cus) +
+                        tile_time(kDwShapes[bw], N, K, (M + 31) / 32, !dw_bf16, cus);
     if (best_time <= apart)
         return bwd_launch_pair(best, a, b, sum, s);
     TileArgs none{};

@@ -177,7 +177,7 @@ hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, i
     a.M = (int)M;
     a.N = (int)N;
     a.K = K;
-    switch (pick_tile(kMxShapes, 6, M, N, (K + 127) / 128, device_cu_count())) {
+    switch (pick_tile(kMxShapes, 6, M, N, (K + 127) / 128, !y_bf16, device_cu_count())) {
     case 0: return mx_tile<16, 16, 1, 1, 8, 4, 4>(a, s);
     case 1: return mx_tile<16, 32, 1, 1, 4, 4, 4>(a, s);
     case 2: return mx_tile<32, 32, 2, 1, 4, 4, 4>(a, s);

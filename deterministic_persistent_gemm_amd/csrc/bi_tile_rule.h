@@ -33,9 +33,15 @@ inline int64_t tile_count(const TileShape& t, int64_t M, int64_t N)
     return ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
 }
 
-inline float tile_once(const TileShape& t, int64_t slices) { return t.per_tile + t.per_slice * (float)slices; }
+// One workgroup's time.  The costs were taken with bf16 outputs; fp32 outputs
+// write two bytes more each, at the 19 KB a microsecond that a compute unit has
+// of the HBM's write rate when all of them write.
+inline float tile_once(const TileShape& t, int64_t slices, bool f32_out)
+{
+    return t.per_tile + t.per_slice * (float)slices + (f32_out ? (float)(t.bm * t.bn) * 2.f / 18750.f : 0.f);
+}
 
-inline float tile_time(const TileShape& t, int64_t M, int64_t N, int64_t slices, int cus)
+inline float tile_time(const TileShape& t, int64_t M, int64_t N, int64_t slices, bool f32_out, int cus)
 {
     const int64_t tiles = tile_count(t, M, N);
     float rounds;
@@ -45,16 +51,16 @@ inline float tile_time(const TileShape& t, int64_t M, int64_t N, int64_t slices,
     } else {
         rounds = (float)((tiles + cus - 1) / cus);
     }
-    return kTileLaunch + rounds * tile_once(t, slices);
+    return kTileLaunch + rounds * tile_once(t, slices, f32_out);
 }
 
 // The index of the fastest of n shapes.
-inline int pick_tile(const TileShape* t, int n, int64_t M, int64_t N, int64_t slices, int cus)
+inline int pick_tile(const TileShape* t, int n, int64_t M, int64_t N, int64_t slices, bool f32_out, int cus)
 {
     int best = 0;
-    float best_time = tile_time(t[0], M, N, slices, cus);
+    float best_time = tile_time(t[0], M, N, slices, f32_out, cus);
     for (int i = 1; i < n; ++i) {
-        const float time = tile_time(t[i], M, N, slices, cus);
+        const float time = tile_time(t[i], M, N, slices, f32_out, cus);
         if (time < best_time) {
             best = i;
             best_time = time;
