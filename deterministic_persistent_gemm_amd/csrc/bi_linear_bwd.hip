@@ -60,8 +60,8 @@ __device__ __forceinline__ void colsum_body(const SumArgs& p, unsigned char* lds
 }
 
 // Tile shapes of the two products, all on 512 threads so that any two can share
-// a launch: S32 streams (short batches: few tiles and a long sum over N),
-// the others load and compute in every wave.
+// a launch.  dx's two smallest stream (short batches: few tiles and a long sum
+// over N); the others load and compute in every wave.
 template <int SHAPE, bool CA> struct BwdShape;
 template <bool CA> struct BwdShape<0, CA> {
     using C = TileCfg<32, 32, 2, 2, 4, 4, CA, true, false, kEpiLinear>;
@@ -70,6 +70,10 @@ template <bool CA> struct BwdShape<0, CA> {
 template <bool CA> struct BwdShape<1, CA> {
     using C = TileCfg<64, 64, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
     static constexpr int NL = 0;
+};
+template <> struct BwdShape<1, false> {
+    using C = TileCfg<32, 64, 2, 2, 4, 3, false, true, false, kEpiLinear>;
+    static constexpr int NL = 4;
 };
 template <bool CA> struct BwdShape<2, CA> {
     using C = TileCfg<128, 64, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
@@ -115,24 +119,30 @@ __global__ __launch_bounds__(kBwdThreads) void k_bwd(TileArgs dx, TileArgs dw, S
 }
 
 // the costs are explained in bi_tile_rule.h
-static const TileShape kDxShapes[] = {{32, 32, 0.74f, 0.086f, 0.76f}, {64, 64, 0.79f, 0.128f, 1.05f}, {128, 64, 0.99f, 0.171f, 0.f},
-                                      {128, 128, 1.37f, 0.238f, 0.f}, {256, 256, 2.47f, 0.649f, 0.f}};
-static const TileShape kDwShapes[] = {{0, 0, 0.f, 0.f, 0.f},          {64, 64, 1.51f, 0.110f, 1.01f}, {128, 64, 2.25f, 0.161f, 0.f},
-                                      {128, 128, 2.98f, 0.235f, 0.f}, {256, 256, 7.12f, 0.635f, 0.f}};
+static const TileShape kDxShapes[] = {{32, 32, 1.17f, 0.054f, 1.13f}, {32, 64, 1.71f, 0.075f, 1.05f}, {128, 64, 1.38f, 0.154f, 0.f},
+                                      {128, 128, 1.61f, 0.231f, 0.f}, {256, 256, 3.29f, 0.554f, 0.f}};
+static const TileShape kDwShapes[] = {{0, 0, 0.f, 0.f, 0.f},          {64, 64, 1.61f, 0.113f, 1.04f}, {128, 64, 2.34f, 0.165f, 0.f},
+                                      {128, 128, 2.88f, 0.235f, 0.f}, {256, 256, 6.22f, 0.590f, 0.f}};
 constexpr int kNumDxShapes = 5, kNumDwShapes = 4;       // dw: shapes 1 .. 4
 
 // The shape pairs that are built; a product alone may use its side of any.
 static const int kBwdPairs[][2] = {{0, 1}, {1, 1}, {2, 1}, {0, 2}, {2, 2}, {0, 3}, {2, 3}, {3, 3}, {3, 4}, {4, 4}};
 constexpr int kNumBwdPairs = (int)(sizeof(kBwdPairs) / sizeof(kBwdPairs[0]));
 
-// Both products in one launch: the longer of one tile's time and of all tiles'
-// times spread over the compute units, the last round half empty.
+// Both products in one launch: all tiles' times spread over the compute units
+// plus a part of a last round, but at least the longest tile's time, with some of
+// the other's where there is more than one round.  Over 54 problems the launches
+// chosen this way took 1.02 times the fastest of the ten pairs and of all shapes
+// in two launches.
 static float pair_time(const TileShape& a, const TileShape& b, int64_t M, int64_t N, int64_t K, bool dw_f32, int cus)
 {
     const float ta = tile_once(a, (N + 31) / 32, false), tb = tile_once(b, (M + 31) / 32, dw_f32);
     const int64_t na = tile_count(a, M, K), nb = tile_count(b, N, K);
-    const float longest = ta > tb ? ta : tb, shortest = ta > tb ? tb : ta;
-    const float all = ((float)na * ta + (float)nb * tb) / (float)cus + (na + nb > cus ? 0.5f * shortest : 0.f);
+    const bool shared = a.share > 0.f && b.share > 0.f, rounds = na + nb > cus;
+    const float most = ta > tb ? ta : tb, least = ta > tb ? tb : ta;
+    const float all = ((float)na * ta * (shared ? a.share : 1.f) + (float)nb * tb * (shared ? b.share : 1.f)) / (float)cus +
+                      (rounds ? (shared ? 0.25f : 0.75f) * least : 0.f);
+    const float longest = most + (rounds ? 0.2f * least : 0.f);
     return kTileLaunch + (all > longest ? all : longest);
 }
 
