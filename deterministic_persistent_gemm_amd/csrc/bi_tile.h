@@ -234,11 +234,12 @@ struct TileCfg {
 };
 
 // The loads of a stage, spread over NL loading waves (this one is `wl`).
-// Row operands: a load covers 16 tile rows of one slice; lane i lands at row
-// i / 4, chunk position i % 4 and fetches the chunk that belongs there.  Rows
-// past the end read the last row, chunks past the end of k the last chunk:
-// neither reaches a stored result.  Column operands: a load covers 1024 / pitch
-// k rows of one slice, columns past the end read the last eight.
+// Row operands: a load covers 16 tile rows of one slice, or 8 rows of a pair;
+// the lanes land on a row's chunk positions in turn, each fetching the chunk
+// that belongs there.  Rows past the end read the last row, chunks past the end
+// of k the last chunk: neither reaches a stored result.  Column operands: a load
+// covers 1024 / pitch k rows of one slice, columns past the end read the last
+// eight.  Each load is a scalar base and 32 bits of byte offset per lane.
 template <typename C, int NL>
 struct TileLoads {
     using A = typename C::A;
@@ -560,11 +561,14 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, const f32x4 (&acc)
     }
 }
 
-// Large tiles: every wave loads and computes.  A wave holds the fragments of
-// two slices: while the MFMAs of slice s issue, the fragments of slice s + 1
+// Middle tiles (64 x 64 to 128 x 128): every wave loads and computes.  A wave
+// holds the fragments of two slices: while the MFMAs of slice s issue, the fragments of slice s + 1
 // are read -- the A fragments first, then one B fragment after each group of
 // MFMAs that used slice s's fragment at that position, which is then free --
-// and the loads of a later stage are issued between the groups.
+// and the loads of a later stage are issued between the groups.  128 x 128 runs
+// at 0.96 to 1.0 PFLOP/s in bf16 (4096 x 12288 x 4096), bound by the LDS bytes
+// per MFMA (8 KiB of fragments for every 8 MFMAs of a wave); it is taken where
+// larger tiles would leave compute units idle.
 template <typename C>
 __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring, int block)
 {
@@ -627,6 +631,9 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
                     __attribute__((always_inline)) {
         const bool stage_end = j % KB == KB - 1;                   // compile-time after unrolling
         if (stage_end) {
+            // no MFMA of the slices before may sink past the barrier: having
+            // issued, they are the proof that their fragments have been read
+            __builtin_amdgcn_sched_barrier(0);
             async_wait<(R - 3) * LS>();
             wg_barrier();
         }
@@ -699,6 +706,14 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
 //   4S + 3  group 0 computes 2S + 1        group 1 reads 2S + 1
 // The slot of stage S + 1 had its last reader in turn 4S - 1, so its loads are
 // issued in turns 4S and 4S + 1 and waited for at the end of turn 4S + 3.
+//
+// Measured on the gated layer at M = 4096, H = 4096, I = 4096 (two rounds of 256
+// tiles): 195 us, 1.41 PFLOP/s, where every wave loading and computing at once
+// (as in the middle tiles) took 222.  Timing copies with parts removed: MFMAs
+// and barriers alone 135 us (2.03 PFLOP/s, the rate of MFMAs on registers only),
+// with the output 153, with the LDS reads 167, with loads that all hit one line
+// 180, that hit L2 195 (before the shorter epilogue), with the real ones 207.
+// What is left is the delivery of 64 KiB per stage and compute unit.
 template <typename C, bool SECOND>
 __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ring, const TileLoads<C, C::NW>& loads, int ns,
                                             int wm, int wn, int r, int g, f32x4 (&acc)[C::FM][C::FN])
@@ -839,7 +854,10 @@ __device__ __forceinline__ void turns_body(const TileArgs& p, unsigned char* rin
 // ahead, and the computing waves read all fragments of a stage at once.  One
 // barrier per stage hands it over: a loading wave waits for its own loads of
 // the stage first, a computing wave for its reads of the stage before, whose
-// slot is refilled next.
+// slot is refilled next.  One token through H = 2048, I = 768 (6.3 MB): 3.4 us
+// against 8.1 with 64 x 64 tiles whose waves all load and compute; 16 tokens
+// through H = 4096, I = 12288 (203 MB): 36 to 39 us, 5.2 to 5.6 TB/s, the rate of a
+// large copy.
 template <typename C, int NL>
 __device__ __forceinline__ void stream_body(const TileArgs& p, unsigned char* ring, int block)
 {
