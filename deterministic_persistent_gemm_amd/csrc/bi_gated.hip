@@ -70,6 +70,8 @@ hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int
 // h in, both halves of dh out.  With s = sigma(z(g)), act = g s:
 //   silu  act' = s + g s (1 - s)
 //   gelu  act' = s + g s (1 - s) z'(g),  z = c (g + b g^3)
+// g^2 in z' is held below 1e30: s or 1 - s is exactly 0 long before, and zero
+// times an overflowed z' would be NaN.
 // dh is rounded to bf16 once: it is the matrix instructions' operand in both
 // products that follow.
 __global__ __launch_bounds__(256) void k_gate_bwd(const uint16_t* __restrict__ dy, int64_t lddy,
@@ -94,7 +96,7 @@ __global__ __launch_bounds__(256) void k_gate_bwd(const uint16_t* __restrict__ d
                 const float gg = __uint_as_float(q ? gv[j] & 0xffff0000u : gv[j] << 16);
                 const float uu = __uint_as_float(q ? uv[j] & 0xffff0000u : uv[j] << 16);
                 const float sg = gate_sigma(gg, gate);
-                const float dz = gate == kGateSilu ? 1.0f : kGeluC2 * (1.0f + 3.0f * kGeluB * gg * gg);
+                const float dz = gate == kGateSilu ? 1.0f : kGeluC2 * (1.0f + 3.0f * kGeluB * fminf(gg * gg, 1e30f));
                 const float act = gg * sg;
                 rg[q] = d * uu * (sg + act * (1.0f - sg) * dz);
                 ru[q] = d * act;

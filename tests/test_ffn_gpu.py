@@ -260,6 +260,19 @@ def test_gated_bwd_elementwise_part(gate):
     within(dx, want, ref.HALF_BF16 * want.abs() + 2 * ref.ACT_REL * slack + 1e-30, "dh")
 
 
+@pytest.mark.parametrize("gate", GATES)
+def test_gated_bwd_large_projections(gate):
+    """Projections whose square or cube passes fp32's range: act' is 1 or 0 there."""
+    I = 64
+    vals = [1e10, 1e13, 1e19, 2e19, 1e20, 1e25, 1e30, 3e38]
+    g = torch.tensor(vals + [-v for v in vals], dtype=BF, device="cuda").repeat(2, I // 16)
+    h = torch.cat((g, torch.full_like(g, 2.0)), dim=1)
+    dy = torch.ones_like(g)
+    eye = torch.eye(2 * I, dtype=BF, device="cuda")
+    dx, _ = bi.bi_gated_linear_bf16_bwd(dy, None, eye.t(), h, gate, need_dw=False)
+    same(dx, ref.gate_bwd(dy, h, gate).to(BF) + 0.0, "dh")
+
+
 def test_gated_gradients_against_differences():
     """The layer's own forward pass, differenced: sum(y * dy) along random
     directions of x and w, in steps large enough for bf16 y."""
