@@ -468,9 +468,10 @@ def bi_gated_linear_bf16(x: torch.Tensor, w13t: torch.Tensor, gate: int = BI_GAT
     ldx = _rows(x, torch.bfloat16, M, H, dev, name, "x")
     ldw = _rows(w13t, torch.bfloat16, 2 * I, H, dev, name, "w13t.t()", transposed=True)
     if out is None:
-        out = x.new_empty((M, I))
-    ldy = _rows(out, torch.bfloat16, M, I, dev, name, "out")
-    h = x.new_empty((M, 2 * I)) if save_h else None
+        out, ldy = x.new_empty(M, I), I
+    else:
+        ldy = _rows(out, torch.bfloat16, M, I, dev, name, "out")
+    h = x.new_empty(M, 2 * I) if save_h else None
     _call(_lib.bi_gated_linear_bf16, name, dev, x.data_ptr(), ldx, w13t.data_ptr(), ldw, int(gate), out.data_ptr(), ldy,
           _dp(h), 2 * I, M, I, H)
     return (out, h) if save_h else out
@@ -483,8 +484,8 @@ def bi_gated_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, w13t: tor
     kept: (dx [M, H] bf16 or None, dw [2I, H] of dw_dtype or None).  x is read
     for dw only and w13t for dx only; the other may be None."""
     name = "bi_gated_linear_bf16_bwd"
-    if dy.dim() != 2 or (need_dx and w13t is None) or (need_dw and x is None):
-        raise ValueError(f"{name}: dy is [M, I]; dx needs w13t and dw needs x")
+    if dy.dim() != 2 or (need_dx and (w13t is None or w13t.dim() != 2)) or (need_dw and (x is None or x.dim() != 2)):
+        raise ValueError(f"{name}: dy is [M, I]; dx needs w13t [H, 2I] and dw needs x [M, H]")
     M, I = dy.shape
     H = w13t.shape[0] if need_dx else x.shape[1] if need_dw else 32
     code = _dtype_code(dw_dtype, name, "dw_dtype")
@@ -496,10 +497,10 @@ def bi_gated_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, w13t: tor
     ldx = ldw = 0
     if need_dx:
         ldw = _rows(w13t, torch.bfloat16, 2 * I, H, dev, name, "w13t.t()", transposed=True)
-        dx = dy.new_empty((M, H))
+        dx = dy.new_empty(M, H)
     if need_dw:
         ldx = _rows(x, torch.bfloat16, M, H, dev, name, "x")
-        dw = dy.new_empty((2 * I, H), dtype=dw_dtype)
+        dw = dy.new_empty(2 * I, H, dtype=dw_dtype)
     ws = _scratch(_lib.bi_gated_linear_bwd_workspace_size(M, I), dy.device, ws, name)
     _call(_lib.bi_gated_linear_bf16_bwd, name, dev, dy.data_ptr(), lddy, _dp(x) if need_dw else None, ldx,
           _dp(w13t) if need_dx else None, ldw, h.data_ptr(), ldh, int(gate), _dp(dx), H, _dp(dw), code, H, M, I, H,
@@ -513,8 +514,8 @@ def bi_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tenso
     [N] fp32), each None if not wanted.  dy [M, N] bf16; x [M, K] is read for
     dw only and wt = weight.t() [K, N] for dx only; either may be None."""
     name = "bi_linear_bf16_bwd"
-    if dy.dim() != 2 or (need_dx and wt is None) or (need_dw and x is None):
-        raise ValueError(f"{name}: dy is [M, N]; dx needs wt and dw needs x")
+    if dy.dim() != 2 or (need_dx and (wt is None or wt.dim() != 2)) or (need_dw and (x is None or x.dim() != 2)):
+        raise ValueError(f"{name}: dy is [M, N]; dx needs wt [K, N] and dw needs x [M, K]")
     M, N = dy.shape
     K = wt.shape[0] if need_dx else x.shape[1] if need_dw else 32
     code = _dtype_code(dw_dtype, name, "dw_dtype")
@@ -525,12 +526,12 @@ def bi_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tenso
     ldx = ldw = 0
     if need_dx:
         ldw = _rows(wt, torch.bfloat16, N, K, dev, name, "wt.t()", transposed=True)
-        dx = dy.new_empty((M, K))
+        dx = dy.new_empty(M, K)
     if need_dw:
         ldx = _rows(x, torch.bfloat16, M, K, dev, name, "x")
-        dw = dy.new_empty((N, K), dtype=dw_dtype)
+        dw = dy.new_empty(N, K, dtype=dw_dtype)
     if need_db:
-        db = dy.new_empty((N,), dtype=torch.float32)
+        db = dy.new_empty(N, dtype=torch.float32)
     _call(_lib.bi_linear_bf16_bwd, name, dev, dy.data_ptr(), lddy, _dp(x) if need_dw else None, ldx,
           _dp(wt) if need_dx else None, ldw, _dp(dx), K, _dp(dw), code, K, _dp(db), M, N, K)
     return dx, dw, db
@@ -565,9 +566,9 @@ def bi_quantize_mxfp4(x: torch.Tensor):
     _sizes(name, 16, K)
     dev = x.get_device()
     ldx = _rows(x, x.dtype, rows, K, dev, name, "x")
-    q = x.new_empty((rows, K // 2), dtype=torch.uint8)
+    q = x.new_empty(rows, K // 2, dtype=torch.uint8)
     lds = (K // 32 + 3) // 4 * 4
-    s = x.new_empty((rows, lds), dtype=torch.uint8)
+    s = x.new_empty(rows, lds, dtype=torch.uint8)
     _call(_lib.bi_quantize_mxfp4, name, dev, x.data_ptr(), code, ldx, q.data_ptr(), K // 2, s.data_ptr(), lds, rows, K)
     return q, s if lds == K // 32 else s[:, :K // 32]
 
@@ -578,7 +579,7 @@ def bi_dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, out_dtype: torch.dtype
     code = _dtype_code(out_dtype, name, "out_dtype")
     dev = q.get_device()
     ldq, lds, rows, K = _mx_operand(q, s, dev, name, "q", "s")
-    y = q.new_empty((rows, K), dtype=out_dtype)
+    y = q.new_empty(rows, K, dtype=out_dtype)
     _call(_lib.bi_dequantize_mxfp4, name, dev, q.data_ptr(), ldq, s.data_ptr(), lds, y.data_ptr(), code, K, rows, K)
     return y
 
@@ -599,8 +600,9 @@ def bi_linear_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: to
     _sizes(name, N, K)
     _check_bias(bias, N, xq.device, name)
     if out is None:
-        out = xq.new_empty((M, N), dtype=out_dtype)
-    ldy = _rows(out, out.dtype, M, N, dev, name, "out")
+        out, ldy = xq.new_empty(M, N, dtype=out_dtype), N
+    else:
+        ldy = _rows(out, out.dtype, M, N, dev, name, "out")
     _call(_lib.bi_linear_mxfp4, name, dev, xq.data_ptr(), ldxq, xs.data_ptr(), ldxs, wq.data_ptr(), ldwq, ws.data_ptr(),
           ldws, _dp(bias), out.data_ptr(), code, ldy, M, N, K)
     return out

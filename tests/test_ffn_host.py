@@ -110,6 +110,10 @@ def test_binding_refuses_before_it_enqueues():
                  lambda: bi.bi_linear_bf16_bwd(x, None, w.t()),                     # dw without x
                  lambda: bi.bi_linear_bf16_bwd(x, x, None),                         # dx without w
                  lambda: bi.bi_gated_linear_bf16_bwd(x, None, w.t(), x),
+                 lambda: bi.bi_gated_linear_bf16_bwd(x, cpu(64), None, x, need_dx=False),       # 1-D x
+                 lambda: bi.bi_gated_linear_bf16_bwd(x, x, cpu(64), x),                         # 1-D w
+                 lambda: bi.bi_linear_bf16_bwd(x, cpu(64), None, need_dx=False),
+                 lambda: bi.bi_linear_bf16_bwd(x, x, cpu(64)),
                  lambda: bi.bi_quantize_mxfp4(cpu(4, 48)),
                  lambda: bi.bi_quantize_mxfp4(cpu(64)),
                  lambda: bi.bi_linear_mxfp4(cpu(4, 32, dtype=torch.uint8), cpu(4, 2, dtype=torch.uint8),
