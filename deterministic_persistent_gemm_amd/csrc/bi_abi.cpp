@@ -87,6 +87,13 @@ bool mx_ok(const void* q, int64_t ldq, const void* sc, int64_t lds, int64_t K)
            lds >= K / 32 && lds % 4 == 0 && ldq < (int64_t(1) << 40) && lds < (int64_t(1) << 40);
 }
 
+// The status of a feed-forward launch: a grid too large for one is a size that
+// is not served.
+bi_status_t launch_status(hipError_t e)
+{
+    return e == hipSuccess ? BI_OK : e == hipErrorInvalidConfiguration ? BI_EUNSUPPORTED : BI_EHIP;
+}
+
 size_t dh_bytes(int64_t M, int64_t I) { return (size_t)M * 2 * (size_t)I * 2; }
 
 // The gradients of a linear layer; the operands have been checked.  An empty
@@ -96,10 +103,8 @@ bi_status_t run_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, 
                            int64_t M, int64_t N, int64_t K, hipStream_t stream)
 {
     if (M > 0)
-        return launch_linear_bwd(dy, lddy, x, ldx, w, ldw, dx, lddx, dw, dw_dtype == BI_BF16, lddw, db, M, N, K,
-                                 stream) == hipSuccess
-                   ? BI_OK
-                   : BI_EHIP;
+        return launch_status(launch_linear_bwd(dy, lddy, x, ldx, w, ldw, dx, lddx, dw, dw_dtype == BI_BF16, lddw, db, M,
+                                               N, K, stream));
     const int64_t es = dtype_bytes(dw_dtype);
     if (dw && launch_zero_rows(dw, lddw * es, N, K * es, stream) != hipSuccess)
         return BI_EHIP;
@@ -384,7 +389,7 @@ bi_status_t bi_gated_linear_bf16(const uint16_t* x, int64_t ldx, const uint16_t*
         return BI_EINVAL;
     if (!gated_fits(ldx, ldw, M, I, H))
         return BI_EUNSUPPORTED;
-    return launch_gated(x, ldx, w13, ldw, gate, y, ldy, h, ldh, M, I, H, stream) == hipSuccess ? BI_OK : BI_EHIP;
+    return launch_status(launch_gated(x, ldx, w13, ldw, gate, y, ldy, h, ldh, M, I, H, stream));
 }
 
 size_t bi_gated_linear_bwd_workspace_size(int64_t M, int64_t I)
@@ -489,10 +494,8 @@ bi_status_t bi_linear_mxfp4(const uint8_t* xq, int64_t ldxq, const uint8_t* xs, 
         return BI_EINVAL;
     if (!mx_fits(ldxq, ldxs, ldwq, ldws, M, N, K))
         return BI_EUNSUPPORTED;
-    return launch_mx_linear(xq, ldxq, xs, ldxs, wq, ldwq, wsc, ldws, bias, y, y_dtype == BI_BF16, ldy, M, N, K,
-                            stream) == hipSuccess
-               ? BI_OK
-               : BI_EHIP;
+    return launch_status(launch_mx_linear(xq, ldxq, xs, ldxs, wq, ldwq, wsc, ldws, bias, y, y_dtype == BI_BF16, ldy, M, N,
+                                          K, stream));
 }
 
 }  // extern "C"

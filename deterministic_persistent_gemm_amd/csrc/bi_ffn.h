@@ -10,6 +10,10 @@
 
 namespace bi {
 
+// A launch may hold fewer than 2^32 threads, and a workgroup here has at most
+// 512: launchers return hipErrorInvalidConfiguration for more workgroups.
+inline bool grid_ok(int64_t groups) { return groups < (int64_t(1) << 23); }
+
 // bi_gated.hip
 bool gated_fits(int64_t ldx, int64_t ldw, int64_t M, int64_t I, int64_t H);
 hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int64_t ldw, int gate, uint16_t* y,

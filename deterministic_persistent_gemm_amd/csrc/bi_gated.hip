@@ -22,7 +22,10 @@ static hipError_t gated_tile(TileArgs a, hipStream_t s)
     using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, false, kEpiGated>;
     a.tiles_m = (a.M + BM - 1) / BM;
     a.tiles_n = (a.N + C::kOutN - 1) / C::kOutN;
-    const unsigned grid = (unsigned)(a.tiles_m * a.tiles_n);
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    if (!grid_ok(tiles))
+        return hipErrorInvalidConfiguration;
+    const unsigned grid = (unsigned)tiles;
     if constexpr (NL > 0)
         k_stream<C, NL><<<grid, (C::NW + NL) * 64, 0, s>>>(a);
     else if constexpr (R == 2)

@@ -157,6 +157,8 @@ static hipError_t bwd_launch(TileArgs dx, TileArgs dw, const SumArgs& sum, hipSt
     dw.tiles_n = (dw.N + CW::BN - 1) / CW::BN;
     const int ndx = dx.y ? dx.tiles_m * dx.tiles_n : 0, ndw = dw.y ? dw.tiles_m * dw.tiles_n : 0;
     const int nsum = sum.db ? (sum.N + kSumCols - 1) / kSumCols : 0;
+    if (!grid_ok((int64_t)ndx + ndw + nsum))
+        return hipErrorInvalidConfiguration;
     k_bwd<DX, DW><<<(unsigned)(ndx + ndw + nsum), kBwdThreads, 0, s>>>(dx, dw, sum, ndx, ndw);
     return hipGetLastError();
 }

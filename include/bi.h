@@ -235,7 +235,9 @@ bi_status_t bi_moe_grouped_gemm_ex(const uint16_t* x,
  * All pointers are device pointers on the stream's device, 16-byte aligned
  * unless stated; row pitches are in elements (bytes for codes and scales);
  * outputs must not overlap inputs.  Rows past M and columns past the widths
- * given are neither read nor written.
+ * given are neither read nor written.  BI_EUNSUPPORTED: widths that are not the
+ * multiples stated, pitches at which one tile's rows span 4 GiB, outputs of more
+ * than 2^23 tiles.
  * ------------------------------------------------------------------------- */
 
 typedef enum {

@@ -75,6 +75,14 @@ def test_unsupported_sizes(fn, kw):
     assert fn(**kw) == bi.BI_EUNSUPPORTED
 
 
+def test_more_workgroups_than_a_launch_holds():
+    """2^32 threads and more are refused, not handed to the runtime."""
+    M = 1 << 30
+    assert gated(M=M, I=16, H=32) == bi.BI_EUNSUPPORTED
+    assert mx(M=M, N=16, K=32, ldy=16) == bi.BI_EUNSUPPORTED
+    assert linear_bwd(M=M, N=16, K=32, dw=None, db=None) == bi.BI_EUNSUPPORTED
+
+
 def test_nothing_to_do():
     assert gated(M=0, x=None, y=None) == bi.BI_OK
     assert gated_bwd(dx=None, dw=None) == bi.BI_OK
