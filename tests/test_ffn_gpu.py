@@ -429,6 +429,64 @@ def test_mxfp4_nan_blocks():
 # -------------------------------------------------- streams, graphs, a whole layer
 
 
+def far(t, pitch):
+    """t's values in rows `pitch` elements apart; the buffer passes 4 GiB."""
+    assert t.shape[0] * pitch * t.element_size() > 1 << 32
+    buf = torch.empty((t.shape[0], pitch), dtype=t.dtype, device="cuda")
+    out = buf[:, :t.shape[1]]
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("M,H,I", [(300, 96, 304), (300, 96, 3536), (515, 672, 8752)])
+def test_offsets_past_32_bits_gated(M, H, I):
+    """Rows as far apart as the calls take them: the same bits as packed ones."""
+    banner(f"far rows gated M={M} H={H} I={I}")
+    g = gen(M)
+    x, w, dy = randn(g, (M, H)), randn(g, (2 * I, H), 0.1), randn(g, (M, I))
+    y, h = bi.bi_gated_linear_bf16(x, w.t(), save_h=True)
+    pitch = (1 << 23) - 1024                                        # 255 rows and the last row's end: below 4 GiB
+    xf = far(x, pitch)
+    yf = far(torch.zeros_like(y), pitch)
+    bi.bi_gated_linear_bf16(xf, w.t(), out=yf)
+    same(yf, y, "x, y")
+    del yf
+    wp = ((1 << 32) // (I + 256) // 2 - H) // 8 * 8
+    if 2 * I * wp * 2 > 1 << 32:
+        same(bi.bi_gated_linear_bf16(x, far(w, wp).t()), y, "w")
+    dx, dw = bi.bi_gated_linear_bf16_bwd(dy, x, w.t(), h)
+    dxf, dwf = bi.bi_gated_linear_bf16_bwd(far(dy, pitch), xf, w.t(), far(h, pitch))
+    same(dxf, dx, "dx")
+    same(dwf, dw, "dw")
+
+
+def test_offsets_past_32_bits_linear_bwd():
+    M, N, K = 300, 272, 288
+    g = gen(3)
+    dy, x, w = randn(g, (M, N)), randn(g, (M, K)), randn(g, (N, K))
+    pitch = (1 << 23) - 1024
+    want = bi.bi_linear_bf16_bwd(dy, x, w.t())
+    got = bi.bi_linear_bf16_bwd(far(dy, pitch), far(x, pitch), far(w, pitch).t())
+    for a, b, what in zip(got, want, ("dx", "dw", "db")):
+        same(a, b, what)
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 272, 96), (300, 3536, 2080)])
+def test_offsets_past_32_bits_mxfp4(M, N, K):
+    g = gen(4)
+    x, w = randn(g, (M, K)), randn(g, (N, K))
+    q, s = bi.bi_quantize_mxfp4(x)
+    wq, ws = bi.bi_quantize_mxfp4(w)
+    pitch = (1 << 24) - 2048                                        # bytes
+    xf = far(x, pitch // 2)
+    qf, sf = bi.bi_quantize_mxfp4(xf)
+    same(qf, q, "codes")
+    same(sf, s, "scales")
+    y = bi.bi_linear_mxfp4(q, s, wq, ws)
+    same(bi.bi_linear_mxfp4(far(q, pitch), far(s, pitch), wq, ws, out=far(torch.zeros_like(y), pitch)), y, "y")
+    same(bi.bi_dequantize_mxfp4(far(q, pitch), far(s, pitch)), bi.bi_dequantize_mxfp4(q, s), "values")
+
+
 def test_other_stream_and_shared_weights():
     g = gen(8)
     x, w = randn(g, (100, 256)), randn(g, (256, 256), 0.1)
