@@ -16,10 +16,12 @@ bool linear_bwd_fits(int64_t lddy, int64_t ldx, int64_t ldw, int64_t M, int64_t 
            ((N + 63) / 64) * ((K + 63) / 64) < grid;
 }
 
-// Column sums of dy: a workgroup takes 64 columns and all rows; thread (row
+// Column sums of dy where dw's tiles do not take them along (dw not wanted, or in
+// its largest tiles, whose matrix instructions leave no room: 221 us against 217
+// at 4096 x 4096 x 4096): a workgroup takes 64 columns and all rows; thread (row
 // lane, group of 8 columns) adds its rows in ascending order in fp32, and the 64
-// row lanes are added in order.  No split over rows, so nothing is left to fold:
-// the workgroups run beside the products' tiles, whose time grows with M too.
+// row lanes are added in order.  No split over rows, so nothing is left to fold.
+// 4096 x 4096 alone: 11 us, 3.4 TB/s (256 workgroups of 16 columns: the same).
 struct SumArgs {
     const uint16_t* dy;
     int64_t lddy;
@@ -147,7 +149,7 @@ static float pair_time(const TileShape& a, const TileShape& b, int64_t M, int64_
 }
 
 template <int DX, int DW>
-static hipError_t bwd_launch(TileArgs dx, TileArgs dw, const SumArgs& sum, hipStream_t s)
+static hipError_t bwd_launch(TileArgs dx, TileArgs dw, SumArgs sum, hipStream_t s)
 {
     using CX = typename BwdShape<DX, false>::C;
     using CW = typename BwdShape<DW, true>::C;
@@ -156,6 +158,12 @@ static hipError_t bwd_launch(TileArgs dx, TileArgs dw, const SumArgs& sum, hipSt
     dw.tiles_m = (dw.M + CW::BM - 1) / CW::BM;
     dw.tiles_n = (dw.N + CW::BN - 1) / CW::BN;
     const int ndx = dx.y ? dx.tiles_m * dx.tiles_n : 0, ndw = dw.y ? dw.tiles_m * dw.tiles_n : 0;
+    // beside the tiles, workgroups of sums end last: M 4096, N and K 1024 took 38.9
+    // us with them and takes 31.4 (N 256, K 4096: 42.1, 34.9; M 333: 10.9, 11.2)
+    if (dw.y && CW::kSums) {
+        dw.db = sum.db;
+        sum.db = nullptr;
+    }
     const int nsum = sum.db ? (sum.N + kSumCols - 1) / kSumCols : 0;
     if (!grid_ok((int64_t)ndx + ndw + nsum))
         return hipErrorInvalidConfiguration;
@@ -232,8 +240,9 @@ hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x
         return bwd_launch_pair(best, a, b, sum, s);
     TileArgs none{};
     SumArgs nosum{};
-    const hipError_t e = bwd_launch_pair(pair_with(0, bx), a, none, sum, s);
-    return e != hipSuccess ? e : bwd_launch_pair(pair_with(1, bw), none, b, nosum, s);
+    const bool summed = bw < kNumDwShapes;          // by dw's tiles: all but the largest
+    const hipError_t e = bwd_launch_pair(pair_with(0, bx), a, none, summed ? nosum : sum, s);
+    return e != hipSuccess ? e : bwd_launch_pair(pair_with(1, bw), none, b, summed ? sum : nosum, s);
 }
 
 __global__ __launch_bounds__(256) void k_zero_rows(unsigned char* __restrict__ p, int64_t pitch, int64_t rows, int64_t words)

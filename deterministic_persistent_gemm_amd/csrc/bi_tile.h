@@ -49,6 +49,7 @@ struct TileArgs {
     int gate;                   // TileGate
     int M, N;                   // outputs (gated: N = I)
     int64_t K;                  // k values
+    float* db;                  // column operand A: [M] sums of its columns over k, or nullptr
     int tiles_m, tiles_n;
 };
 
@@ -204,6 +205,7 @@ struct TileCfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, R = R_, EPI = EPI_;
     static constexpr bool CA = CA_, CB = CB_, FP4 = FP4_;
     static constexpr int NW = WM * WN;
+    static constexpr bool kSums = CA && BM_ < 256;
     static constexpr int FM = BM / (WM * 16), FN = BN / (WN * 16);
     static constexpr TileDeal kDeal = tile_deal<FN, EPI>();
     // 128 bytes of a row at a time: 17 to 32 percent off a 128 x 128 bf16 tile's
@@ -462,6 +464,53 @@ __device__ __forceinline__ u32x4 mask_k(u32x4 v, int64_t valid)
     }
 }
 
+// Sums of A's columns, taken from the fragments on their way to the matrix
+// instructions by the first wave column of the first tile column.  Each lane adds
+// its k values in ascending order, two per instruction (a bf16 dot product with
+// ones, fp32 accumulation; shifts and adds cost 4096 x 1024 x 1024 31.4 -> 34.8
+// us); the four lanes of a column are added at the end.  Not in the largest
+// tiles: their waves take turns at the barriers, and all wait for the one that
+// adds.
+template <typename C>
+struct TileSums {
+    float v[C::kSums ? C::FM : 1] = {};
+    bool on;
+
+    __device__ __forceinline__ TileSums(const TileArgs& p, int n0, int wn) : on(C::kSums && p.db && n0 == 0 && wn == 0) {}
+    __device__ __forceinline__ void add(const u32x4 (&x)[C::FM])
+    {
+        if constexpr (C::kSums) {
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            const bf16x2 ones = __builtin_bit_cast(bf16x2, 0x3f803f80u);
+            if (on) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int f = 0; f < C::FM; ++f) {
+                        const uint32_t two = x[f][j];
+                        v[f] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two), ones, v[f], false);
+                    }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(const TileArgs& p, int m0, int wm, int r, int g)
+    {
+        if constexpr (C::kSums) {
+            if (on) {
+#pragma unroll
+                for (int fm = 0; fm < C::FM; ++fm) {
+                    float t = v[fm];
+                    t += __shfl_xor(t, 16);
+                    t += __shfl_xor(t, 32);
+                    const int m = m0 + (wm * C::FM + fm) * 16 + r;
+                    if (g == 0 && m < p.M)
+                        p.db[m] = t;
+                }
+            }
+        }
+    }
+};
+
 // Stores a wave's outputs: row r of fragment fm, columns as dealt.
 template <typename C>
 __device__ __forceinline__ void tile_store(const TileArgs& p, const f32x4 (&acc)[C::FM][C::FN], int m0, int n0, int wm, int wn,
@@ -600,6 +649,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn)
             acc[fm][fn] = f32x4{0.f, 0.f, 0.f, 0.f};
+    TileSums<C> sums(p, n0, wn);
     u32x4 xa[FM], xb[FM], wf[FN];
     int sxa[FM], sxb[FM], swf[FN];
 
@@ -630,13 +680,6 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
     auto step = [&](auto whole_loads, auto tail, int s, int j, u32x4 (&xc)[FM], int (&sxc)[FM], u32x4 (&xn)[FM], int (&sxn)[FM])
                     __attribute__((always_inline)) {
         const bool stage_end = j % KB == KB - 1;                   // compile-time after unrolling
-        if (stage_end) {
-            // no MFMA of the slices before may sink past the barrier: having
-            // issued, they are the proof that their fragments have been read
-            __builtin_amdgcn_sched_barrier(0);
-            async_wait<(R - 3) * LS>();
-            wg_barrier();
-        }
         if constexpr (decltype(tail)::value) {
             // this lane's slot: k values from s * kSliceK + g * kSliceK / 4 on
             const int64_t valid = p.K - (int64_t)s * kSliceK - g * (kSliceK / 4);
@@ -650,6 +693,20 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
                 wf[f] = mask_k<FP4>(wf[f], valid);
                 swf[f] = valid > 0 ? swf[f] : 127;
             }
+        }
+        if (stage_end) {
+            // no MFMA of the slices before may sink past the barrier: having
+            // issued, they are the proof that their fragments have been read
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (C::kSums) {
+                // here, where nothing may be scheduled across anyway: the slice
+                // before, still in the registers the next reads will fill, and this one
+                static_assert(KB == 2, "two slices per stage");
+                sums.add(xn);
+                sums.add(xc);
+            }
+            async_wait<(R - 3) * LS>();
+            wg_barrier();
         }
         const int nat = at(s + 1), nj = (j + 1) % KB;
 #pragma unroll
@@ -690,6 +747,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
         body(std::false_type{}, std::true_type{}, whole);
     // the loads still in flight land before the workgroup's LDS is given away
     async_wait<0>();
+    sums.store(p, m0, wm, r, g);
     tile_store<C>(p, acc, m0, n0, wm, wn, r, g);
 }
 
@@ -756,7 +814,7 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
     // the MFMAs of a slice with loads t0 .. t1-1 of stage st spread among them
     auto compute = [&](auto whole_loads, int st, auto t0, auto t1) __attribute__((always_inline)) {
         constexpr int kLoads = decltype(t1)::value - decltype(t0)::value;
-        constexpr int kEvery = kLoads > 0 ? FM * FN / kLoads : FM * FN + 1;
+        constexpr int kEvery = FM * FN / (kLoads > 0 ? kLoads : 1);
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll

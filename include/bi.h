@@ -274,8 +274,8 @@ bi_status_t bi_gated_linear_bf16_bwd(const uint16_t* dy, int64_t lddy,
 size_t bi_gated_linear_bwd_workspace_size(int64_t M, int64_t I);
 
 /* Gradients of bi_linear_bf16: dx[M,K] = bf16( dy[M,N] . w[N,K] ),
- * dw[N,K] = dy^T . x (bf16 or fp32), db[N] = sum of dy's rows (fp32).  Any of
- * dx, dw, db may be NULL, and w (read for dx only) and x (for dw only) with
+ * dw[N,K] = dy^T . x (bf16 or fp32), db[N] = sum of dy's rows (fp32; subnormal
+ * values may count as zero).  Any of dx, dw, db may be NULL, and w (read for dx only) and x (for dw only) with
  * them.  M == 0 clears dw and db.  Requires N % 16 == 0, K % 32 == 0.  No
  * workspace. */
 bi_status_t bi_linear_bf16_bwd(const uint16_t* dy, int64_t lddy,

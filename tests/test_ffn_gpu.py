@@ -196,6 +196,20 @@ def test_linear_bwd_exact_on_integers(M, N, K):
     same(bi.bi_linear_bf16_bwd(dy, None, None, need_dx=False, need_dw=False)[2], db, "db alone")
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 528, 512), (16, 4096, 4096), (333, 2048, 768), (700, 80, 64), (1000, 1040, 1024),
+                                   (1031, 2064, 2080), (4100, 272, 32)])
+def test_linear_bwd_column_sums(M, N, K):
+    """db by dw's tiles and by workgroups of its own, beside both gradients, one
+    and none; small integers, so that every order of adding is exact."""
+    banner(f"linear_bwd sums M={M} N={N} K={K}")
+    g = gen(M + N + K)
+    dy, x, w = ints(g, (M, N), -3, 3), ints(g, (M, K), -3, 3), ints(g, (N, K), -3, 3)
+    want = dy.double().sum(0).float()
+    for kw in (dict(), dict(need_dx=False), dict(need_dw=False), dict(need_dx=False, need_dw=False),
+               dict(dw_dtype=torch.float32)):
+        same(bi.bi_linear_bf16_bwd(dy, x, w.t(), **kw)[2] + 0.0, want, f"db {kw}")
+
+
 @pytest.mark.parametrize("M,N,K", BWD)
 def test_linear_bwd_against_64_bits(M, N, K):
     banner(f"linear_bwd M={M} N={N} K={K}")
