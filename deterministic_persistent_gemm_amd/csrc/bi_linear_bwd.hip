@@ -62,8 +62,11 @@ __device__ __forceinline__ void colsum_body(const SumArgs& p, unsigned char* lds
 }
 
 // Tile shapes of the two products, all on 512 threads so that any two can share
-// a launch.  dx's two smallest stream (short batches: few tiles and a long sum
-// over N); the others load and compute in every wave.
+// a launch.  dx's three smallest stream (short batches: few tiles and a long sum
+// over N); the others load and compute in every wave.  16 x 32 is for the
+// longest sums on the fewest tiles, where a slice's time is the delivery of its
+// bytes to one compute unit: 30 rows, N 16928, K 992 take 45 us instead of 56 on
+// 32 x 32 tiles, 119 rows, N 6752, K 1792 35 instead of 27.
 template <int SHAPE, bool CA> struct BwdShape;
 template <bool CA> struct BwdShape<0, CA> {
     using C = TileCfg<32, 32, 2, 2, 4, 4, CA, true, false, kEpiLinear>;
@@ -85,6 +88,10 @@ template <bool CA> struct BwdShape<3, CA> {
     using C = TileCfg<128, 128, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
     static constexpr int NL = 0;
 };
+template <> struct BwdShape<5, false> {
+    using C = TileCfg<16, 32, 1, 2, 4, 4, false, true, false, kEpiLinear>;
+    static constexpr int NL = 4;
+};
 template <bool CA> struct BwdShape<4, CA> {
     using C = TileCfg<256, 256, CA ? 4 : 2, CA ? 2 : 4, 2, 2, CA, true, false, kEpiLinear>;
     static constexpr int NL = 0;
@@ -93,7 +100,10 @@ template <bool CA> struct BwdShape<4, CA> {
 template <typename S>
 __device__ __forceinline__ void bwd_body(const TileArgs& p, unsigned char* ring, int block)
 {
-    static_assert((S::C::NW + S::NL) * 64 == kBwdThreads, "one workgroup size");
+    constexpr int kUsed = (S::C::NW + S::NL) * 64;
+    static_assert(kUsed == kBwdThreads || (S::NL > 0 && kUsed < kBwdThreads), "one workgroup size");
+    if (kUsed < kBwdThreads && (int)threadIdx.x >= kUsed)
+        return;                                         // a barrier counts the waves that are left
     if constexpr (S::NL > 0)
         stream_body<typename S::C, S::NL>(p, ring, block);
     else if constexpr (S::C::R == 2)
@@ -122,20 +132,22 @@ __global__ __launch_bounds__(kBwdThreads) void k_bwd(TileArgs dx, TileArgs dw, S
 
 // the costs are explained in bi_tile_rule.h
 static const TileShape kDxShapes[] = {{32, 32, 1.17f, 0.054f, 1.13f}, {32, 64, 1.71f, 0.075f, 1.05f}, {128, 64, 1.38f, 0.154f, 0.f},
-                                      {128, 128, 1.61f, 0.231f, 0.f}, {256, 256, 3.29f, 0.554f, 0.f}};
+                                      {128, 128, 1.61f, 0.231f, 0.f}, {256, 256, 3.29f, 0.554f, 0.f}, {16, 32, 1.00f, 0.047f, 1.76f}};
 static const TileShape kDwShapes[] = {{0, 0, 0.f, 0.f, 0.f},          {64, 64, 1.61f, 0.113f, 1.04f}, {128, 64, 2.34f, 0.165f, 0.f},
                                       {128, 128, 2.88f, 0.235f, 0.f}, {256, 256, 6.22f, 0.590f, 0.f}};
-constexpr int kNumDxShapes = 5, kNumDwShapes = 4;       // dw: shapes 1 .. 4
+constexpr int kNumDxShapes = 6, kNumDwShapes = 4;       // dw: shapes 1 .. 4
 
 // The shape pairs that are built; a product alone may use its side of any.
-static const int kBwdPairs[][2] = {{0, 1}, {1, 1}, {2, 1}, {0, 2}, {2, 2}, {0, 3}, {2, 3}, {3, 3}, {3, 4}, {4, 4}};
+static const int kBwdPairs[][2] = {{0, 1}, {1, 1}, {2, 1}, {0, 2}, {2, 2}, {0, 3}, {2, 3}, {3, 3}, {3, 4}, {4, 4},
+                                   {5, 1}, {5, 2}, {5, 3}};
 constexpr int kNumBwdPairs = (int)(sizeof(kBwdPairs) / sizeof(kBwdPairs[0]));
 
 // Both products in one launch: all tiles' times spread over the compute units
 // plus a part of a last round, but at least the longest tile's time, with some of
 // the other's where there is more than one round.  Over 54 problems the launches
-// chosen this way took 1.02 times the fastest of the ten pairs and of all shapes
-// in two launches.
+// chosen this way took 1.02 times the fastest of the ten pairs without 16 x 32
+// tiles and of all shapes in two launches; with those, 98 drawn backward passes took
+// 0.98 of their time before, 0.78 to 0.95 where dx runs on them.
 static float pair_time(const TileShape& a, const TileShape& b, int64_t M, int64_t N, int64_t K, bool dw_f32, int cus)
 {
     const float ta = tile_once(a, (N + 31) / 32, false), tb = tile_once(b, (M + 31) / 32, dw_f32);
@@ -183,7 +195,10 @@ static hipError_t bwd_launch_pair(int pair, const TileArgs& dx, const TileArgs& 
     case 6: return bwd_launch<2, 3>(dx, dw, sum, s);
     case 7: return bwd_launch<3, 3>(dx, dw, sum, s);
     case 8: return bwd_launch<3, 4>(dx, dw, sum, s);
-    default: return bwd_launch<4, 4>(dx, dw, sum, s);
+    case 9: return bwd_launch<4, 4>(dx, dw, sum, s);
+    case 10: return bwd_launch<5, 1>(dx, dw, sum, s);
+    case 11: return bwd_launch<5, 2>(dx, dw, sum, s);
+    default: return bwd_launch<5, 3>(dx, dw, sum, s);
     }
 }
 
