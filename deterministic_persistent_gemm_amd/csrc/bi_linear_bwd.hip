@@ -62,7 +62,7 @@ __device__ __forceinline__ void colsum_body(const SumArgs& p, unsigned char* lds
 }
 
 // Tile shapes of the two products, all on 512 threads so that any two can share
-// a launch.  dx's three smallest stream (short batches: few tiles and a long sum
+// a launch.  dx's four smallest stream (short batches: few tiles and a long sum
 // over N); the others load and compute in every wave.  16 x 32 is for the
 // longest sums on the fewest tiles, where a slice's time is the delivery of its
 // bytes to one compute unit: 30 rows, N 16928, K 992 take 45 us instead of 56 on
@@ -90,6 +90,10 @@ template <bool CA> struct BwdShape<3, CA> {
 };
 template <> struct BwdShape<5, false> {
     using C = TileCfg<16, 32, 1, 2, 4, 4, false, true, false, kEpiLinear>;
+    static constexpr int NL = 4;
+};
+template <> struct BwdShape<6, false> {
+    using C = TileCfg<64, 64, 2, 2, 2, 4, false, true, false, kEpiLinear>;
     static constexpr int NL = 4;
 };
 template <bool CA> struct BwdShape<4, CA> {
@@ -132,22 +136,29 @@ __global__ __launch_bounds__(kBwdThreads) void k_bwd(TileArgs dx, TileArgs dw, S
 
 // the costs are explained in bi_tile_rule.h
 static const TileShape kDxShapes[] = {{32, 32, 1.17f, 0.054f, 1.13f}, {32, 64, 1.71f, 0.075f, 1.05f}, {128, 64, 1.38f, 0.154f, 0.f},
-                                      {128, 128, 1.61f, 0.231f, 0.f}, {256, 256, 3.29f, 0.554f, 0.f}, {16, 32, 1.00f, 0.047f, 1.76f}};
+                                      {128, 128, 1.61f, 0.231f, 0.f}, {256, 256, 3.29f, 0.554f, 0.f}, {16, 32, 1.00f, 0.047f, 1.76f},
+                                      {64, 64, 1.20f, 0.095f, 1.28f}};
 static const TileShape kDwShapes[] = {{0, 0, 0.f, 0.f, 0.f},          {64, 64, 1.61f, 0.113f, 1.04f}, {128, 64, 2.34f, 0.165f, 0.f},
                                       {128, 128, 2.88f, 0.235f, 0.f}, {256, 256, 6.22f, 0.590f, 0.f}};
-constexpr int kNumDxShapes = 6, kNumDwShapes = 4;       // dw: shapes 1 .. 4
+constexpr int kNumDxShapes = 7, kNumDwShapes = 4;       // dw: shapes 1 .. 4
+// A launch before dw's takes one of dx's first six: the seventh's cost was taken
+// beside dw's tiles and is too low for two launches (290 rows, N 16032, K 3296:
+// 184 us instead of 157).
+constexpr int kNumDxApart = 6;
 
 // The shape pairs that are built; a product alone may use its side of any.
 static const int kBwdPairs[][2] = {{0, 1}, {1, 1}, {2, 1}, {0, 2}, {2, 2}, {0, 3}, {2, 3}, {3, 3}, {3, 4}, {4, 4},
-                                   {5, 1}, {5, 2}, {5, 3}};
+                                   {5, 1}, {5, 2}, {5, 3}, {6, 1}, {6, 2}, {6, 3}};
 constexpr int kNumBwdPairs = (int)(sizeof(kBwdPairs) / sizeof(kBwdPairs[0]));
 
 // Both products in one launch: all tiles' times spread over the compute units
 // plus a part of a last round, but at least the longest tile's time, with some of
 // the other's where there is more than one round.  Over 54 problems the launches
 // chosen this way took 1.02 times the fastest of the ten pairs without 16 x 32
-// tiles and of all shapes in two launches; with those, 98 drawn backward passes took
-// 0.98 of their time before, 0.78 to 0.95 where dx runs on them.
+// tiles and streaming 64 x 64 ones and of all shapes in two launches; with the
+// first 98 drawn backward passes took 0.98 of their time, with the second 122 took
+// 0.99 of that (0.72 to 0.95 where dx runs on them; 349 rows, N 8032, K 1568 of a
+// gated layer 70 -> 50 us).
 static float pair_time(const TileShape& a, const TileShape& b, int64_t M, int64_t N, int64_t K, bool dw_f32, int cus)
 {
     const float ta = tile_once(a, (N + 31) / 32, false), tb = tile_once(b, (M + 31) / 32, dw_f32);
@@ -198,7 +209,10 @@ static hipError_t bwd_launch_pair(int pair, const TileArgs& dx, const TileArgs& 
     case 9: return bwd_launch<4, 4>(dx, dw, sum, s);
     case 10: return bwd_launch<5, 1>(dx, dw, sum, s);
     case 11: return bwd_launch<5, 2>(dx, dw, sum, s);
-    default: return bwd_launch<5, 3>(dx, dw, sum, s);
+    case 12: return bwd_launch<5, 3>(dx, dw, sum, s);
+    case 13: return bwd_launch<6, 1>(dx, dw, sum, s);
+    case 14: return bwd_launch<6, 2>(dx, dw, sum, s);
+    default: return bwd_launch<6, 3>(dx, dw, sum, s);
     }
 }
 
@@ -228,7 +242,7 @@ hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x
     b.K = M;
     const int cus = device_cu_count();
     // each product's own best shape, and the best pair for one launch
-    const int bx = pick_tile(kDxShapes, kNumDxShapes, M, K, (N + 31) / 32, false, cus);
+    const int bx = pick_tile(kDxShapes, dw ? kNumDxApart : kNumDxShapes, M, K, (N + 31) / 32, false, cus);
     const int bw = 1 + pick_tile(kDwShapes + 1, kNumDwShapes, N, K, (M + 31) / 32, !dw_bf16, cus);
     auto pair_with = [](int side, int shape) {
         for (int i = 0; i < kNumBwdPairs; ++i)
@@ -243,6 +257,9 @@ hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x
     int best = 0;
     float best_time = 0.f;
     for (int i = 0; i < kNumBwdPairs; ++i) {
+        // half of 64 rows idle (M 1, N 3232, K 1856: 14.8 us against 13.0)
+        if (kBwdPairs[i][0] == 6 && M <= 32)
+            continue;
         const float t = pair_time(kDxShapes[kBwdPairs[i][0]], kDwShapes[kBwdPairs[i][1]], M, N, K, !dw_bf16, cus);
         if (i == 0 || t < best_time) {
             best = i;

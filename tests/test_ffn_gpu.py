@@ -177,7 +177,8 @@ BWD = [(1, 32, 32), (1, 544, 64), (7, 96, 64), (31, 64, 96), (32, 128, 128), (33
 BWD_SHAPES = [(1, 272, 2784), (1, 272, 4192), (1, 80, 4128), (89, 80, 4128), (1, 272, 3424), (1, 400, 4192), (133, 496, 4128),
               (226, 1712, 4000), (1304, 1552, 3360), (135, 4016, 2016), (41, 3728, 3552), (235, 4048, 3872), (1442, 432, 2400),
               (2569, 144, 4128), (807, 816, 4256), (996, 3184, 3616), (4100, 48, 8160),
-              (84, 1440, 672), (29, 1984, 96), (17, 2064, 544), (5, 8208, 32), (2, 2864, 4000)]
+              (84, 1440, 672), (29, 1984, 96), (17, 2064, 544), (5, 8208, 32), (2, 2864, 4000),
+              (33, 80, 2752), (134, 736, 1632), (69, 480, 1632), (65, 528, 2496), (551, 3488, 768)]
 
 
 @pytest.mark.parametrize("M,N,K", BWD + BWD_SHAPES)
