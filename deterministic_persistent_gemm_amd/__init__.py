@@ -70,6 +70,7 @@ _lib.bi_lab_lds_read.argtypes = [_P, _I32, _I32, _P]
 _lib.bi_lab_mfma_rate.argtypes = [_P, _I32, _I32, _I32, _I32, _P]
 _lib.bi_lab_plan.argtypes = [_I32, _I64, _I64, _I64, ctypes.POINTER(_I32)]
 _lib.bi_lab_moe_layout.argtypes = [_I64, _I64, _I64, _I64, _I64, ctypes.POINTER(_I64)]
+_lib.bi_lab_ffn_tile.argtypes = [_I32, _I64, _I64, _I64, _I32, ctypes.POINTER(_I32)]
 _lib.bi_linear_f32_noalloc.argtypes = [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _P]
 _lib.bi_gated_linear_bf16.argtypes = [_P, _I64, _P, _I64, _I32, _P, _I64, _P, _I64, _I64, _I64, _I64, _P]
 _lib.bi_gated_linear_bf16_bwd.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _I64, _P, _I32, _I64,
@@ -84,7 +85,8 @@ for _f in (_lib.bi_linear_f32, _lib.bi_linear_bf16, _lib.bi_negctl_linear_f32, _
            _lib.bi_quantize_mxfp4, _lib.bi_dequantize_mxfp4, _lib.bi_linear_mxfp4,
            _lib.bi_moe_grouped_gemm, _lib.bi_describe_recipe, _lib.bi_indexer_topk,
            _lib.bi_moe_grouped_gemm_ex, _lib.bi_lab_xcc_ids, _lib.bi_lab_empty, _lib.bi_lab_stream_read,
-           _lib.bi_lab_clock, _lib.bi_lab_plan, _lib.bi_lab_moe_layout, _lib.bi_linear_f32_noalloc,
+           _lib.bi_lab_clock, _lib.bi_lab_plan, _lib.bi_lab_moe_layout, _lib.bi_lab_ffn_tile,
+           _lib.bi_linear_f32_noalloc,
            _lib.bi_lab_lds_read, _lib.bi_lab_mfma_rate, _lib.bi_lab_l2_read):
     _f.restype = _I32
 for _f in (_lib.bi_linear_workspace_size, _lib.bi_lab_workspace_size, _lib.bi_moe_workspace_size,
@@ -630,6 +632,16 @@ def moe_layout(M: int, H: int, E: int, I: int, topk: int) -> dict:
     out = (_I64 * 4)()
     _check(_lib.bi_lab_moe_layout(M, H, E, I, topk, out), "bi_lab_moe_layout")
     return {"sorted": out[0], "act": out[1], "part": out[2], "total": out[3]}
+
+
+BI_FFN_MXFP4 = 1
+
+
+def ffn_tile(op: int, M: int, N: int, K: int, out_dtype: int = BI_BF16) -> dict:
+    """The tile shape a feed-forward product of this size takes (bi_lab_ffn_tile)."""
+    out = (_I32 * 8)()
+    _check(_lib.bi_lab_ffn_tile(op, M, N, K, out_dtype, out), "bi_lab_ffn_tile")
+    return dict(zip(("shape", "kernel", "rows", "cols", "slice_k", "stage_slices", "ring_stages", "scale_groups"), out))
 
 
 def bi_lab_empty(grid: int, threads: int = 64):

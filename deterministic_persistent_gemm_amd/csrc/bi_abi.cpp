@@ -7,6 +7,7 @@
 // result is raised, not returned).
 #include <hip/hip_runtime_api.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "bi.h"
 #include "bi_ffn.h"
@@ -496,6 +497,18 @@ bi_status_t bi_linear_mxfp4(const uint8_t* xq, int64_t ldxq, const uint8_t* xs, 
         return BI_EUNSUPPORTED;
     return launch_status(launch_mx_linear(xq, ldxq, xs, ldxs, wq, ldwq, wsc, ldws, bias, y, y_dtype == BI_BF16, ldy, M, N,
                                           K, stream));
+}
+
+bi_status_t bi_lab_ffn_tile(int32_t op, int64_t M, int64_t N, int64_t K, int32_t out_dtype, int32_t* info)
+{
+    if (op != BI_FFN_MXFP4 || !dtype_ok(out_dtype) || M <= 0 || !info)
+        return BI_EINVAL;
+    const bi_status_t st = check_sizes(M, N, K);
+    if (st != BI_OK)
+        return st;
+    const TileInfo t = mx_tile_info(M, N, K, out_dtype == BI_BF16);
+    memcpy(info, &t, sizeof t);
+    return BI_OK;
 }
 
 }  // extern "C"

@@ -14,6 +14,11 @@ namespace bi {
 // 512: launchers return hipErrorInvalidConfiguration for more workgroups.
 inline bool grid_ok(int64_t groups) { return groups < (int64_t(1) << 23); }
 
+// What bi_lab_ffn_tile reports of the tile shape a product takes.
+struct TileInfo {
+    int32_t shape, kernel, bm, bn, slice_k, stage_slices, ring_stages, scale_groups;
+};
+
 // bi_gated.hip
 bool gated_fits(int64_t ldx, int64_t ldw, int64_t M, int64_t I, int64_t H);
 hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int64_t ldw, int gate, uint16_t* y,
@@ -41,5 +46,6 @@ bool mx_fits(int64_t ldx, int64_t ldxs, int64_t ldw, int64_t ldws, int64_t M, in
 hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, int64_t ldxs, const uint8_t* wq,
                             int64_t ldw, const uint8_t* wsc, int64_t ldws, const float* bias, void* y, int y_bf16,
                             int64_t ldy, int64_t M, int64_t N, int64_t K, hipStream_t s);
+TileInfo mx_tile_info(int64_t M, int64_t N, int64_t K, int y_bf16);
 
 }  // namespace bi

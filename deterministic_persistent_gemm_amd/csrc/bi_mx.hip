@@ -135,19 +135,25 @@ bool mx_fits(int64_t ldx, int64_t ldxs, int64_t ldw, int64_t ldws, int64_t M, in
            K < (int64_t(1) << 30) && ((M + 15) / 16) * ((N + 15) / 16) < (int64_t(1) << 31);
 }
 
-template <int BM, int BN, int WM, int WN, int KB, int R, int NL>
+template <int BM, int BN, int WM, int WN, int KB, int R, int NL_>
+struct MxShape {
+    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, true, kEpiLinear>;
+    static constexpr int NL = NL_;
+};
+
+template <typename S>
 static hipError_t mx_tile(TileArgs a, hipStream_t s)
 {
-    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, true, kEpiLinear>;
-    a.tiles_m = (a.M + BM - 1) / BM;
-    a.tiles_n = (a.N + BN - 1) / BN;
+    using C = typename S::C;
+    a.tiles_m = (a.M + C::BM - 1) / C::BM;
+    a.tiles_n = (a.N + C::BN - 1) / C::BN;
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
     if (!grid_ok(tiles))
         return hipErrorInvalidConfiguration;
     const unsigned grid = (unsigned)tiles;
-    if constexpr (NL > 0)
-        k_stream<C, NL><<<grid, (C::NW + NL) * 64, 0, s>>>(a);
-    else if constexpr (R == 2)
+    if constexpr (S::NL > 0)
+        k_stream<C, S::NL><<<grid, (C::NW + S::NL) * 64, 0, s>>>(a);
+    else if constexpr (C::R == 2)
         k_turns<C><<<grid, C::NW * 64, 0, s>>>(a);
     else
         k_tile<C><<<grid, C::NW * 64, 0, s>>>(a);
@@ -159,6 +165,25 @@ static const TileShape kMxShapes[] = {
     {16, 16, 0.87f, 0.032f, 1.10f}, {16, 32, 0.78f, 0.051f, 0.92f},   {32, 32, 0.97f, 0.068f, 1.10f},
     {64, 64, 1.26f, 0.162f, 1.00f}, {128, 128, 2.25f, 0.393f, 1.10f}, {256, 256, 5.08f, 0.961f, 0.f},
 };
+
+static int mx_pick(int64_t M, int64_t N, int64_t K, int y_bf16)
+{
+    return pick_tile(kMxShapes, 6, M, N, (K + 127) / 128, !y_bf16, device_cu_count());
+}
+
+// f of the shape at an index of kMxShapes
+template <typename F>
+static auto mx_shape(int i, F f)
+{
+    switch (i) {
+    case 0: return f(MxShape<16, 16, 1, 1, 8, 4, 4>{});
+    case 1: return f(MxShape<16, 32, 1, 1, 4, 4, 4>{});
+    case 2: return f(MxShape<32, 32, 2, 1, 4, 4, 4>{});
+    case 3: return f(MxShape<64, 64, 4, 1, 2, 4, 0>{});
+    case 4: return f(MxShape<128, 128, 2, 2, 1, 4, 0>{});
+    default: return f(MxShape<256, 256, 2, 4, 2, 2, 0>{});
+    }
+}
 
 hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, int64_t ldxs, const uint8_t* wq,
                             int64_t ldw, const uint8_t* wsc, int64_t ldws, const float* bias, void* y, int y_bf16,
@@ -180,14 +205,13 @@ hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, i
     a.M = (int)M;
     a.N = (int)N;
     a.K = K;
-    switch (pick_tile(kMxShapes, 6, M, N, (K + 127) / 128, !y_bf16, device_cu_count())) {
-    case 0: return mx_tile<16, 16, 1, 1, 8, 4, 4>(a, s);
-    case 1: return mx_tile<16, 32, 1, 1, 4, 4, 4>(a, s);
-    case 2: return mx_tile<32, 32, 2, 1, 4, 4, 4>(a, s);
-    case 3: return mx_tile<64, 64, 4, 1, 2, 4, 0>(a, s);
-    case 4: return mx_tile<128, 128, 2, 2, 1, 4, 0>(a, s);
-    default: return mx_tile<256, 256, 2, 4, 2, 2, 0>(a, s);
-    }
+    return mx_shape(mx_pick(M, N, K, y_bf16), [&](auto shape) { return mx_tile<decltype(shape)>(a, s); });
+}
+
+TileInfo mx_tile_info(int64_t M, int64_t N, int64_t K, int y_bf16)
+{
+    const int i = mx_pick(M, N, K, y_bf16);
+    return mx_shape(i, [i](auto shape) { return tile_info<decltype(shape)>(i); });
 }
 
 }  // namespace bi

@@ -27,6 +27,7 @@
 #pragma once
 
 #include "bi_async.h"
+#include "bi_ffn.h"
 
 namespace bi {
 
@@ -197,6 +198,21 @@ struct TileOperand {
     }
 };
 
+// Groups of four slices' scales a ring must hold where stages of kb < 4 slices each
+// bring a part of the group after theirs, r stages deep: at the end of stage c the
+// loads of stage c + r - 1 overwrite the group that lies a ring behind theirs, while
+// the scales of stage c's last slice may still be on their way to registers (the
+// barrier there waits for loads, not for LDS reads).
+constexpr int scale_ring_groups(int kb, int r)
+{
+    int most = 0;
+    for (int c = 0; c < 4; ++c) {                       // parts repeat every 4 / kb stages
+        const int newest = (c + r - 1) / (4 / kb) + 1, oldest = (c * kb + kb - 1) / 4;
+        most = newest - oldest + 1 > most ? newest - oldest + 1 : most;
+    }
+    return most;
+}
+
 // A tile: BM x BN outputs (gated: BN weight rows, BN / 2 outputs) on WM x WN
 // computing waves, R ring stages of KB slices.  CA, CB: operand A / B stored by
 // columns.
@@ -222,10 +238,11 @@ struct TileCfg {
     // four bytes of 64 rows touches 64 cache lines, which cost the 256 x 256
     // tile 30 percent of its time).  A stage of a whole number of groups brings
     // its own; smaller stages each bring a part of the group after theirs, in a
-    // ring of three groups.
+    // ring of as many groups as are in use at a time: four in the 64 x 64 tile,
+    // three in the larger ones.
     static constexpr int kGroup = (BM + BN) * 16;
     static constexpr bool kGroupInStage = KB % 4 == 0;
-    static constexpr int kGroups = !FP4 ? 0 : kGroupInStage ? R * (KB / 4) : 3;
+    static constexpr int kGroups = !FP4 ? 0 : kGroupInStage ? R * (KB / 4) : scale_ring_groups(KB < 4 ? KB : 4, R);
     static constexpr int kScaleAt = R * kStage;
     static constexpr int kScaleLoads = !FP4 ? 0 : (BM + BN) / 16 * KB / 4;     // per stage, 16 rows each
     static constexpr int kRing = kScaleAt + kGroups * kGroup;
@@ -234,6 +251,14 @@ struct TileCfg {
     static_assert(!(FP4 && (CA || CB)), "4-bit operands are stored by rows");
     static_assert(EPI != kEpiGated || !CB, "the gated weight is stored by rows");
 };
+
+// Shape S (its TileCfg S::C and loading waves S::NL) at index i of its product's list.
+template <typename S>
+TileInfo tile_info(int i)
+{
+    using C = typename S::C;
+    return {i, S::NL > 0 ? 0 : C::R == 2 ? 2 : 1, C::BM, C::kOutN, C::kSliceK, C::KB, C::R, C::kGroups};
+}
 
 // The loads of a stage, spread over NL loading waves (this one is `wl`).
 // Row operands: a load covers 16 tile rows of one slice, or 8 rows of a pair;
@@ -696,7 +721,10 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
         }
         if (stage_end) {
             // no MFMA of the slices before may sink past the barrier: having
-            // issued, they are the proof that their fragments have been read
+            // issued, they are the proof that their fragments have been read.  This
+            // slice's fragments and scales may still be on their way: the loads
+            // below refill the code slot of the stage before, and a scale group
+            // that scale_ring_groups keeps clear of this slice's
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (C::kSums) {
                 // here, where nothing may be scheduled across anyway: the slice
