@@ -97,15 +97,9 @@ bi_status_t launch_status(hipError_t e)
 
 size_t dh_bytes(int64_t M, int64_t I) { return (size_t)M * 2 * (size_t)I * 2; }
 
-// The gradients of a linear layer; the operands have been checked.  An empty
-// batch has no dx, and zero dw and db.
-bi_status_t run_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
-                           int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int32_t dw_dtype, int64_t lddw, float* db,
-                           int64_t M, int64_t N, int64_t K, hipStream_t stream)
+// The gradients of an empty batch: zero dw and db.
+bi_status_t run_empty_bwd(void* dw, int32_t dw_dtype, int64_t lddw, float* db, int64_t N, int64_t K, hipStream_t stream)
 {
-    if (M > 0)
-        return launch_status(launch_linear_bwd(dy, lddy, x, ldx, w, ldw, dx, lddx, dw, dw_dtype == BI_BF16, lddw, db, M,
-                                               N, K, stream));
     const int64_t es = dtype_bytes(dw_dtype);
     if (dw && launch_zero_rows(dw, lddw * es, N, K * es, stream) != hipSuccess)
         return BI_EHIP;
@@ -412,22 +406,25 @@ bi_status_t bi_gated_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uin
         return st;
     if (dw && !matrix_ok(dw, lddw, H, dtype_bytes(dw_dtype)))
         return BI_EINVAL;
-    if (M > 0) {
-        if (!matrix_ok(dy, lddy, I, 2) || !matrix_ok(h, ldh, 2 * I, 2))
-            return BI_EINVAL;
-        if (dx && (!matrix_ok(dx, lddx, H, 2) || !matrix_ok(w13, ldw, H, 2)))
-            return BI_EINVAL;
-        if (dw && !matrix_ok(x, ldx, H, 2))
-            return BI_EINVAL;
-        if (!linear_bwd_fits(2 * I, dw ? ldx : 0, dx ? ldw : 0, M, 2 * I, H))
-            return BI_EUNSUPPORTED;
-        if (!ws || ws_bytes < kDecodeCounterBytes + dh_bytes(M, I) || !aligned16(ws))
-            return BI_EWORKSPACE;
-    }
-    uint16_t* dh = M > 0 ? reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(ws) + kDecodeCounterBytes) : nullptr;
-    if (M > 0 && launch_gate_bwd(dy, lddy, h, ldh, gate, dh, 2 * I, M, I, stream) != hipSuccess)
+    if (M == 0)
+        return run_empty_bwd(dw, dw_dtype, lddw, nullptr, 2 * I, H, stream);
+    if (!matrix_ok(dy, lddy, I, 2) || !matrix_ok(h, ldh, 2 * I, 2))
+        return BI_EINVAL;
+    if (dx && (!matrix_ok(dx, lddx, H, 2) || !matrix_ok(w13, ldw, H, 2)))
+        return BI_EINVAL;
+    if (dw && !matrix_ok(x, ldx, H, 2))
+        return BI_EINVAL;
+    BwdPlan plan;
+    if (!plan_linear_bwd(dx, dw, false, dw_dtype == BI_BF16, 2 * I, ldx, ldw, M, 2 * I, H, &plan))
+        return BI_EUNSUPPORTED;
+    if (!ws || ws_bytes < kDecodeCounterBytes + dh_bytes(M, I) || !aligned16(ws))
+        return BI_EWORKSPACE;
+    uint16_t* dh = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(ws) + kDecodeCounterBytes);
+    if (launch_gate_bwd(dy, lddy, h, ldh, gate, dh, 2 * I, M, I, stream) != hipSuccess ||
+        launch_linear_bwd(plan, dh, 2 * I, x, ldx, w13, ldw, dx, lddx, dw, dw_dtype == BI_BF16, lddw, nullptr, M, 2 * I, H,
+                          stream) != hipSuccess)
         return BI_EHIP;
-    return run_linear_bwd(dh, 2 * I, x, ldx, w13, ldw, dx, lddx, dw, dw_dtype, lddw, nullptr, M, 2 * I, H, stream);
+    return BI_OK;
 }
 
 bi_status_t bi_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
@@ -441,17 +438,21 @@ bi_status_t bi_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uint16_t*
         return st;
     if ((dw && !matrix_ok(dw, lddw, K, dtype_bytes(dw_dtype))) || (db && !aligned16(db)))
         return BI_EINVAL;
-    if (M > 0) {
-        if (!matrix_ok(dy, lddy, N, 2))
-            return BI_EINVAL;
-        if (dx && (!matrix_ok(dx, lddx, K, 2) || !matrix_ok(w, ldw, K, 2)))
-            return BI_EINVAL;
-        if (dw && !matrix_ok(x, ldx, K, 2))
-            return BI_EINVAL;
-        if (!linear_bwd_fits(lddy, dw ? ldx : 0, dx ? ldw : 0, M, N, K))
-            return BI_EUNSUPPORTED;
-    }
-    return run_linear_bwd(dy, lddy, x, ldx, w, ldw, dx, lddx, dw, dw_dtype, lddw, db, M, N, K, stream);
+    if (M == 0)
+        return run_empty_bwd(dw, dw_dtype, lddw, db, N, K, stream);
+    if (!matrix_ok(dy, lddy, N, 2))
+        return BI_EINVAL;
+    if (dx && (!matrix_ok(dx, lddx, K, 2) || !matrix_ok(w, ldw, K, 2)))
+        return BI_EINVAL;
+    if (dw && !matrix_ok(x, ldx, K, 2))
+        return BI_EINVAL;
+    BwdPlan plan;
+    if (!plan_linear_bwd(dx, dw, db, dw_dtype == BI_BF16, lddy, ldx, ldw, M, N, K, &plan))
+        return BI_EUNSUPPORTED;
+    return launch_linear_bwd(plan, dy, lddy, x, ldx, w, ldw, dx, lddx, dw, dw_dtype == BI_BF16, lddw, db, M, N, K, stream) ==
+                   hipSuccess
+               ? BI_OK
+               : BI_EHIP;
 }
 
 bi_status_t bi_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t ldx, uint8_t* q, int64_t ldq, uint8_t* sc,

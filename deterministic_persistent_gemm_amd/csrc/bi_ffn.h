@@ -28,12 +28,20 @@ hipError_t launch_gate_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* h, 
                            int64_t lddh, int64_t M, int64_t I, hipStream_t s);
 
 // bi_linear_bwd.hip
-bool linear_bwd_fits(int64_t lddy, int64_t ldx, int64_t ldw, int64_t M, int64_t N, int64_t K);
+// The launches of a backward pass: pairs of tile shapes, second -1 where one
+// launch takes both products.
+struct BwdPlan {
+    int first, second;
+};
+// Plans the pass for the outputs wanted, M >= 1; false where the sizes or a
+// launch's grid are out of range.
+bool plan_linear_bwd(bool dx, bool dw, bool db, int dw_bf16, int64_t lddy, int64_t ldx, int64_t ldw, int64_t M, int64_t N,
+                     int64_t K, BwdPlan* plan);
 // dx [M, K] = dy [M, N] . w [N, K], dw [N, K] = dy^T . x [M, K] and db [N] = the
-// sum of dy's rows, each where its output is not null; M >= 1
-hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
-                             int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int dw_bf16, int64_t lddw, float* db,
-                             int64_t M, int64_t N, int64_t K, hipStream_t s);
+// sum of dy's rows, each where its output is not null
+hipError_t launch_linear_bwd(const BwdPlan& plan, const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                             const uint16_t* w, int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int dw_bf16, int64_t lddw,
+                             float* db, int64_t M, int64_t N, int64_t K, hipStream_t s);
 // rows of `bytes` (a multiple of 4) at a pitch of `pitch` bytes, set to zero
 hipError_t launch_zero_rows(void* p, int64_t pitch, int64_t rows, int64_t bytes, hipStream_t s);
 

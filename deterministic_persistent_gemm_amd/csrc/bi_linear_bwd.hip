@@ -8,7 +8,8 @@
 
 namespace bi {
 
-bool linear_bwd_fits(int64_t lddy, int64_t ldx, int64_t ldw, int64_t M, int64_t N, int64_t K)
+// What the kernels' 32-bit offsets and tile counts can hold.
+static bool in_range(int64_t lddy, int64_t ldx, int64_t ldw, int64_t M, int64_t N, int64_t K)
 {
     const int64_t lim = int64_t(1) << 32, grid = int64_t(1) << 29;
     return 255 * lddy * 2 + N * 2 < lim && 32 * lddy * 2 + 512 < lim && 32 * ldw * 2 + 512 < lim &&
@@ -135,10 +136,10 @@ __global__ __launch_bounds__(kBwdThreads) void k_bwd(TileArgs dx, TileArgs dw, S
 }
 
 // the costs are explained in bi_tile_rule.h
-static const TileShape kDxShapes[] = {{32, 32, 1.17f, 0.054f, 1.13f}, {32, 64, 1.71f, 0.075f, 1.05f}, {128, 64, 1.38f, 0.154f, 0.f},
+static constexpr TileShape kDxShapes[] = {{32, 32, 1.17f, 0.054f, 1.13f}, {32, 64, 1.71f, 0.075f, 1.05f}, {128, 64, 1.38f, 0.154f, 0.f},
                                       {128, 128, 1.61f, 0.231f, 0.f}, {256, 256, 3.29f, 0.554f, 0.f}, {16, 32, 1.00f, 0.047f, 1.76f},
                                       {64, 64, 1.20f, 0.095f, 1.28f}};
-static const TileShape kDwShapes[] = {{0, 0, 0.f, 0.f, 0.f},          {64, 64, 1.61f, 0.113f, 1.04f}, {128, 64, 2.34f, 0.165f, 0.f},
+static constexpr TileShape kDwShapes[] = {{0, 0, 0.f, 0.f, 0.f},          {64, 64, 1.61f, 0.113f, 1.04f}, {128, 64, 2.34f, 0.165f, 0.f},
                                       {128, 128, 2.88f, 0.235f, 0.f}, {256, 256, 6.22f, 0.590f, 0.f}};
 constexpr int kNumDxShapes = 7, kNumDwShapes = 4;       // dw: shapes 1 .. 4
 // A launch before dw's takes one of dx's first six: the seventh's cost was taken
@@ -171,25 +172,28 @@ static float pair_time(const TileShape& a, const TileShape& b, int64_t M, int64_
     return kTileLaunch + (all > longest ? all : longest);
 }
 
+// Beside dw's tiles, workgroups of sums end last: M 4096, N and K 1024 took 38.9
+// us with them and takes 31.4 (N 256, K 4096: 42.1, 34.9; M 333: 10.9, 11.2).  So
+// dw's tiles sum, all but the largest.
+constexpr bool tiles_sum(int dw_shape) { return dw_shape < kNumDwShapes; }
+
 template <int DX, int DW>
 static hipError_t bwd_launch(TileArgs dx, TileArgs dw, SumArgs sum, hipStream_t s)
 {
     using CX = typename BwdShape<DX, false>::C;
     using CW = typename BwdShape<DW, true>::C;
+    static_assert(CX::BM == kDxShapes[DX].bm && CX::BN == kDxShapes[DX].bn && CW::BM == kDwShapes[DW].bm &&
+                      CW::BN == kDwShapes[DW].bn && CW::kSums == tiles_sum(DW), "the rule's table");
     dx.tiles_m = (dx.M + CX::BM - 1) / CX::BM;
     dx.tiles_n = (dx.N + CX::BN - 1) / CX::BN;
     dw.tiles_m = (dw.M + CW::BM - 1) / CW::BM;
     dw.tiles_n = (dw.N + CW::BN - 1) / CW::BN;
     const int ndx = dx.y ? dx.tiles_m * dx.tiles_n : 0, ndw = dw.y ? dw.tiles_m * dw.tiles_n : 0;
-    // beside the tiles, workgroups of sums end last: M 4096, N and K 1024 took 38.9
-    // us with them and takes 31.4 (N 256, K 4096: 42.1, 34.9; M 333: 10.9, 11.2)
     if (dw.y && CW::kSums) {
         dw.db = sum.db;
         sum.db = nullptr;
     }
     const int nsum = sum.db ? (sum.N + kSumCols - 1) / kSumCols : 0;
-    if (!grid_ok((int64_t)ndx + ndw + nsum))
-        return hipErrorInvalidConfiguration;
     k_bwd<DX, DW><<<(unsigned)(ndx + ndw + nsum), kBwdThreads, 0, s>>>(dx, dw, sum, ndx, ndw);
     return hipGetLastError();
 }
@@ -216,9 +220,68 @@ static hipError_t bwd_launch_pair(int pair, const TileArgs& dx, const TileArgs& 
     }
 }
 
-hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
-                             int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int dw_bf16, int64_t lddw, float* db,
-                             int64_t M, int64_t N, int64_t K, hipStream_t s)
+// Workgroups of a launch of shape pair `pair` with these outputs.
+static int64_t pair_groups(int pair, bool dx, bool dw, bool db, int64_t M, int64_t N, int64_t K)
+{
+    const int w = kBwdPairs[pair][1];
+    return (dx ? tile_count(kDxShapes[kBwdPairs[pair][0]], M, K) : 0) + (dw ? tile_count(kDwShapes[w], N, K) : 0) +
+           (db && !(dw && tiles_sum(w)) ? (N + kSumCols - 1) / kSumCols : 0);
+}
+
+// The first pair with this shape on its dx (0) or dw (1) side.
+static int pair_with(int side, int shape)
+{
+    for (int i = 0; i < kNumBwdPairs; ++i)
+        if (kBwdPairs[i][side] == shape)
+            return i;
+    return 0;
+}
+
+static BwdPlan choose(bool dx, bool dw, int dw_bf16, int64_t M, int64_t N, int64_t K)
+{
+    const int cus = device_cu_count();
+    // each product's own best shape, and the best pair for one launch
+    const int bx = pick_tile(kDxShapes, dw ? kNumDxApart : kNumDxShapes, M, K, (N + 31) / 32, false, cus);
+    const int bw = 1 + pick_tile(kDwShapes + 1, kNumDwShapes, N, K, (M + 31) / 32, !dw_bf16, cus);
+    if (!dw)
+        return {pair_with(0, dx ? bx : 1), -1};
+    if (!dx)
+        return {pair_with(1, bw), -1};
+    int best = 0;
+    float best_time = 0.f;
+    for (int i = 0; i < kNumBwdPairs; ++i) {
+        // half of 64 rows idle (M 1, N 3232, K 1856: 14.8 us against 13.0)
+        if (kBwdPairs[i][0] == 6 && M <= 32)
+            continue;
+        const float t = pair_time(kDxShapes[kBwdPairs[i][0]], kDwShapes[kBwdPairs[i][1]], M, N, K, !dw_bf16, cus);
+        if (i == 0 || t < best_time) {
+            best = i;
+            best_time = t;
+        }
+    }
+    const float apart = tile_time(kDxShapes[bx], M, K, (N + 31) / 32, false, cus) +
+                        tile_time(kDwShapes[bw], N, K, (M + 31) / 32, !dw_bf16, cus);
+    if (best_time <= apart)
+        return {best, -1};
+    return {pair_with(0, bx), pair_with(1, bw)};
+}
+
+bool plan_linear_bwd(bool dx, bool dw, bool db, int dw_bf16, int64_t lddy, int64_t ldx, int64_t ldw, int64_t M, int64_t N,
+                     int64_t K, BwdPlan* plan)
+{
+    if (!in_range(lddy, dw ? ldx : 0, dx ? ldw : 0, M, N, K))
+        return false;
+    const BwdPlan p = *plan = choose(dx, dw, dw_bf16, M, N, K);
+    if (p.second < 0)
+        return grid_ok(pair_groups(p.first, dx, dw, db, M, N, K));
+    const bool late = tiles_sum(kBwdPairs[p.second][1]);
+    return grid_ok(pair_groups(p.first, true, false, db && !late, M, N, K)) &&
+           grid_ok(pair_groups(p.second, false, true, db && late, M, N, K));
+}
+
+hipError_t launch_linear_bwd(const BwdPlan& plan, const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                             const uint16_t* w, int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int dw_bf16, int64_t lddw,
+                             float* db, int64_t M, int64_t N, int64_t K, hipStream_t s)
 {
     TileArgs a{}, b{};
     SumArgs sum{dy, lddy, db, M, (int)N};
@@ -240,41 +303,13 @@ hipError_t launch_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x
     b.M = (int)N;
     b.N = (int)K;
     b.K = M;
-    const int cus = device_cu_count();
-    // each product's own best shape, and the best pair for one launch
-    const int bx = pick_tile(kDxShapes, dw ? kNumDxApart : kNumDxShapes, M, K, (N + 31) / 32, false, cus);
-    const int bw = 1 + pick_tile(kDwShapes + 1, kNumDwShapes, N, K, (M + 31) / 32, !dw_bf16, cus);
-    auto pair_with = [](int side, int shape) {
-        for (int i = 0; i < kNumBwdPairs; ++i)
-            if (kBwdPairs[i][side] == shape)
-                return i;
-        return 0;
-    };
-    if (!dw)
-        return bwd_launch_pair(pair_with(0, dx ? bx : 1), a, b, sum, s);
-    if (!dx)
-        return bwd_launch_pair(pair_with(1, bw), a, b, sum, s);
-    int best = 0;
-    float best_time = 0.f;
-    for (int i = 0; i < kNumBwdPairs; ++i) {
-        // half of 64 rows idle (M 1, N 3232, K 1856: 14.8 us against 13.0)
-        if (kBwdPairs[i][0] == 6 && M <= 32)
-            continue;
-        const float t = pair_time(kDxShapes[kBwdPairs[i][0]], kDwShapes[kBwdPairs[i][1]], M, N, K, !dw_bf16, cus);
-        if (i == 0 || t < best_time) {
-            best = i;
-            best_time = t;
-        }
-    }
-    const float apart = tile_time(kDxShapes[bx], M, K, (N + 31) / 32, false, cus) +
-                        tile_time(kDwShapes[bw], N, K, (M + 31) / 32, !dw_bf16, cus);
-    if (best_time <= apart)
-        return bwd_launch_pair(best, a, b, sum, s);
+    if (plan.second < 0)
+        return bwd_launch_pair(plan.first, a, b, sum, s);
     TileArgs none{};
     SumArgs nosum{};
-    const bool summed = bw < kNumDwShapes;          // by dw's tiles: all but the largest
-    const hipError_t e = bwd_launch_pair(pair_with(0, bx), a, none, summed ? nosum : sum, s);
-    return e != hipSuccess ? e : bwd_launch_pair(pair_with(1, bw), none, b, summed ? sum : nosum, s);
+    const bool late = tiles_sum(kBwdPairs[plan.second][1]);
+    const hipError_t e = bwd_launch_pair(plan.first, a, none, late ? nosum : sum, s);
+    return e != hipSuccess ? e : bwd_launch_pair(plan.second, none, b, late ? sum : nosum, s);
 }
 
 __global__ __launch_bounds__(256) void k_zero_rows(unsigned char* __restrict__ p, int64_t pitch, int64_t rows, int64_t words)

@@ -83,6 +83,15 @@ def test_more_workgroups_than_a_launch_holds():
     assert linear_bwd(M=M, N=16, K=32, dw=None, db=None) == bi.BI_EUNSUPPORTED
 
 
+def test_a_refused_backward_pass_enqueues_nothing():
+    """The gated layer's too: its elementwise part is a launch of its own, which
+    without a GPU would be a HIP error."""
+    M = 1 << 30
+    n = L.bi_gated_linear_bwd_workspace_size(M, 16)
+    for kw in (dict(dw=None), dict()):
+        assert gated_bwd(M=M, I=16, H=32, n=n, **kw) == bi.BI_EUNSUPPORTED
+
+
 def test_nothing_to_do():
     assert gated(M=0, x=None, y=None) == bi.BI_OK
     assert gated_bwd(dx=None, dw=None) == bi.BI_OK
