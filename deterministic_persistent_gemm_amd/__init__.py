@@ -634,7 +634,7 @@ def moe_layout(M: int, H: int, E: int, I: int, topk: int) -> dict:
     return {"sorted": out[0], "act": out[1], "part": out[2], "total": out[3]}
 
 
-BI_FFN_MXFP4 = 1
+BI_FFN_GATED, BI_FFN_MXFP4, BI_FFN_DX, BI_FFN_DW = 0, 1, 2, 3
 
 
 def ffn_tile(op: int, M: int, N: int, K: int, out_dtype: int = BI_BF16) -> dict:

@@ -502,12 +502,14 @@ bi_status_t bi_linear_mxfp4(const uint8_t* xq, int64_t ldxq, const uint8_t* xs, 
 
 bi_status_t bi_lab_ffn_tile(int32_t op, int64_t M, int64_t N, int64_t K, int32_t out_dtype, int32_t* info)
 {
-    if (op != BI_FFN_MXFP4 || !dtype_ok(out_dtype) || M <= 0 || !info)
+    if (op < BI_FFN_GATED || op > BI_FFN_DW || !dtype_ok(out_dtype) || M <= 0 || !info)
         return BI_EINVAL;
     const bi_status_t st = check_sizes(M, N, K);
     if (st != BI_OK)
         return st;
-    const TileInfo t = mx_tile_info(M, N, K, out_dtype == BI_BF16);
+    const int bf16 = out_dtype == BI_BF16;
+    const TileInfo t = op == BI_FFN_GATED ? gated_tile_info(M, N, K) : op == BI_FFN_MXFP4 ? mx_tile_info(M, N, K, bf16)
+                       : linear_bwd_tile_info(op == BI_FFN_DW, bf16, M, N, K);
     memcpy(info, &t, sizeof t);
     return BI_OK;
 }

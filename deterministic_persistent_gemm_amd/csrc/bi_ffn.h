@@ -23,6 +23,7 @@ struct TileInfo {
 bool gated_fits(int64_t ldx, int64_t ldw, int64_t M, int64_t I, int64_t H);
 hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int64_t ldw, int gate, uint16_t* y,
                         int64_t ldy, uint16_t* h, int64_t ldh, int64_t M, int64_t I, int64_t H, hipStream_t s);
+TileInfo gated_tile_info(int64_t M, int64_t I, int64_t H);
 // dh [M, 2 I] = [dy * h_u * act'(h_g), dy * act(h_g)]
 hipError_t launch_gate_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* h, int64_t ldh, int gate, uint16_t* dh,
                            int64_t lddh, int64_t M, int64_t I, hipStream_t s);
@@ -42,6 +43,8 @@ bool plan_linear_bwd(bool dx, bool dw, bool db, int dw_bf16, int64_t lddy, int64
 hipError_t launch_linear_bwd(const BwdPlan& plan, const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
                              const uint16_t* w, int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int dw_bf16, int64_t lddw,
                              float* db, int64_t M, int64_t N, int64_t K, hipStream_t s);
+// The shape that dx (side 0) or dw (side 1) takes in a pass with both.
+TileInfo linear_bwd_tile_info(int side, int dw_bf16, int64_t M, int64_t N, int64_t K);
 // rows of `bytes` (a multiple of 4) at a pitch of `pitch` bytes, set to zero
 hipError_t launch_zero_rows(void* p, int64_t pitch, int64_t rows, int64_t bytes, hipStream_t s);
 

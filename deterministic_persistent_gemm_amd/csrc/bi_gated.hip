@@ -16,19 +16,25 @@ bool gated_fits(int64_t ldx, int64_t ldw, int64_t M, int64_t I, int64_t H)
            ((M + 15) / 16) * ((I + 7) / 8) < (int64_t(1) << 31);
 }
 
-template <int BM, int BN, int WM, int WN, int KB, int R, int NL>
+template <int BM, int BN, int WM, int WN, int KB, int R, int NL_>
+struct GatedShape {
+    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, false, kEpiGated>;
+    static constexpr int NL = NL_;
+};
+
+template <typename S>
 static hipError_t gated_tile(TileArgs a, hipStream_t s)
 {
-    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, false, kEpiGated>;
-    a.tiles_m = (a.M + BM - 1) / BM;
+    using C = typename S::C;
+    a.tiles_m = (a.M + C::BM - 1) / C::BM;
     a.tiles_n = (a.N + C::kOutN - 1) / C::kOutN;
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
     if (!grid_ok(tiles))
         return hipErrorInvalidConfiguration;
     const unsigned grid = (unsigned)tiles;
-    if constexpr (NL > 0)
-        k_stream<C, NL><<<grid, (C::NW + NL) * 64, 0, s>>>(a);
-    else if constexpr (R == 2)
+    if constexpr (S::NL > 0)
+        k_stream<C, S::NL><<<grid, (C::NW + S::NL) * 64, 0, s>>>(a);
+    else if constexpr (C::R == 2)
         k_turns<C><<<grid, C::NW * 64, 0, s>>>(a);
     else
         k_tile<C><<<grid, C::NW * 64, 0, s>>>(a);
@@ -40,6 +46,26 @@ static const TileShape kGatedShapes[] = {
     {16, 8, 0.67f, 0.037f, 1.10f}, {16, 16, 0.29f, 0.063f, 1.10f}, {32, 16, 0.64f, 0.072f, 1.10f}, {64, 16, 0.90f, 0.088f, 0.f},
     {128, 32, 0.65f, 0.204f, 0.f}, {128, 64, 0.72f, 0.277f, 0.f},  {256, 128, 1.87f, 0.688f, 0.f},
 };
+
+static int gated_pick(int64_t M, int64_t I, int64_t H)
+{
+    return pick_tile(kGatedShapes, 7, M, I, (H + 31) / 32, false, device_cu_count());
+}
+
+// f of the shape at an index of kGatedShapes
+template <typename F>
+static auto gated_shape(int i, F f)
+{
+    switch (i) {
+    case 0: return f(GatedShape<16, 16, 1, 1, 8, 4, 4>{});
+    case 1: return f(GatedShape<16, 32, 1, 1, 4, 4, 4>{});
+    case 2: return f(GatedShape<32, 32, 2, 1, 4, 4, 4>{});
+    case 3: return f(GatedShape<64, 32, 4, 1, 4, 4, 4>{});
+    case 4: return f(GatedShape<128, 64, 4, 1, 2, 4, 0>{});
+    case 5: return f(GatedShape<128, 128, 4, 2, 2, 4, 0>{});
+    default: return f(GatedShape<256, 256, 4, 2, 2, 2, 0>{});
+    }
+}
 
 hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int64_t ldw, int gate, uint16_t* y,
                         int64_t ldy, uint16_t* h, int64_t ldh, int64_t M, int64_t I, int64_t H, hipStream_t s)
@@ -58,15 +84,13 @@ hipError_t launch_gated(const uint16_t* x, int64_t ldx, const uint16_t* w13, int
     a.M = (int)M;
     a.N = (int)I;
     a.K = H;
-    switch (pick_tile(kGatedShapes, 7, M, I, (H + 31) / 32, false, device_cu_count())) {
-    case 0: return gated_tile<16, 16, 1, 1, 8, 4, 4>(a, s);
-    case 1: return gated_tile<16, 32, 1, 1, 4, 4, 4>(a, s);
-    case 2: return gated_tile<32, 32, 2, 1, 4, 4, 4>(a, s);
-    case 3: return gated_tile<64, 32, 4, 1, 4, 4, 4>(a, s);
-    case 4: return gated_tile<128, 64, 4, 1, 2, 4, 0>(a, s);
-    case 5: return gated_tile<128, 128, 4, 2, 2, 4, 0>(a, s);
-    default: return gated_tile<256, 256, 4, 2, 2, 2, 0>(a, s);
-    }
+    return gated_shape(gated_pick(M, I, H), [&](auto shape) { return gated_tile<decltype(shape)>(a, s); });
+}
+
+TileInfo gated_tile_info(int64_t M, int64_t I, int64_t H)
+{
+    const int i = gated_pick(M, I, H);
+    return gated_shape(i, [i](auto shape) { return tile_info<decltype(shape)>(i); });
 }
 
 // One thread per eight columns of a row: dy, the gate half and the up half of

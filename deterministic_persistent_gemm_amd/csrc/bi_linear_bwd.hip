@@ -279,6 +279,29 @@ bool plan_linear_bwd(bool dx, bool dw, bool db, int dw_bf16, int64_t lddy, int64
            grid_ok(pair_groups(p.second, false, true, db && late, M, N, K));
 }
 
+TileInfo linear_bwd_tile_info(int side, int dw_bf16, int64_t M, int64_t N, int64_t K)
+{
+    const BwdPlan p = choose(true, true, dw_bf16, M, N, K);
+    const int i = kBwdPairs[side == 1 && p.second >= 0 ? p.second : p.first][side];
+    if (side == 1) {
+        switch (i) {
+        case 1: return tile_info<BwdShape<1, true>>(i);
+        case 2: return tile_info<BwdShape<2, true>>(i);
+        case 3: return tile_info<BwdShape<3, true>>(i);
+        default: return tile_info<BwdShape<4, true>>(i);
+        }
+    }
+    switch (i) {
+    case 0: return tile_info<BwdShape<0, false>>(i);
+    case 1: return tile_info<BwdShape<1, false>>(i);
+    case 2: return tile_info<BwdShape<2, false>>(i);
+    case 3: return tile_info<BwdShape<3, false>>(i);
+    case 4: return tile_info<BwdShape<4, false>>(i);
+    case 5: return tile_info<BwdShape<5, false>>(i);
+    default: return tile_info<BwdShape<6, false>>(i);
+    }
+}
+
 hipError_t launch_linear_bwd(const BwdPlan& plan, const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
                              const uint16_t* w, int64_t ldw, uint16_t* dx, int64_t lddx, void* dw, int dw_bf16, int64_t lddw,
                              float* db, int64_t M, int64_t N, int64_t K, hipStream_t s)

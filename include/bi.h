@@ -425,15 +425,16 @@ bi_status_t bi_lab_xcc_ids(uint32_t* out, int32_t grid_x, int32_t grid_y, hipStr
  * the recipe table cannot serve. */
 bi_status_t bi_lab_plan(int32_t dtype, int64_t M, int64_t N, int64_t K, int32_t* path);
 
-/* The tile shape a feed-forward product of this size takes.  op BI_FFN_MXFP4:
- * bi_linear_mxfp4 with out_dtype.  info: host int32[8] = the shape's index in
+/* The tile shape a feed-forward product of this size takes: bi_gated_linear_bf16
+ * (N = I, K = H), bi_linear_mxfp4 with outputs of out_dtype, and dx or dw of
+ * bi_linear_bf16_bwd where both are wanted and dw is of out_dtype.  info: host int32[8] = the shape's index in
  * the product's list; the kernel (0: waves that load beside waves that compute,
  * 1: every wave loads and computes, 2: two groups of waves in turns); output
  * rows and columns per tile; k per slice; slices per stage; stages in the LDS
  * ring; groups of four slices' scales in theirs (0: no scales).  BI_EINVAL for
  * M <= 0, an unknown op or a NULL info, BI_EUNSUPPORTED for widths the product
  * does not serve. */
-typedef enum { BI_FFN_MXFP4 = 1 } bi_ffn_op_t;
+typedef enum { BI_FFN_GATED = 0, BI_FFN_MXFP4 = 1, BI_FFN_DX = 2, BI_FFN_DW = 3 } bi_ffn_op_t;
 bi_status_t bi_lab_ffn_tile(int32_t op, int64_t M, int64_t N, int64_t K, int32_t out_dtype, int32_t* info);
 
 /* Where a MoE call of this shape keeps its storage points in the workspace,

@@ -3,6 +3,8 @@ reads in their LDS rings, on the host.  Nothing here needs a GPU."""
 import pytest
 
 pytest.importorskip("torch")
+from tests import ffn_shapes
+
 bi = pytest.importorskip("deterministic_persistent_gemm_amd")
 
 STREAM, ALL, TURNS = 0, 1, 2
@@ -104,3 +106,32 @@ def test_refusals():
     assert tile(9, 4, 32, 64, 1, out) == tile(1, 0, 32, 64, 1, out) == tile(1, 4, 32, 64, 7, out) == bi.BI_EINVAL
     assert tile(1, 4, 32, 64, 1, None) == bi.BI_EINVAL
     assert tile(1, 4, 24, 64, 1, out) == tile(1, 4, 32, 48, 1, out) == bi.BI_EUNSUPPORTED
+
+
+def steady(op, sizes, dts):
+    """Shapes that some size keeps busy for at least two stages past its ring, and
+    two groups past its ring of scales."""
+    seen = set()
+    for M, N, K in sizes:
+        for dt in dts:
+            t = bi.ffn_tile(op, M, N, K, dt)
+            k = {bi.BI_FFN_DX: N, bi.BI_FFN_DW: M}.get(op, K)
+            slices = -(-k // t["slice_k"])
+            if slices >= (t["ring_stages"] + 1) * t["stage_slices"] + 1 and (
+                    not t["scale_groups"] or -(-slices // 4) >= t["scale_groups"] + 2):
+                seen.add((t["shape"], dt))
+    return seen
+
+
+BF, F32 = bi.BI_BF16, bi.BI_F32
+
+
+@pytest.mark.parametrize("op,sizes,shapes,dts", [
+    (bi.BI_FFN_GATED, ffn_shapes.GATED, range(7), (BF,)), (bi.BI_FFN_MXFP4, ffn_shapes.MXFP4, range(6), (BF, F32)),
+    (bi.BI_FFN_DX, ffn_shapes.LINEAR_BWD, range(7), (BF,)), (bi.BI_FFN_DW, ffn_shapes.LINEAR_BWD, range(1, 5), (BF, F32))],
+    ids=["gated", "mxfp4", "dx", "dw"])
+def test_every_shape_is_tested_past_its_ring(op, sizes, shapes, dts):
+    seen = steady(op, sizes, (BF, F32) if op == bi.BI_FFN_DX else dts)
+    for shape in shapes:
+        for dt in dts:
+            assert (shape, dt) in seen or (op == bi.BI_FFN_DX and (shape, F32) in seen), (shape, dt)
