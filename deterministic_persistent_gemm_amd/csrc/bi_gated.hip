@@ -122,9 +122,9 @@ __global__ __launch_bounds__(256) void k_gate_bwd(const uint16_t* __restrict__ d
                 const float d = __uint_as_float(q ? dv[j] & 0xffff0000u : dv[j] << 16);
                 const float gg = __uint_as_float(q ? gv[j] & 0xffff0000u : gv[j] << 16);
                 const float uu = __uint_as_float(q ? uv[j] & 0xffff0000u : uv[j] << 16);
-                const float sg = gate_sigma(gg, gate);
+                const float s8 = gate_sigma8(gg, gate), sg = s8 * kSigmaScale;
                 const float dz = gate == kGateSilu ? 1.0f : kGeluC2 * (1.0f + 3.0f * kGeluB * fminf(gg * gg, 1e30f));
-                const float act = gg * sg;
+                const float act = gg * kSigmaScale * s8;
                 rg[q] = d * uu * (sg + act * (1.0f - sg) * dz);
                 ru[q] = d * act;
             }

@@ -58,16 +58,21 @@ struct TileArgs {
 constexpr float kGeluC2 = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-// act(g) = g * gate_sigma(g).  exp overflows to +inf for very negative g,
-// where the reciprocal is 0 as it should be.  The hardware exponential and
-// reciprocal (one ulp each, the argument's rounding times its magnitude of at
-// most 88 on top: below 2^-15 relative, far under the bf16 rounding of what is
-// stored) in place of expf and a full division, which made the epilogue of a
-// 256 x 256 tile 9 us long.
-__device__ __forceinline__ float gate_sigma(float g, int gate)
+// 2^8 sigma(z(g)), which the callers scale back: act(g) = (g 2^-8) gate_sigma8(g).
+// For z of -87.4 and below sigma is subnormal, where the hardware reciprocal gives
+// zero, but act = g sigma still a normal number; scaled, it lasts to z = -92.8
+// (sigma = 2^-134), below which act is zero: by then |act| < 2^-127.  g 2^-8
+// keeps 16 bits of fp32's smallest normal g.  exp overflows to +inf for very
+// negative z, where the reciprocal is 0 as it should be.
+// The hardware exponential and reciprocal (one ulp each; the argument's roundings
+// times its magnitude of at most 93 on top: below 2^-14 relative, far under the
+// bf16 rounding of what is stored) in place of expf and a full division, which made
+// the epilogue of a 256 x 256 tile 9 us long.
+constexpr float kSigmaScale = 0.00390625f;          // 2^-8
+__device__ __forceinline__ float gate_sigma8(float g, int gate)
 {
     const float z = gate == kGateSilu ? g : kGeluC2 * (g + kGeluB * g * g * g);
-    return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+    return __builtin_amdgcn_rcpf(kSigmaScale + __builtin_amdgcn_exp2f(__builtin_fmaf(z, -1.4426950408889634f, -8.0f)));
 }
 
 // two fp32 -> packed bf16, round to nearest even
@@ -542,7 +547,7 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, const f32x4 (&acc)
                                            int r, int g)
 {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    auto gated = [&](float gv, float uv) __attribute__((always_inline)) { return gv * gate_sigma(gv, p.gate) * uv; };
+    auto gated = [&](float gv, float uv) __attribute__((always_inline)) { return gv * kSigmaScale * gate_sigma8(gv, p.gate) * uv; };
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm) {
         const int m = m0 + (wm * C::FM + fm) * 16 + r;

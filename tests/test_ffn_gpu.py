@@ -594,3 +594,33 @@ def test_results_repeat():
     for _ in range(5):
         for a, b in zip(first, bi.bi_linear_bf16_bwd(dy, x, w.t(), dw_dtype=torch.float32)):
             same(a, b)
+
+
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 40])
+def test_gated_projections_whose_sigmoid_is_subnormal(gate, scale):
+    """act is still a normal fp32 number where its sigmoid is below fp32's normal
+    range.  Projections are the inputs (one product each), u is `scale`.  Values of
+    act below 2^-127 and of act' below 2^-125 may count as zero; above, relative bounds."""
+    H = I = 64
+    lo, hi, step = ((-92.5, -77.0, 0.5), (-10.75, -9.8125, 0.0625))[gate]
+    vals = torch.arange(lo, hi + step / 2, step, dtype=torch.float64)[:32]
+    w = torch.zeros((2 * I, H), dtype=BF, device="cuda")
+    w[:32, :32] = torch.eye(32, dtype=BF, device="cuda")
+    w[I:, 32] = scale
+    x = torch.zeros((40, H), dtype=BF, device="cuda")
+    x[:, :len(vals)] = vals.to(BF).cuda()
+    assert torch.equal(x[0, :len(vals)].double().cpu(), vals), "the values are bf16 numbers"
+    x[:, 32] = 1.0
+    a, da = ref.act(x[:, :32].double(), gate)
+    y, h = bi.bi_gated_linear_bf16(x, w.t(), gate, save_h=True)
+    # bf16 steps below 2^-126 are 2^-133
+    within(y[:, :32], a * scale, (ref.HALF_BF16 + ref.ACT_REL) * a.abs() * scale + 2.0 ** -127 * scale + 2.0 ** -134, "y")
+    # dh by an identity weight, dy as large as u: both halves, rounded twice
+    dy = torch.full((40, I), 2.0 ** 20, dtype=BF, device="cuda")
+    eye = torch.eye(2 * I, dtype=BF, device="cuda")
+    dx, _ = bi.bi_gated_linear_bf16_bwd(dy, None, eye.t(), h, gate, need_dw=False)
+    wg, wu = da * scale * 2.0 ** 20, a * 2.0 ** 20
+    g = x[:, :32].double()
+    within(dx[:, :32], wg, ref.HALF_BF16 * wg.abs() + 2 * ref.ACT_REL * wg.abs() + 2.0 ** -125 * scale * 2.0 ** 20, "dh gate")
+    within(dx[:, I:I + 32], wu, ref.HALF_BF16 * wu.abs() + 2 * ref.ACT_REL * wu.abs() + 2.0 ** -127 * 2.0 ** 20, "dh up")
