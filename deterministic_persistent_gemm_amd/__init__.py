@@ -539,9 +539,10 @@ def bi_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tenso
     return dx, dw, db
 
 
-def _mx_operand(q, s, dev, name, codes, scales):
+def _mx_operand(q, s, dev, name, codes, scales, words=True):
     """Pitches (bytes) of an MXFP4 operand's codes [rows, K/2] and scales
-    [rows, K/32], and its shape (rows, K)."""
+    [rows, K/32], and its shape (rows, K).  words: scale rows are read in whole
+    32-bit words."""
     if q.dim() != 2:
         raise ValueError(f"{name}: {codes} is [rows, K/2]")
     rows, half = q.shape
@@ -550,7 +551,7 @@ def _mx_operand(q, s, dev, name, codes, scales):
     kb = K // 32
     ldq = _rows(q, torch.uint8, rows, half, dev, name, codes)
     lds = _rows(s, torch.uint8, rows, kb, dev, name, scales, align=4)
-    if kb % 4 and rows and s.storage_offset() + (rows - 1) * lds + (kb + 3) // 4 * 4 > s.untyped_storage().nbytes():
+    if words and kb % 4 and rows and s.storage_offset() + (rows - 1) * lds + (kb + 3) // 4 * 4 > s.untyped_storage().nbytes():
         raise ValueError(f"{name}: {scales} must be readable in whole 32-bit words up to the last row's end")
     return ldq, lds, rows, K
 
@@ -580,7 +581,7 @@ def bi_dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, out_dtype: torch.dtype
     name = "bi_dequantize_mxfp4"
     code = _dtype_code(out_dtype, name, "out_dtype")
     dev = q.get_device()
-    ldq, lds, rows, K = _mx_operand(q, s, dev, name, "q", "s")
+    ldq, lds, rows, K = _mx_operand(q, s, dev, name, "q", "s", words=False)
     y = q.new_empty(rows, K, dtype=out_dtype)
     _call(_lib.bi_dequantize_mxfp4, name, dev, q.data_ptr(), ldq, s.data_ptr(), lds, y.data_ptr(), code, K, rows, K)
     return y

@@ -299,7 +299,8 @@ bi_status_t bi_quantize_mxfp4(const void* x, int32_t x_dtype, int64_t ldx,
                               int64_t rows, int64_t K, hipStream_t stream);
 
 /* The values that codes and scales stand for, as bf16 or fp32 (exact wherever
- * the type holds them; NaN for blocks with s = 255). */
+ * the type holds them; NaN for blocks with s = 255).  The layouts of
+ * bi_quantize_mxfp4; nothing past a row's last code and scale byte is read. */
 bi_status_t bi_dequantize_mxfp4(const uint8_t* q, int64_t ldq, const uint8_t* sc, int64_t lds,
                                 void* y, int32_t y_dtype, int64_t ldy,
                                 int64_t rows, int64_t K, hipStream_t stream);

@@ -624,3 +624,19 @@ def test_gated_projections_whose_sigmoid_is_subnormal(gate, scale):
     g = x[:, :32].double()
     within(dx[:, :32], wg, ref.HALF_BF16 * wg.abs() + 2 * ref.ACT_REL * wg.abs() + 2.0 ** -125 * scale * 2.0 ** 20, "dh gate")
     within(dx[:, I:I + 32], wu, ref.HALF_BF16 * wu.abs() + 2 * ref.ACT_REL * wu.abs() + 2.0 ** -127 * 2.0 ** 20, "dh up")
+
+
+@pytest.mark.parametrize("rows,K", [(1, 32), (1, 96), (3, 96), (5, 544)])
+def test_dequantize_scales_that_end_inside_a_word(rows, K):
+    """Dequantisation reads single scale bytes: the last row may end at its last
+    one.  The product reads words and refuses such scales."""
+    q, s = bi.bi_quantize_mxfp4(randn(gen(rows + K), (rows, K)))
+    pitch, kb = s.stride(0), K // 32
+    tight = torch.empty((rows - 1) * pitch + kb, dtype=torch.uint8, device="cuda")
+    st = tight.as_strided((rows, kb), (pitch, 1))
+    st.copy_(s)
+    for dt in (BF, torch.float32):
+        same(bi.bi_dequantize_mxfp4(q, st, dt), bi.bi_dequantize_mxfp4(q, s, dt))
+    wq, ws = bi.bi_quantize_mxfp4(randn(gen(1), (16, K)))
+    with pytest.raises(ValueError, match="32-bit words"):
+        bi.bi_linear_mxfp4(q, st, wq, ws)
