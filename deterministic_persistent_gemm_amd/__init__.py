@@ -514,7 +514,9 @@ def bi_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tenso
                        need_dw: bool = True, need_db: bool = True, dw_dtype: torch.dtype = torch.bfloat16):
     """Gradients of bi_linear_bf16: (dx [M, K] bf16, dw [N, K] of dw_dtype, db
     [N] fp32), each None if not wanted.  dy [M, N] bf16; x [M, K] is read for
-    dw only and wt = weight.t() [K, N] for dx only; either may be None."""
+    dw only and wt = weight.t() [K, N] for dx only; either may be None.  db's
+    order of addition depends on which outputs are wanted and on dw_dtype; the
+    same call repeats its bits."""
     name = "bi_linear_bf16_bwd"
     if dy.dim() != 2 or (need_dx and (wt is None or wt.dim() != 2)) or (need_dw and (x is None or x.dim() != 2)):
         raise ValueError(f"{name}: dy is [M, N]; dx needs wt [K, N] and dw needs x [M, K]")

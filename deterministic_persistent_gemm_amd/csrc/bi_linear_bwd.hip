@@ -19,7 +19,8 @@ static bool in_range(int64_t lddy, int64_t ldx, int64_t ldw, int64_t M, int64_t 
 
 // Column sums of dy where dw's tiles do not take them along (dw not wanted, or in
 // its largest tiles, whose matrix instructions leave no room: 221 us against 217
-// at 4096 x 4096 x 4096): a workgroup takes 64 columns and all rows; thread (row
+// at 4096 x 4096 x 4096), so db's order of addition follows from the launch: a
+// workgroup takes 64 columns and all rows; thread (row
 // lane, group of 8 columns) adds its rows in ascending order in fp32, and the 64
 // row lanes are added in order.  No split over rows, so nothing is left to fold.
 // 4096 x 4096 alone: 11 us, 3.4 TB/s (256 workgroups of 16 columns: the same).

@@ -231,7 +231,9 @@ bi_status_t bi_moe_grouped_gemm_ex(const uint16_t* x,
  * shape: one fp32 accumulator per output element threaded through all of k in
  * ascending order, by v_mfma_f32_16x16x32_bf16 on 32 k at a time (4-bit
  * operands: v_mfma_scale_f32_16x16x128_f8f6f4 on 128).  dw and db sum over the
- * batch, so their bits depend on M; they repeat exactly from run to run.
+ * batch, so their bits depend on M; they repeat exactly from run to run.  dw is
+ * one such accumulator over the batch; db has one of two orders of addition,
+ * taken from M, the widths, dw_dtype and which of the outputs are wanted.
  * All pointers are device pointers on the stream's device, 16-byte aligned
  * unless stated; row pitches are in elements (bytes for codes and scales);
  * outputs must not overlap inputs.  Rows past M and columns past the widths
