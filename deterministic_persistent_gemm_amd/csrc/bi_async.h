@@ -5,7 +5,7 @@
 // LDS byte address `lds` + i * (bytes per lane), with the wave's base in M0.
 // The loads are inline assembly so that the compiler does not order each
 // after the previous one (it would treat every load as an aliasing LDS write);
-// what a consumer needs is waited for explicitly with wait_vm / wait_later.
+// what a consumer needs is waited for explicitly with async_wait / async_wait_later.
 #pragma once
 
 #include <hip/hip_runtime.h>

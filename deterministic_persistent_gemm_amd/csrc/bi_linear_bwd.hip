@@ -67,8 +67,9 @@ __device__ __forceinline__ void colsum_body(const SumArgs& p, unsigned char* lds
 // a launch.  dx's four smallest stream (short batches: few tiles and a long sum
 // over N); the others load and compute in every wave.  16 x 32 is for the
 // longest sums on the fewest tiles, where a slice's time is the delivery of its
-// bytes to one compute unit: 30 rows, N 16928, K 992 take 45 us instead of 56 on
-// 32 x 32 tiles, 119 rows, N 6752, K 1792 35 instead of 27.
+// bytes to one compute unit: dx of 30 rows, N 16928, K 992 takes 45 us instead of
+// 56 on 32 x 32 tiles.  On more tiles it is the slower one (119 rows, N 6752, K
+// 1792: 35 us against 27), and the rule does not take it there.
 template <int SHAPE, bool CA> struct BwdShape;
 template <bool CA> struct BwdShape<0, CA> {
     using C = TileCfg<32, 32, 2, 2, 4, 4, CA, true, false, kEpiLinear>;
