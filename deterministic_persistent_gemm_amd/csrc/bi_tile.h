@@ -566,10 +566,11 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, const f32x4 (&acc)
                         gv[i] = pack_bf16(g0, g1);
                         uv[i] = pack_bf16(u0, u1);
                     }
-                    // past the caches: 1 to 8 percent at 4096 x 12288 down to k = 512
-                    // (the plain products' outputs lost up to 3 percent that way, fp32 ones 5)
-                    __builtin_nontemporal_store(
-                        yv, reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p.y) + (int64_t)m * p.ldy + n));
+                    // through the caches, also in large tiles: past them the call alone is up to 3
+                    // percent faster, but the down projection that reads y next pays more (both
+                    // calls, past / through: M 1000, H 1024, I 2048 33.4 / 29.4 us, M 1000, H 4096,
+                    // I 6144 211 / 197, M 4096, H 4096, I 12288 917 / 906)
+                    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p.y) + (int64_t)m * p.ldy + n) = yv;
                     if (p.h) {
                         *reinterpret_cast<u32x4*>(p.h + (int64_t)m * p.ldh + n) = gv;
                         *reinterpret_cast<u32x4*>(p.h + (int64_t)m * p.ldh + p.N + n) = uv;
