@@ -100,7 +100,8 @@ TileInfo gated_tile_info(int64_t M, int64_t I, int64_t H)
 // g^2 in z' is held below 1e30: s or 1 - s is exactly 0 long before, and zero
 // times an overflowed z' would be NaN.
 // dh is rounded to bf16 once: it is the matrix instructions' operand in both
-// products that follow.
+// products that follow, where a wider one would double their work (dx and dw are
+// off by 0.0023 of their size instead of the 0.0017 of their own rounding).
 __global__ __launch_bounds__(256) void k_gate_bwd(const uint16_t* __restrict__ dy, int64_t lddy,
                                                   const uint16_t* __restrict__ h, int64_t ldh, int gate,
                                                   uint16_t* __restrict__ dh, int64_t lddh, int64_t M, int I)

@@ -7,12 +7,20 @@
 //
 // with the two costs of one workgroup fitted to timings of 32 to 34 problems per
 // product, drawn over M 1 .. 4096, widths 128 .. 12288 and k 256 .. 4096, on an
-// MI355X (fit within 5 to 20 percent).  rounds: workgroups per compute unit,
+// MI355X (fit within 5 to 20 percent there).  rounds: workgroups per compute unit,
 // counted whole where a shape's LDS ring leaves room for one workgroup per
 // compute unit and as a fraction where several share it.  Over those problems
 // the shapes chosen this way come within 1 to 4 percent of the fastest of 6 to 14
 // shapes on average; always taking 64 x 64 costs 1.24 to 1.38 times the fastest,
 // always 128 x 128 1.40 to 1.70, always 256 x 256 2.0 to 3.4.
+//
+// What it does not hold for: contractions far past 4096, as dx has over wide
+// layers, are priced too low (290 rows, K 3296, contraction 16032 on 64 x 64 tiles:
+// 65 us estimated, 113 taken), and rows of a tile that lie past M count like others.
+// Costs refitted on contractions up to 24576 picked dx alone within 1.04 of the
+// fastest (1.11 with these) but changed passes with both products by -20 to +20
+// percent, so they are not used; the backward pass has two exceptions instead
+// (kNumDxApart and the streaming 64 x 64 tiles below 33 rows).
 #pragma once
 
 #include <stdint.h>
