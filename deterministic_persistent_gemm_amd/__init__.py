@@ -459,7 +459,8 @@ def bi_gated_linear_bf16(x: torch.Tensor, w13t: torch.Tensor, gate: int = BI_GAT
     """y = act(x @ wg) * (x @ wu) in one launch, batch-invariant.  x [M, H] bf16,
     w13t [H, 2I] = weight.t() of an nn.Linear weight whose rows are the gate
     projection, then the up projection.  Returns y [M, I] bf16, or (y, h) with
-    save_h: h [M, 2I] bf16, the projections the backward pass needs."""
+    save_h: h [M, 2I] bf16, the projections the backward pass needs.  out must
+    not overlap x or w13t."""
     name = "bi_gated_linear_bf16"
     if x.dim() != 2 or w13t.dim() != 2 or w13t.shape[1] % 2:
         raise ValueError(f"{name}: x is [M, H] and w13t is [H, 2I]")
@@ -594,7 +595,7 @@ def bi_linear_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: to
                     out: torch.Tensor | None = None) -> torch.Tensor:
     """y = x @ w.t() + bias of MXFP4 operands (bi_quantize_mxfp4 of x [M, K] and of
     an nn.Linear weight w [N, K]), fp32 accumulation, bf16 or fp32 out,
-    batch-invariant."""
+    batch-invariant.  out must not overlap an operand."""
     name = "bi_linear_mxfp4"
     code = _dtype_code(out_dtype if out is None else out.dtype, name, "out")
     dev = xq.get_device()

@@ -238,8 +238,10 @@ bi_status_t bi_moe_grouped_gemm_ex(const uint16_t* x,
  * unless stated; row pitches are in elements (bytes for codes and scales);
  * outputs must not overlap inputs.  Rows past M and columns past the widths
  * given are neither read nor written.  BI_EUNSUPPORTED: widths that are not the
- * multiples stated, pitches at which one tile's rows span 4 GiB, outputs of more
- * than 2^23 tiles.
+ * multiples stated, more than 2^30 rows, widths of 2^29 and more (I of the gated
+ * layer's backward pass: 2^28), pitches at which one tile's rows span 4 GiB (256
+ * rows; 32 of an operand whose rows are summed over; I + 256 of w13 in the gated
+ * layer), outputs of more than 2^23 tiles.  A refused call enqueues nothing.
  * ------------------------------------------------------------------------- */
 
 typedef enum {
