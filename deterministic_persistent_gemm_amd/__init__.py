@@ -80,17 +80,29 @@ _lib.bi_quantize_mxfp4.argtypes = [_P, _I32, _I64, _P, _I64, _P, _I64, _I64, _I6
 _lib.bi_dequantize_mxfp4.argtypes = [_P, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64, _P]
 _lib.bi_linear_mxfp4.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I32, _I64, _I64, _I64, _I64, _P]
 _lib.bi_gated_linear_bwd_workspace_size.argtypes = [_I64, _I64]
+_lib.bi_layer_norm.argtypes = [_P, _I32, _I64, _P, _P, ctypes.c_float, _P, _I32, _I64, _P, _P, _I64, _I64, _P]
+_lib.bi_layer_norm_bwd.argtypes = [_P, _I32, _I64, _P, _I32, _I64, _P, _P, _P, _P, _I64, _P, _P, _I64, _I64, _P, _SZ, _P]
+_lib.bi_layer_norm_bwd_workspace_size.argtypes = [_I64, _I64]
+_lib.bi_grouped_linear_bf16.argtypes = [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64, _I64, _P]
+_lib.bi_grouped_linear_bf16_bwd.argtypes = [_P, _I64, _P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _I64,
+                                            _I64, _I64, _I64, _P]
+_lib.bi_quantize_int8.argtypes = [_P, _I32, _I64, _P, _I64, _P, _I64, _I64, _P]
+_lib.bi_linear_int8.argtypes = [_P, _I64, _P, _P, _I64, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P]
+_lib.bi_grouped_linear_int8.argtypes = [_P, _I64, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64, _I64, _P]
+_lib.bi_lab_grouped_tile.argtypes = [_I32, _I64, _I64, _I64, _I64, _I32, ctypes.POINTER(_I32)]
 for _f in (_lib.bi_linear_f32, _lib.bi_linear_bf16, _lib.bi_negctl_linear_f32, _lib.bi_lab_linear,
            _lib.bi_gated_linear_bf16, _lib.bi_gated_linear_bf16_bwd, _lib.bi_linear_bf16_bwd,
            _lib.bi_quantize_mxfp4, _lib.bi_dequantize_mxfp4, _lib.bi_linear_mxfp4,
            _lib.bi_moe_grouped_gemm, _lib.bi_describe_recipe, _lib.bi_indexer_topk,
            _lib.bi_moe_grouped_gemm_ex, _lib.bi_lab_xcc_ids, _lib.bi_lab_empty, _lib.bi_lab_stream_read,
            _lib.bi_lab_clock, _lib.bi_lab_plan, _lib.bi_lab_moe_layout, _lib.bi_lab_ffn_tile,
-           _lib.bi_linear_f32_noalloc,
+           _lib.bi_linear_f32_noalloc, _lib.bi_layer_norm, _lib.bi_layer_norm_bwd, _lib.bi_grouped_linear_bf16,
+           _lib.bi_grouped_linear_bf16_bwd, _lib.bi_quantize_int8, _lib.bi_linear_int8, _lib.bi_grouped_linear_int8,
+           _lib.bi_lab_grouped_tile,
            _lib.bi_lab_lds_read, _lib.bi_lab_mfma_rate, _lib.bi_lab_l2_read):
     _f.restype = _I32
 for _f in (_lib.bi_linear_workspace_size, _lib.bi_lab_workspace_size, _lib.bi_moe_workspace_size,
-           _lib.bi_gated_linear_bwd_workspace_size):
+           _lib.bi_gated_linear_bwd_workspace_size, _lib.bi_layer_norm_bwd_workspace_size):
     _f.restype = _SZ
 _lib.bi_status_str.restype = ctypes.c_char_p
 
@@ -385,7 +397,7 @@ def bi_indexer_topk(scores, topk: int, row_start=None, row_end=None, out=None):
 BI_GATE_SILU, BI_GATE_GELU_TANH = 0, 1
 
 
-_ELEM = {torch.bfloat16: 2, torch.float32: 4, torch.uint8: 1}
+_ELEM = {torch.bfloat16: 2, torch.float32: 4, torch.uint8: 1, torch.int8: 1}
 
 
 def _rows(t, dtype, rows, cols, dev, name, what, align=16, transposed=False):
@@ -614,6 +626,237 @@ def bi_linear_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: to
     return out
 
 
+# -------------------------- experts as operators of their own, layer norm, int8
+
+
+def _vector(t, dtype, n, dev, name, what, align=16):
+    """A contiguous vector of n elements on GPU `dev` (None passes)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {what} must be {dtype}, got {t.dtype}")
+    if t.shape != (n,) or not t.is_contiguous() or dev < 0 or t.get_device() != dev or t.data_ptr() % align:
+        raise ValueError(f"{name}: {what} must be a contiguous, {align}-byte aligned [{n}] tensor on the other tensors' GPU")
+
+
+def _norm_sizes(name, H):
+    if H == 0 or H % 8 or H > 16384:
+        raise ValueError(f"{name}: needs rows of a multiple of 8 values, at most 16384, got {H}")
+
+
+def bi_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, eps: float = 1e-5,
+                  out_dtype: torch.dtype | None = None, save_stats: bool = False, out: torch.Tensor | None = None):
+    """y = (x - mean) * rstd * weight + bias over the rows of x [M, H] (bf16 or
+    fp32), rstd = 1 / sqrt(var + eps), batch-invariant.  weight, bias: fp32 [H] or
+    None.  y is of out_dtype (x's if None).  Returns y, or (y, mean, rstd) with
+    save_stats: fp32 [M], what the backward pass needs.  out may be x itself
+    where their types agree, else it must not overlap x."""
+    name = "bi_layer_norm"
+    if x.dim() != 2:
+        raise ValueError(f"{name}: x is [M, H]")
+    M, H = x.shape
+    xcode = _dtype_code(x.dtype, name, "x")
+    ydt = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
+    ycode = _dtype_code(ydt, name, "out")
+    _norm_sizes(name, H)
+    dev = x.get_device()
+    ldx = _rows(x, x.dtype, M, H, dev, name, "x")
+    _vector(weight, torch.float32, H, dev, name, "weight")
+    _vector(bias, torch.float32, H, dev, name, "bias")
+    if out is None:
+        out, ldy = x.new_empty(M, H, dtype=ydt), H
+    else:
+        ldy = _rows(out, ydt, M, H, dev, name, "out")
+    mean = rstd = None
+    if save_stats:
+        mean, rstd = x.new_empty(M, dtype=torch.float32), x.new_empty(M, dtype=torch.float32)
+    _call(_lib.bi_layer_norm, name, dev, x.data_ptr(), xcode, ldx, _dp(weight), _dp(bias), eps, out.data_ptr(), ycode, ldy,
+          _dp(mean), _dp(rstd), M, H)
+    return (out, mean, rstd) if save_stats else out
+
+
+def bi_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                      weight: torch.Tensor | None = None, need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
+                      ws: torch.Tensor | None = None):
+    """Gradients of bi_layer_norm at the statistics its forward pass kept: (dx
+    [M, H] of x's type, dw [H] fp32, db [H] fp32), each None if not wanted.  dy
+    [M, H]: bf16 or fp32."""
+    name = "bi_layer_norm_bwd"
+    if dy.dim() != 2:
+        raise ValueError(f"{name}: dy is [M, H]")
+    M, H = dy.shape
+    dcode, xcode = _dtype_code(dy.dtype, name, "dy"), _dtype_code(x.dtype, name, "x")
+    _norm_sizes(name, H)
+    dev = dy.get_device()
+    lddy = _rows(dy, dy.dtype, M, H, dev, name, "dy")
+    ldx = _rows(x, x.dtype, M, H, dev, name, "x")
+    _vector(mean, torch.float32, M, dev, name, "mean", 4)
+    _vector(rstd, torch.float32, M, dev, name, "rstd", 4)
+    _vector(weight, torch.float32, H, dev, name, "weight")
+    dx = x.new_empty(M, H) if need_dx else None
+    dw = x.new_empty(H, dtype=torch.float32) if need_dw else None
+    db = x.new_empty(H, dtype=torch.float32) if need_db else None
+    ws = _scratch(_lib.bi_layer_norm_bwd_workspace_size(M, H) if need_dw or need_db else 0, dy.device, ws, name)
+    _call(_lib.bi_layer_norm_bwd, name, dev, dy.data_ptr(), dcode, lddy, x.data_ptr(), xcode, ldx, mean.data_ptr(),
+          rstd.data_ptr(), _dp(weight), _dp(dx), H, _dp(dw), _dp(db), M, H, _dp(ws), 0 if ws is None else ws.numel())
+    return dx, dw, db
+
+
+def _experts(w, dtype, E, N, K, dev, name, what):
+    """Row pitch and expert stride (elements) of weights [E, N, K]."""
+    if w.dim() != 3 or w.shape != (E, N, K):
+        raise ValueError(f"{name}: {what} must have shape {(E, N, K)}, got {tuple(w.shape)}")
+    ldw = _rows(w[0], dtype, N, K, dev, name, what)
+    step = w.stride(0) if E > 1 else 0
+    if step < 0 or step * _ELEM[dtype] % 16:
+        raise ValueError(f"{name}: {what}'s experts must lie a multiple of 16 bytes apart; its strides are {w.stride()}")
+    return ldw, step
+
+
+def _grouped_sizes(name, w, what):
+    if w.dim() != 3:
+        raise ValueError(f"{name}: {what} is [E, N, K]")
+    E, N, K = w.shape
+    if E == 0 or E > 1024:
+        raise ValueError(f"{name}: needs 1 to 1024 experts, got {E}")
+    _sizes(name, N, K)
+    return E, N, K
+
+
+def bi_grouped_linear_bf16(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16,
+                           out: torch.Tensor | None = None) -> torch.Tensor:
+    """y[t] = x[t] @ w[e].t() for the expert e of row t, batch-invariant.  x [T, K]
+    bf16, rows sorted by expert: e's are ends[e-1] .. ends[e] - 1.  w [E, N, K]
+    bf16 (each expert an nn.Linear weight), ends [E] int64 on the GPU, ascending
+    (torch.cumsum of the experts' row counts).  Rows from ends[-1] on are not
+    written: in a y made here they hold anything, in `out` what they held."""
+    name = "bi_grouped_linear_bf16"
+    if x.dim() != 2:
+        raise ValueError(f"{name}: x is [T, K]")
+    E, N, K = _grouped_sizes(name, w, "w")
+    T = x.shape[0]
+    dev = x.get_device()
+    ldx = _rows(x, torch.bfloat16, T, K, dev, name, "x")
+    ldw, step = _experts(w, torch.bfloat16, E, N, K, dev, name, "w")
+    _vector(ends, torch.int64, E, dev, name, "ends", 8)
+    code = _dtype_code(out_dtype if out is None else out.dtype, name, "out")
+    if out is None:
+        out, ldy = x.new_empty(T, N, dtype=out_dtype), N
+    else:
+        ldy = _rows(out, out.dtype, T, N, dev, name, "out")
+    _call(_lib.bi_grouped_linear_bf16, name, dev, x.data_ptr(), ldx, w.data_ptr(), ldw, step, ends.data_ptr(), E, out.data_ptr(),
+          code, ldy, T, N, K)
+    return out
+
+
+def bi_grouped_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | None, ends: torch.Tensor,
+                               need_dx: bool = True, need_dw: bool = True, dw_dtype: torch.dtype = torch.bfloat16,
+                               out_dx: torch.Tensor | None = None):
+    """Gradients of bi_grouped_linear_bf16: (dx [T, K] bf16 or None, dw [E, N, K]
+    of dw_dtype or None; dw is zero for an expert without rows).  dy [T, N] bf16;
+    x is read for dw only and w for dx only; the other may be None.  Rows of
+    dx from ends[-1] on are not written (out_dx: a dx of the caller's)."""
+    name = "bi_grouped_linear_bf16_bwd"
+    if dy.dim() != 2 or (need_dx and (w is None or w.dim() != 3)) or (need_dw and (x is None or x.dim() != 2)):
+        raise ValueError(f"{name}: dy is [T, N]; dx needs w [E, N, K] and dw needs x [T, K]")
+    T, N = dy.shape
+    E = ends.shape[0] if ends.dim() == 1 else 0
+    K = w.shape[2] if need_dx else x.shape[1] if need_dw else 32
+    if E == 0 or E > 1024:
+        raise ValueError(f"{name}: ends is [E], for 1 to 1024 experts")
+    code = _dtype_code(dw_dtype, name, "dw_dtype")
+    _sizes(name, N, K)
+    dev = dy.get_device()
+    lddy = _rows(dy, torch.bfloat16, T, N, dev, name, "dy")
+    _vector(ends, torch.int64, E, dev, name, "ends", 8)
+    dx = dw = None
+    ldx = ldw = step = lddx = 0
+    if need_dx:
+        ldw, step = _experts(w, torch.bfloat16, E, N, K, dev, name, "w")
+        dx = dy.new_empty(T, K) if out_dx is None else out_dx
+        lddx = _rows(dx, torch.bfloat16, T, K, dev, name, "out_dx")
+    if need_dw:
+        ldx = _rows(x, torch.bfloat16, T, K, dev, name, "x")
+        dw = dy.new_empty(E, N, K, dtype=dw_dtype)
+    _call(_lib.bi_grouped_linear_bf16_bwd, name, dev, dy.data_ptr(), lddy, _dp(x) if need_dw else None, ldx,
+          _dp(w) if need_dx else None, ldw, step, ends.data_ptr(), E, _dp(dx), lddx, _dp(dw), code, K, N * K, T, N, K)
+    return dx, dw
+
+
+def bi_quantize_int8(x: torch.Tensor):
+    """Rows of x [rows, K] (bf16 or fp32) as 8-bit integers: (codes int8 [rows, K] in
+    [-127, 127], scales fp32 [rows]), x = codes * scale up to rounding."""
+    name = "bi_quantize_int8"
+    code = _dtype_code(x.dtype, name, "x")
+    if x.dim() != 2:
+        raise ValueError(f"{name}: x is [rows, K]")
+    rows, K = x.shape
+    _sizes(name, 16, K)
+    dev = x.get_device()
+    ldx = _rows(x, x.dtype, rows, K, dev, name, "x")
+    q, s = x.new_empty(rows, K, dtype=torch.int8), x.new_empty(rows, dtype=torch.float32)
+    _call(_lib.bi_quantize_int8, name, dev, x.data_ptr(), code, ldx, q.data_ptr(), K, s.data_ptr(), rows, K)
+    return q, s
+
+
+def _int8_sizes(name, N, K):
+    _sizes(name, N, K)
+    if K > 131040:
+        raise ValueError(f"{name}: k of {K} could overflow 32-bit sums; at most 131040")
+
+
+def bi_linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, bias: torch.Tensor | None = None,
+                   out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """y = (xq @ wq.t()) * xs[:, None] * ws + bias of 8-bit codes xq [M, K] and wq
+    [N, K] (bi_quantize_int8 of activations and of an nn.Linear weight), sums
+    exact in 32-bit integers, bf16 or fp32 out, batch-invariant."""
+    name = "bi_linear_int8"
+    if xq.dim() != 2 or wq.dim() != 2:
+        raise ValueError(f"{name}: xq is [M, K] and wq is [N, K]")
+    code = _dtype_code(out_dtype if out is None else out.dtype, name, "out")
+    (M, K), N = xq.shape, wq.shape[0]
+    _int8_sizes(name, N, K)
+    dev = xq.get_device()
+    ldx = _rows(xq, torch.int8, M, K, dev, name, "xq")
+    ldw = _rows(wq, torch.int8, N, K, dev, name, "wq")
+    _vector(xs, torch.float32, M, dev, name, "xs", 4)
+    _vector(ws, torch.float32, N, dev, name, "ws")
+    _vector(bias, torch.float32, N, dev, name, "bias")
+    if out is None:
+        out, ldy = xq.new_empty(M, N, dtype=out_dtype), N
+    else:
+        ldy = _rows(out, out.dtype, M, N, dev, name, "out")
+    _call(_lib.bi_linear_int8, name, dev, xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), _dp(bias),
+          out.data_ptr(), code, ldy, M, N, K)
+    return out
+
+
+def bi_grouped_linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, ends: torch.Tensor,
+                           out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """bi_linear_int8 with each row's own expert: xq [T, K] and xs [T] sorted by
+    expert, wq [E, N, K], ws [E, N], ends as for bi_grouped_linear_bf16."""
+    name = "bi_grouped_linear_int8"
+    if xq.dim() != 2:
+        raise ValueError(f"{name}: xq is [T, K]")
+    E, N, K = _grouped_sizes(name, wq, "wq")
+    _int8_sizes(name, N, K)
+    T = xq.shape[0]
+    dev = xq.get_device()
+    ldx = _rows(xq, torch.int8, T, K, dev, name, "xq")
+    ldw, step = _experts(wq, torch.int8, E, N, K, dev, name, "wq")
+    _vector(xs, torch.float32, T, dev, name, "xs", 4)
+    lds = _rows(ws, torch.float32, E, N, dev, name, "ws")
+    _vector(ends, torch.int64, E, dev, name, "ends", 8)
+    code = _dtype_code(out_dtype if out is None else out.dtype, name, "out")
+    if out is None:
+        out, ldy = xq.new_empty(T, N, dtype=out_dtype), N
+    else:
+        ldy = _rows(out, out.dtype, T, N, dev, name, "out")
+    _call(_lib.bi_grouped_linear_int8, name, dev, xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, step, ws.data_ptr(),
+          lds if E > 1 else 0, ends.data_ptr(), E, out.data_ptr(), code, ldy, T, N, K)
+    return out
+
+
 def bi_lab_xcc_ids(grid_x: int, grid_y: int = 1, device=None) -> torch.Tensor:
     """XCD id each workgroup of a grid_x x grid_y grid ran on (int64 [grid_y, grid_x])."""
     device = torch.device(device or "cuda")
@@ -638,14 +881,23 @@ def moe_layout(M: int, H: int, E: int, I: int, topk: int) -> dict:
     return {"sorted": out[0], "act": out[1], "part": out[2], "total": out[3]}
 
 
-BI_FFN_GATED, BI_FFN_MXFP4, BI_FFN_DX, BI_FFN_DW = 0, 1, 2, 3
+BI_FFN_GATED, BI_FFN_MXFP4, BI_FFN_DX, BI_FFN_DW, BI_FFN_INT8 = 0, 1, 2, 3, 4
+BI_GROUPED_BF16, BI_GROUPED_INT8, BI_GROUPED_DX, BI_GROUPED_DW = 0, 1, 2, 3
+_TILE_FIELDS = ("shape", "kernel", "rows", "cols", "slice_k", "stage_slices", "ring_stages", "scale_groups")
 
 
 def ffn_tile(op: int, M: int, N: int, K: int, out_dtype: int = BI_BF16) -> dict:
     """The tile shape a feed-forward product of this size takes (bi_lab_ffn_tile)."""
     out = (_I32 * 8)()
     _check(_lib.bi_lab_ffn_tile(op, M, N, K, out_dtype, out), "bi_lab_ffn_tile")
-    return dict(zip(("shape", "kernel", "rows", "cols", "slice_k", "stage_slices", "ring_stages", "scale_groups"), out))
+    return dict(zip(_TILE_FIELDS, out))
+
+
+def grouped_tile(op: int, T: int, E: int, N: int, K: int, out_dtype: int = BI_BF16) -> dict:
+    """The tile shape a product grouped by expert takes (bi_lab_grouped_tile)."""
+    out = (_I32 * 8)()
+    _check(_lib.bi_lab_grouped_tile(op, T, E, N, K, out_dtype, out), "bi_lab_grouped_tile")
+    return dict(zip(_TILE_FIELDS, out))
 
 
 def bi_lab_empty(grid: int, threads: int = 64):

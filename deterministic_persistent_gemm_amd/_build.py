@@ -23,7 +23,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["bi_abi.cpp", "bi_plan.cpp", "bi_linear.hip", "bi_moe.hip", "bi_topk.hip", "bi_lab.hip",
-           "bi_noalloc.hip", "bi_gated.hip", "bi_linear_bwd.hip", "bi_mx.hip"]
+           "bi_noalloc.hip", "bi_gated.hip", "bi_linear_bwd.hip", "bi_mx.hip", "bi_int8.hip", "bi_grouped.hip",
+           "bi_norm.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", "-Wno-unused-function",
           "-I", INCLUDE, "-I", CSRC]

@@ -95,6 +95,29 @@ bi_status_t launch_status(hipError_t e)
     return e == hipSuccess ? BI_OK : e == hipErrorInvalidConfiguration ? BI_EUNSUPPORTED : BI_EHIP;
 }
 
+// A vector of floats, and an 8-bit operand's codes.
+bool floats_ok(const void* p, uintptr_t align) { return p && (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0; }
+bool codes_ok(const int8_t* q, int64_t ldq, int64_t K) { return matrix_ok(q, ldq, K, 1); }
+
+// Experts' sizes; rows may be 0.
+bi_status_t check_grouped(int64_t T, int64_t N, int64_t K, int64_t E)
+{
+    if (E < 0)
+        return BI_EINVAL;
+    const bi_status_t st = check_sizes(T, N, K);
+    return st != BI_OK ? st : E == 0 || E > kMaxExperts ? BI_EUNSUPPORTED : BI_OK;
+}
+
+// The step from expert to expert, in elements: 0 or more, whole 16-byte units.
+bool stride_ok(int64_t stride, int elem) { return stride >= 0 && stride < (int64_t(1) << 40) && (stride * elem) % 16 == 0; }
+
+bi_status_t check_norm(int64_t M, int64_t H, int32_t a_dtype, int32_t b_dtype)
+{
+    if (M < 0 || H < 0 || !dtype_ok(a_dtype) || !dtype_ok(b_dtype))
+        return BI_EINVAL;
+    return H == 0 || H % 8 != 0 || H > kNormMaxH || M > (int64_t(1) << 30) ? BI_EUNSUPPORTED : BI_OK;
+}
+
 size_t dh_bytes(int64_t M, int64_t I) { return (size_t)M * 2 * (size_t)I * 2; }
 
 // The gradients of an empty batch: zero dw and db.
@@ -500,16 +523,172 @@ bi_status_t bi_linear_mxfp4(const uint8_t* xq, int64_t ldxq, const uint8_t* xs, 
                                           K, stream));
 }
 
+bi_status_t bi_layer_norm(const void* x, int32_t x_dtype, int64_t ldx, const float* w, const float* b, float eps, void* y,
+                          int32_t y_dtype, int64_t ldy, float* mean, float* rstd, int64_t M, int64_t H, hipStream_t stream)
+{
+    const bi_status_t st = check_norm(M, H, x_dtype, y_dtype);
+    if (st != BI_OK)
+        return st;
+    if (!(eps >= 0.f) || eps > 3.4028234e38f)
+        return BI_EINVAL;
+    if (M == 0)
+        return BI_OK;
+    if (!matrix_ok(x, ldx, H, dtype_bytes(x_dtype)) || !matrix_ok(y, ldy, H, dtype_bytes(y_dtype)) ||
+        (w && !aligned16(w)) || (b && !aligned16(b)) || (mean && !floats_ok(mean, 4)) || (rstd && !floats_ok(rstd, 4)))
+        return BI_EINVAL;
+    return launch_layer_norm(x, x_dtype == BI_BF16, ldx, w, b, eps, y, y_dtype == BI_BF16, ldy, mean, rstd, M, H, stream) ==
+                   hipSuccess
+               ? BI_OK
+               : BI_EHIP;
+}
+
+size_t bi_layer_norm_bwd_workspace_size(int64_t M, int64_t H)
+{
+    if (check_norm(M, H, BI_F32, BI_F32) != BI_OK || M == 0)
+        return 0;
+    return kDecodeCounterBytes + layer_norm_bwd_ws(M, H);
+}
+
+bi_status_t bi_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t lddy, const void* x, int32_t x_dtype, int64_t ldx,
+                              const float* mean, const float* rstd, const float* w, void* dx, int64_t lddx, float* dw, float* db,
+                              int64_t M, int64_t H, void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    const bi_status_t st = check_norm(M, H, dy_dtype, x_dtype);
+    if (st != BI_OK || (!dx && !dw && !db))
+        return st;
+    if ((dw && !aligned16(dw)) || (db && !aligned16(db)))
+        return BI_EINVAL;
+    if (M == 0) {
+        for (float* p : {dw, db})
+            if (p && launch_zero_rows(p, H * 4, 1, H * 4, stream) != hipSuccess)
+                return BI_EHIP;
+        return BI_OK;
+    }
+    const int xe = dtype_bytes(x_dtype);
+    if (!matrix_ok(dy, lddy, H, dtype_bytes(dy_dtype)) || !matrix_ok(x, ldx, H, xe) || !floats_ok(mean, 4) ||
+        !floats_ok(rstd, 4) || (w && !aligned16(w)) || (dx && !matrix_ok(dx, lddx, H, xe)))
+        return BI_EINVAL;
+    if ((dw || db) && (!ws || !aligned16(ws) || ws_bytes < bi_layer_norm_bwd_workspace_size(M, H)))
+        return BI_EWORKSPACE;
+    return launch_layer_norm_bwd(dy, dy_dtype == BI_BF16, lddy, x, x_dtype == BI_BF16, ldx, mean, rstd, w, dx, lddx, dw, db, M, H,
+                                 reinterpret_cast<char*>(ws) + kDecodeCounterBytes, stream) == hipSuccess
+               ? BI_OK
+               : BI_EHIP;
+}
+
+bi_status_t bi_grouped_linear_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, int64_t stride_w,
+                                   const int64_t* ends, int64_t E, void* y, int32_t y_dtype, int64_t ldy, int64_t T, int64_t N,
+                                   int64_t K, hipStream_t stream)
+{
+    if (!dtype_ok(y_dtype))
+        return BI_EINVAL;
+    const bi_status_t st = check_grouped(T, N, K, E);
+    if (st != BI_OK || T == 0)
+        return st;
+    if (!matrix_ok(x, ldx, K, 2) || !matrix_ok(w, ldw, K, 2) || !stride_ok(stride_w, 2) || !floats_ok(ends, 8) ||
+        !matrix_ok(y, ldy, N, dtype_bytes(y_dtype)))
+        return BI_EINVAL;
+    if (!grouped_fits(ldx, ldw, 2, T, N, K, E))
+        return BI_EUNSUPPORTED;
+    return launch_status(launch_grouped_bf16(x, ldx, w, ldw, stride_w, ends, E, y, y_dtype == BI_BF16, ldy, T, N, K, stream));
+}
+
+bi_status_t bi_grouped_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w,
+                                       int64_t ldw, int64_t stride_w, const int64_t* ends, int64_t E, uint16_t* dx, int64_t lddx,
+                                       void* dw, int32_t dw_dtype, int64_t lddw, int64_t stride_dw, int64_t T, int64_t N,
+                                       int64_t K, hipStream_t stream)
+{
+    if (!dtype_ok(dw_dtype))
+        return BI_EINVAL;
+    const bi_status_t st = check_grouped(T, N, K, E);
+    if (st != BI_OK || (!dx && !dw) || (T == 0 && !dw))
+        return st;
+    if (!floats_ok(ends, 8))
+        return BI_EINVAL;
+    if (dw && (!matrix_ok(dw, lddw, K, dtype_bytes(dw_dtype)) || !stride_ok(stride_dw, dtype_bytes(dw_dtype)) ||
+               (E > 1 && stride_dw < (N - 1) * lddw + K)))
+        return BI_EINVAL;
+    if (T > 0 && (!matrix_ok(dy, lddy, N, 2) || (dx && (!matrix_ok(dx, lddx, K, 2) || !matrix_ok(w, ldw, K, 2) ||
+                                                        !stride_ok(stride_w, 2))) ||
+                  (dw && !matrix_ok(x, ldx, K, 2))))
+        return BI_EINVAL;
+    if (!grouped_bwd_fits(T > 0 ? lddy : 0, T > 0 && dw ? ldx : 0, T > 0 && dx ? ldw : 0, T, N, K, E))
+        return BI_EUNSUPPORTED;
+    return launch_status(launch_grouped_bwd(dy, lddy, x, ldx, w, ldw, stride_w, ends, E, dx, lddx, dw, dw_dtype == BI_BF16, lddw,
+                                            stride_dw, T, N, K, stream));
+}
+
+bi_status_t bi_quantize_int8(const void* x, int32_t x_dtype, int64_t ldx, int8_t* q, int64_t ldq, float* s, int64_t rows,
+                             int64_t K, hipStream_t stream)
+{
+    if (!dtype_ok(x_dtype))
+        return BI_EINVAL;
+    const bi_status_t st = check_sizes(rows, 16, K);
+    if (st != BI_OK || rows == 0)
+        return st;
+    if (!matrix_ok(x, ldx, K, dtype_bytes(x_dtype)) || !codes_ok(q, ldq, K) || !floats_ok(s, 4))
+        return BI_EINVAL;
+    return launch_quantize_int8(x, x_dtype == BI_BF16, ldx, q, ldq, s, rows, K, stream) == hipSuccess ? BI_OK : BI_EHIP;
+}
+
+bi_status_t bi_linear_int8(const int8_t* xq, int64_t ldxq, const float* xs, const int8_t* wq, int64_t ldwq, const float* ws,
+                           const float* bias, void* y, int32_t y_dtype, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                           hipStream_t stream)
+{
+    if (!dtype_ok(y_dtype))
+        return BI_EINVAL;
+    const bi_status_t st = check_sizes(M, N, K);
+    if (st != BI_OK || M == 0)
+        return st;
+    if (!codes_ok(xq, ldxq, K) || !codes_ok(wq, ldwq, K) || !floats_ok(xs, 4) || !floats_ok(ws, 16) || (bias && !aligned16(bias)) ||
+        !matrix_ok(y, ldy, N, dtype_bytes(y_dtype)))
+        return BI_EINVAL;
+    if (!int8_fits(ldxq, ldwq, M, N, K))
+        return BI_EUNSUPPORTED;
+    return launch_status(launch_int8_linear(xq, ldxq, xs, wq, ldwq, ws, bias, y, y_dtype == BI_BF16, ldy, M, N, K, stream));
+}
+
+bi_status_t bi_grouped_linear_int8(const int8_t* xq, int64_t ldxq, const float* xs, const int8_t* wq, int64_t ldwq,
+                                   int64_t stride_wq, const float* ws, int64_t stride_ws, const int64_t* ends, int64_t E, void* y,
+                                   int32_t y_dtype, int64_t ldy, int64_t T, int64_t N, int64_t K, hipStream_t stream)
+{
+    if (!dtype_ok(y_dtype))
+        return BI_EINVAL;
+    const bi_status_t st = check_grouped(T, N, K, E);
+    if (st != BI_OK || T == 0)
+        return st;
+    if (!codes_ok(xq, ldxq, K) || !codes_ok(wq, ldwq, K) || !stride_ok(stride_wq, 1) || !floats_ok(xs, 4) || !floats_ok(ws, 16) ||
+        !stride_ok(stride_ws, 4) || !floats_ok(ends, 8) || !matrix_ok(y, ldy, N, dtype_bytes(y_dtype)))
+        return BI_EINVAL;
+    if (!grouped_fits(ldxq, ldwq, 1, T, N, K, E))
+        return BI_EUNSUPPORTED;
+    return launch_status(launch_grouped_int8(xq, ldxq, xs, wq, ldwq, stride_wq, ws, stride_ws, ends, E, y, y_dtype == BI_BF16, ldy, T,
+                                             N, K, stream));
+}
+
 bi_status_t bi_lab_ffn_tile(int32_t op, int64_t M, int64_t N, int64_t K, int32_t out_dtype, int32_t* info)
 {
-    if (op < BI_FFN_GATED || op > BI_FFN_DW || !dtype_ok(out_dtype) || M <= 0 || !info)
+    if (op < BI_FFN_GATED || op > BI_FFN_INT8 || !dtype_ok(out_dtype) || M <= 0 || !info)
         return BI_EINVAL;
     const bi_status_t st = check_sizes(M, N, K);
     if (st != BI_OK)
         return st;
     const int bf16 = out_dtype == BI_BF16;
     const TileInfo t = op == BI_FFN_GATED ? gated_tile_info(M, N, K) : op == BI_FFN_MXFP4 ? mx_tile_info(M, N, K, bf16)
+                       : op == BI_FFN_INT8 ? int8_tile_info(M, N, K, bf16)
                        : linear_bwd_tile_info(op == BI_FFN_DW, bf16, M, N, K);
+    memcpy(info, &t, sizeof t);
+    return BI_OK;
+}
+
+bi_status_t bi_lab_grouped_tile(int32_t op, int64_t T, int64_t E, int64_t N, int64_t K, int32_t out_dtype, int32_t* info)
+{
+    if (op < BI_GROUPED_BF16 || op > BI_GROUPED_DW || !dtype_ok(out_dtype) || T <= 0 || !info)
+        return BI_EINVAL;
+    const bi_status_t st = check_grouped(T, N, K, E);
+    if (st != BI_OK)
+        return st;
+    const TileInfo t = grouped_tile_info(op, T, E, N, K, out_dtype == BI_BF16);
     memcpy(info, &t, sizeof t);
     return BI_OK;
 }

@@ -1,5 +1,6 @@
 // bi_ffn.h -- launchers of the feed-forward operators (host side): the gated
-// linear layer, the backward passes, 4-bit quantisation and the 4-bit product.
+// linear layer, the backward passes, 4- and 8-bit quantisation and products, the
+// products grouped by expert, and the layer norm in front of them.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -58,5 +59,41 @@ hipError_t launch_mx_linear(const uint8_t* xq, int64_t ldx, const uint8_t* xs, i
                             int64_t ldw, const uint8_t* wsc, int64_t ldws, const float* bias, void* y, int y_bf16,
                             int64_t ldy, int64_t M, int64_t N, int64_t K, hipStream_t s);
 TileInfo mx_tile_info(int64_t M, int64_t N, int64_t K, int y_bf16);
+
+// bi_int8.hip
+// 128 * 128 * K stays below 2^31: no sum of code products overflows
+constexpr int64_t kInt8MaxK = 131040;
+hipError_t launch_quantize_int8(const void* x, int x_bf16, int64_t ldx, int8_t* q, int64_t ldq, float* sc, int64_t rows,
+                                int64_t K, hipStream_t s);
+bool int8_fits(int64_t ldx, int64_t ldw, int64_t M, int64_t N, int64_t K);
+hipError_t launch_int8_linear(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw, const float* ws,
+                              const float* bias, void* y, int y_bf16, int64_t ldy, int64_t M, int64_t N, int64_t K, hipStream_t s);
+TileInfo int8_tile_info(int64_t M, int64_t N, int64_t K, int y_bf16);
+
+// bi_grouped.hip
+constexpr int64_t kMaxExperts = 1024;
+// es: bytes of an operand's element
+bool grouped_fits(int64_t lda, int64_t ldw, int es, int64_t T, int64_t N, int64_t K, int64_t E);
+bool grouped_bwd_fits(int64_t lddy, int64_t ldx, int64_t ldw, int64_t T, int64_t N, int64_t K, int64_t E);
+hipError_t launch_grouped_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, int64_t stride_w,
+                               const int64_t* ends, int64_t E, void* y, int y_bf16, int64_t ldy, int64_t T, int64_t N, int64_t K,
+                               hipStream_t s);
+hipError_t launch_grouped_int8(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw, int64_t stride_w,
+                               const float* ws, int64_t stride_ws, const int64_t* ends, int64_t E, void* y, int y_bf16,
+                               int64_t ldy, int64_t T, int64_t N, int64_t K, hipStream_t s);
+hipError_t launch_grouped_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
+                              int64_t stride_w, const int64_t* ends, int64_t E, uint16_t* dx, int64_t lddx, void* dw, int dw_bf16,
+                              int64_t lddw, int64_t stride_dw, int64_t T, int64_t N, int64_t K, hipStream_t s);
+// op: bi_grouped_op_t
+TileInfo grouped_tile_info(int op, int64_t T, int64_t E, int64_t N, int64_t K, int out_bf16);
+
+// bi_norm.hip
+constexpr int64_t kNormMaxH = 16384;
+hipError_t launch_layer_norm(const void* x, int x_bf16, int64_t ldx, const float* w, const float* b, float eps, void* y, int y_bf16,
+                             int64_t ldy, float* mean, float* rstd, int64_t M, int64_t H, hipStream_t s);
+size_t layer_norm_bwd_ws(int64_t M, int64_t H);
+hipError_t launch_layer_norm_bwd(const void* dy, int dy_bf16, int64_t lddy, const void* x, int x_bf16, int64_t ldx,
+                                 const float* mean, const float* rstd, const float* w, void* dx, int64_t lddx, float* dw, float* db,
+                                 int64_t M, int64_t H, void* ws, hipStream_t s);
 
 }  // namespace bi

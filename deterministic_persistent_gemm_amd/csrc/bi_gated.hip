@@ -18,7 +18,7 @@ bool gated_fits(int64_t ldx, int64_t ldw, int64_t M, int64_t I, int64_t H)
 
 template <int BM, int BN, int WM, int WN, int KB, int R, int NL_>
 struct GatedShape {
-    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, false, kEpiGated>;
+    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, kBf16, kEpiGated>;
     static constexpr int NL = NL_;
 };
 

@@ -1,0 +1,231 @@
+// bi_int8.hip -- 8-bit integer operands: quantisation of rows and the product of
+// two quantised operands.
+//
+// A row x is kept as codes q, integers in [-127, 127], and one fp32 scale s:
+//   s = max(max|x| / 127, 2^-126),  q = x / s to the nearest integer, ties to even
+// The product adds code products in 32-bit integers, which rounds nothing, so
+// any order of addition gives the same bits.
+#include "bi_ffn.h"
+#include "bi_plan.h"
+#include "bi_tile.h"
+#include "bi_tile_rule.h"
+
+namespace bi {
+
+// x / s to the nearest integer, ties to even, for |x / s| < 127.5.  x times the
+// reciprocal may round to the wrong side of a halfway point, or onto one; the
+// sign of x - (q +- 1/2) s, which a fused multiply-add gives exactly, says where
+// x lies.
+__device__ __forceinline__ int code_of(float x, float s, float inv)
+{
+    const float q = rintf(x * inv);
+    const int i = (int)q;
+    const float above = __builtin_fmaf(-(q + 0.5f), s, x), below = __builtin_fmaf(-(q - 0.5f), s, x);
+    const bool odd = i & 1;
+    return above > 0.f || (above == 0.f && odd) ? i + 1 : below < 0.f || (below == 0.f && odd) ? i - 1 : i;
+}
+
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d)
+{
+    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+}
+
+// Eight values of a row in one load (two in fp32).
+template <bool BF16IN>
+__device__ __forceinline__ void load8(const void* x, int64_t at, float (&v)[8])
+{
+    if constexpr (BF16IN) {
+        const u32x4 u = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(x) + at);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(u[j] << 16);
+            v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        }
+    } else {
+        const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(x) + at);
+        const f32x4 a = p[0], b = p[1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = a[j];
+            v[4 + j] = b[j];
+        }
+    }
+}
+
+// One workgroup per row: the largest magnitude by bit pattern, so that NaN and
+// infinity win, then the codes.  The first P chunks of 8 values per thread stay in
+// registers between the two; longer rows are read again.
+template <bool BF16IN, int P>
+__global__ __launch_bounds__(256) void k_quantize_int8(const void* __restrict__ x, int64_t ldx, uint8_t* __restrict__ q,
+                                                       int64_t ldq, float* __restrict__ sc, int64_t rows, int chunks)
+{
+    __shared__ uint32_t tops[4];
+    const int tid = threadIdx.x;
+    for (int64_t m = blockIdx.x; m < rows; m += gridDim.x) {
+        float v[P][8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int c = i * 256 + tid;
+            if (c < chunks) {
+                load8<BF16IN>(x, m * ldx + c * 8, v[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
+            }
+        }
+        for (int c = P * 256 + tid; c < chunks; c += 256) {
+            float w[8];
+            load8<BF16IN>(x, m * ldx + (int64_t)c * 8, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                top = max(top, __float_as_uint(w[j]) & 0x7fffffffu);
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1)
+            top = max(top, (uint32_t)__shfl_xor((int)top, d));
+        if ((tid & 63) == 0)
+            tops[tid >> 6] = top;
+        __syncthreads();
+        top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+        __syncthreads();
+        const bool finite = top < 0x7f800000u;
+        const float s = finite ? fmaxf(__uint_as_float(top) / 127.0f, 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
+        // tiny rows are scaled up by a power of two, so that no half step is subnormal
+        const float up = s < 8.67361738e-19f ? 1.84467441e19f : 1.0f;      // 2^-60, 2^64
+        const float s1 = s * up, inv = 1.0f / s1;
+        auto store = [&](int c, const float (&w)[8]) __attribute__((always_inline)) {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            int k[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                k[j] = finite ? code_of(w[j] * up, s1, inv) : 0;
+            *reinterpret_cast<u32x2*>(q + m * ldq + (int64_t)c * 8) = u32x2{pack4(k[0], k[1], k[2], k[3]), pack4(k[4], k[5], k[6], k[7])};
+        };
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (i * 256 + tid < chunks)
+                store(i * 256 + tid, v[i]);
+        for (int c = P * 256 + tid; c < chunks; c += 256) {
+            float w[8];
+            load8<BF16IN>(x, m * ldx + (int64_t)c * 8, w);
+            store(c, w);
+        }
+        if (tid == 0)
+            sc[m] = s;
+    }
+}
+
+template <bool BF16IN>
+static void quantize_rows(const void* x, int64_t ldx, uint8_t* q, int64_t ldq, float* sc, int64_t rows, int64_t K, hipStream_t s)
+{
+    const int chunks = (int)(K / 8);
+    const unsigned grid = (unsigned)(rows < (1 << 20) ? rows : (1 << 20));
+    if (chunks <= 256)
+        k_quantize_int8<BF16IN, 1><<<grid, 256, 0, s>>>(x, ldx, q, ldq, sc, rows, chunks);
+    else if (chunks <= 512)
+        k_quantize_int8<BF16IN, 2><<<grid, 256, 0, s>>>(x, ldx, q, ldq, sc, rows, chunks);
+    else
+        k_quantize_int8<BF16IN, 4><<<grid, 256, 0, s>>>(x, ldx, q, ldq, sc, rows, chunks);
+}
+
+hipError_t launch_quantize_int8(const void* x, int x_bf16, int64_t ldx, int8_t* q, int64_t ldq, float* sc, int64_t rows,
+                                int64_t K, hipStream_t s)
+{
+    uint8_t* u = reinterpret_cast<uint8_t*>(q);
+    if (x_bf16)
+        quantize_rows<true>(x, ldx, u, ldq, sc, rows, K, s);
+    else
+        quantize_rows<false>(x, ldx, u, ldq, sc, rows, K, s);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------- product
+
+bool int8_fits(int64_t ldx, int64_t ldw, int64_t M, int64_t N, int64_t K)
+{
+    const int64_t lim = int64_t(1) << 32;
+    return 255 * ldx + K < lim && 255 * ldw + K < lim && K <= kInt8MaxK && ((M + 15) / 16) * ((N + 15) / 16) < (int64_t(1) << 31);
+}
+
+template <int BM, int BN, int WM, int WN, int KB, int R, int NL_>
+struct Int8Shape {
+    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, kInt8, kEpiLinear>;
+    static constexpr int NL = NL_;
+};
+
+// the costs are explained in bi_tile_rule.h; a slice is 64 k
+static const TileShape kInt8Shapes[] = {
+    {16, 16, 0.67f, 0.037f, 1.10f}, {16, 32, 0.29f, 0.063f, 1.10f}, {32, 32, 0.64f, 0.072f, 1.10f}, {64, 32, 0.90f, 0.088f, 0.f},
+    {128, 64, 0.65f, 0.204f, 0.f},  {128, 128, 0.72f, 0.277f, 0.f}, {256, 256, 1.87f, 0.688f, 0.f},
+};
+
+static int int8_pick(int64_t M, int64_t N, int64_t K, int y_bf16)
+{
+    return pick_tile(kInt8Shapes, 7, M, N, (K + 63) / 64, !y_bf16, device_cu_count());
+}
+
+// f of the shape at an index of kInt8Shapes
+template <typename F>
+static auto int8_shape(int i, F f)
+{
+    switch (i) {
+    case 0: return f(Int8Shape<16, 16, 1, 1, 8, 4, 4>{});
+    case 1: return f(Int8Shape<16, 32, 1, 1, 4, 4, 4>{});
+    case 2: return f(Int8Shape<32, 32, 2, 1, 4, 4, 4>{});
+    case 3: return f(Int8Shape<64, 32, 4, 1, 4, 4, 4>{});
+    case 4: return f(Int8Shape<128, 64, 4, 1, 2, 4, 0>{});
+    case 5: return f(Int8Shape<128, 128, 4, 2, 2, 4, 0>{});
+    default: return f(Int8Shape<256, 256, 4, 2, 2, 2, 0>{});
+    }
+}
+
+template <typename S>
+__global__ __launch_bounds__((S::C::NW + S::NL) * 64) void k_int8(TileArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char ring[S::C::kRing];
+    int tn;
+    const int tm = tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tn);
+    tile_any<S>(p, ring, tm, tn);
+}
+
+template <typename S>
+static hipError_t int8_tile(TileArgs a, hipStream_t s)
+{
+    using C = typename S::C;
+    a.tiles_m = (a.M + C::BM - 1) / C::BM;
+    a.tiles_n = (a.N + C::BN - 1) / C::BN;
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    if (!grid_ok(tiles))
+        return hipErrorInvalidConfiguration;
+    k_int8<S><<<(unsigned)tiles, (C::NW + S::NL) * 64, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_linear(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw, const float* ws,
+                              const float* bias, void* y, int y_bf16, int64_t ldy, int64_t M, int64_t N, int64_t K, hipStream_t s)
+{
+    TileArgs a{};
+    a.a = reinterpret_cast<const unsigned char*>(xq);
+    a.b = reinterpret_cast<const unsigned char*>(wq);
+    a.lda = ldx;
+    a.ldb = ldw;
+    a.sa = reinterpret_cast<const unsigned char*>(xs);
+    a.sb = reinterpret_cast<const unsigned char*>(ws);
+    a.bias = bias;
+    a.y = y;
+    a.ldy = ldy;
+    a.y_bf16 = y_bf16;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = K;
+    return int8_shape(int8_pick(M, N, K, y_bf16), [&](auto shape) { return int8_tile<decltype(shape)>(a, s); });
+}
+
+TileInfo int8_tile_info(int64_t M, int64_t N, int64_t K, int y_bf16)
+{
+    const int i = int8_pick(M, N, K, y_bf16);
+    return int8_shape(i, [i](auto shape) { return tile_info<decltype(shape)>(i); });
+}
+
+}  // namespace bi

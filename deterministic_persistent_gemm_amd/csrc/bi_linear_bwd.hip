@@ -72,35 +72,35 @@ __device__ __forceinline__ void colsum_body(const SumArgs& p, unsigned char* lds
 // 1792: 35 us against 27), and the rule does not take it there.
 template <int SHAPE, bool CA> struct BwdShape;
 template <bool CA> struct BwdShape<0, CA> {
-    using C = TileCfg<32, 32, 2, 2, 4, 4, CA, true, false, kEpiLinear>;
+    using C = TileCfg<32, 32, 2, 2, 4, 4, CA, true, kBf16, kEpiLinear>;
     static constexpr int NL = 4;
 };
 template <bool CA> struct BwdShape<1, CA> {
-    using C = TileCfg<64, 64, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
+    using C = TileCfg<64, 64, 4, 2, 2, 4, CA, true, kBf16, kEpiLinear>;
     static constexpr int NL = 0;
 };
 template <> struct BwdShape<1, false> {
-    using C = TileCfg<32, 64, 2, 2, 4, 3, false, true, false, kEpiLinear>;
+    using C = TileCfg<32, 64, 2, 2, 4, 3, false, true, kBf16, kEpiLinear>;
     static constexpr int NL = 4;
 };
 template <bool CA> struct BwdShape<2, CA> {
-    using C = TileCfg<128, 64, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
+    using C = TileCfg<128, 64, 4, 2, 2, 4, CA, true, kBf16, kEpiLinear>;
     static constexpr int NL = 0;
 };
 template <bool CA> struct BwdShape<3, CA> {
-    using C = TileCfg<128, 128, 4, 2, 2, 4, CA, true, false, kEpiLinear>;
+    using C = TileCfg<128, 128, 4, 2, 2, 4, CA, true, kBf16, kEpiLinear>;
     static constexpr int NL = 0;
 };
 template <> struct BwdShape<5, false> {
-    using C = TileCfg<16, 32, 1, 2, 4, 4, false, true, false, kEpiLinear>;
+    using C = TileCfg<16, 32, 1, 2, 4, 4, false, true, kBf16, kEpiLinear>;
     static constexpr int NL = 4;
 };
 template <> struct BwdShape<6, false> {
-    using C = TileCfg<64, 64, 2, 2, 2, 4, false, true, false, kEpiLinear>;
+    using C = TileCfg<64, 64, 2, 2, 2, 4, false, true, kBf16, kEpiLinear>;
     static constexpr int NL = 4;
 };
 template <bool CA> struct BwdShape<4, CA> {
-    using C = TileCfg<256, 256, CA ? 4 : 2, CA ? 2 : 4, 2, 2, CA, true, false, kEpiLinear>;
+    using C = TileCfg<256, 256, CA ? 4 : 2, CA ? 2 : 4, 2, 2, CA, true, kBf16, kEpiLinear>;
     static constexpr int NL = 0;
 };
 
@@ -111,12 +111,9 @@ __device__ __forceinline__ void bwd_body(const TileArgs& p, unsigned char* ring,
     static_assert(kUsed == kBwdThreads || (S::NL > 0 && kUsed < kBwdThreads), "one workgroup size");
     if (kUsed < kBwdThreads && (int)threadIdx.x >= kUsed)
         return;                                         // a barrier counts the waves that are left
-    if constexpr (S::NL > 0)
-        stream_body<typename S::C, S::NL>(p, ring, block);
-    else if constexpr (S::C::R == 2)
-        turns_body<typename S::C>(p, ring, block);
-    else
-        tile_body<typename S::C>(p, ring, block);
+    int tn;
+    const int tm = tile_of(block, p.tiles_m, p.tiles_n, tn);
+    tile_any<S>(p, ring, tm, tn);
 }
 
 // Workgroups 0 .. ndx-1 tile dx, the next ndw dw, the rest sum columns.

@@ -137,7 +137,7 @@ bool mx_fits(int64_t ldx, int64_t ldxs, int64_t ldw, int64_t ldws, int64_t M, in
 
 template <int BM, int BN, int WM, int WN, int KB, int R, int NL_>
 struct MxShape {
-    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, true, kEpiLinear>;
+    using C = TileCfg<BM, BN, WM, WN, KB, R, false, false, kFp4, kEpiLinear>;
     static constexpr int NL = NL_;
 };
 

@@ -1,6 +1,6 @@
 // bi_tile.h -- one output tile of C = A . B^T per workgroup, operands streamed
 // through an LDS ring: the kernel behind the gated linear layer, the backward
-// passes and the 4-bit product.
+// passes, the 4- and 8-bit products and the products grouped by expert.
 //
 //   C[m, n] = sum_k A(m, k) B(n, k)
 //
@@ -13,7 +13,9 @@
 // Numerics: one fp32 accumulator per output element, threaded through every
 // slice of k in ascending order by one matrix instruction per slice:
 // v_mfma_f32_16x16x32_bf16 (32 k), or v_mfma_scale_f32_16x16x128_f8f6f4 on
-// 4-bit operands (128 k, one power-of-two scale per operand row and 32 k).
+// 4-bit operands (128 k, one power-of-two scale per operand row and 32 k).  8-bit
+// integers add up in 32-bit integers, without rounding, by v_mfma_i32_16x16x64_i8
+// (64 k).
 // k past the end of a ragged last slice is zero in both operands.  Nothing in
 // that sequence depends on the tile shape, on M or on a row's place in the
 // batch.
@@ -32,14 +34,15 @@
 namespace bi {
 
 enum TileEpilogue { kEpiLinear = 0, kEpiGated = 1 };
+enum TileType { kBf16, kFp4, kInt8 };                   // of both operands
 enum TileGate { kGateSilu = 0, kGateGeluTanh = 1 };
 
 struct TileArgs {
     const unsigned char* a;     // A: row operand: row m at a + m lda; column operand: k at a + k lda
     const unsigned char* b;
     int64_t lda, ldb;           // bytes
-    const unsigned char* sa;    // 4-bit operands: scale bytes, one row of them per operand row
-    const unsigned char* sb;
+    const unsigned char* sa;    // 4-bit operands: scale bytes, one row of them per operand row;
+    const unsigned char* sb;    // 8-bit operands: an fp32 scale per operand row
     int64_t ldsa, ldsb;         // bytes
     const float* bias;          // [N] or nullptr
     void* y;
@@ -88,12 +91,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // Workgroup w runs on XCD w % 8.  Each XCD takes one contiguous eighth of the
 // tiles in an order that walks groups of 8 tile rows column by column, so that
 // the tiles an XCD works on at one time share rows of A and of B in its L2.
-__device__ __forceinline__ int tile_of(int w, int tiles_m, int tiles_n, int& tn)
+__device__ __forceinline__ int tile_at(int t, int tiles_m, int tiles_n, int& tn)
 {
-    const int total = tiles_m * tiles_n;
-    const int x = w & 7, j = w >> 3;
-    const int per = total >> 3, more = total & 7;       // XCD x owns per (+1) tiles
-    const int t = x * per + min(x, more) + j;
     constexpr int kGroup = 8;
     const int group = t / (kGroup * tiles_n);
     const int m0 = group * kGroup;
@@ -101,6 +100,13 @@ __device__ __forceinline__ int tile_of(int w, int tiles_m, int tiles_n, int& tn)
     const int in = t - m0 * tiles_n;
     tn = in / rows;
     return m0 + in % rows;
+}
+__device__ __forceinline__ int tile_of(int w, int tiles_m, int tiles_n, int& tn)
+{
+    const int total = tiles_m * tiles_n;
+    const int x = w & 7, j = w >> 3;
+    const int per = total >> 3, more = total & 7;       // XCD x owns per (+1) tiles
+    return tile_at(x * per + min(x, more) + j, tiles_m, tiles_n, tn);
 }
 
 // How the weight side's output columns are dealt to fragment rows.  kPairs:
@@ -221,10 +227,11 @@ constexpr int scale_ring_groups(int kb, int r)
 // A tile: BM x BN outputs (gated: BN weight rows, BN / 2 outputs) on WM x WN
 // computing waves, R ring stages of KB slices.  CA, CB: operand A / B stored by
 // columns.
-template <int BM_, int BN_, int WM_, int WN_, int KB_, int R_, bool CA_, bool CB_, bool FP4_, int EPI_>
+template <int BM_, int BN_, int WM_, int WN_, int KB_, int R_, bool CA_, bool CB_, TileType TYPE_, int EPI_>
 struct TileCfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, R = R_, EPI = EPI_;
-    static constexpr bool CA = CA_, CB = CB_, FP4 = FP4_;
+    static constexpr TileType TYPE = TYPE_;
+    static constexpr bool CA = CA_, CB = CB_, FP4 = TYPE == kFp4;
     static constexpr int NW = WM * WN;
     static constexpr bool kSums = CA && BM_ < 256;
     static constexpr int FM = BM / (WM * 16), FN = BN / (WN * 16);
@@ -236,7 +243,7 @@ struct TileCfg {
     using A = TileOperand<BM, KB, CA, false, kWide>;
     using B = TileOperand<BN, KB, CB, kDeal == kPairs || kDeal == kGated4, kWide>;
     static constexpr int kOutN = EPI == kEpiGated ? BN / 2 : BN;       // output columns per tile
-    static constexpr int kSliceK = FP4 ? 128 : 32;
+    static constexpr int kSliceK = FP4 ? 128 : TYPE == kInt8 ? 64 : 32;
     static constexpr int kStage = A::kBytes + B::kBytes;
     // Scales travel in groups of four slices, [row][16 bytes], A's rows then B's:
     // a 4-byte load then takes 16 bytes of each of 16 rows (a load of one slice's
@@ -253,8 +260,8 @@ struct TileCfg {
     static constexpr int kRing = kScaleAt + kGroups * kGroup;
     static_assert(!FP4 || kGroupInStage || ((BM + BN) / 16 * KB) % 4 == 0, "equal parts of a group per stage");
     static_assert(FM * WM * 16 == BM && FN * WN * 16 == BN, "whole fragments per wave");
-    static_assert(!(FP4 && (CA || CB)), "4-bit operands are stored by rows");
-    static_assert(EPI != kEpiGated || !CB, "the gated weight is stored by rows");
+    static_assert(TYPE == kBf16 || !(CA || CB), "4- and 8-bit operands are stored by rows");
+    static_assert(EPI != kEpiGated || (!CB && TYPE == kBf16), "the gated weight: bf16, stored by rows");
 };
 
 // Shape S (its TileCfg S::C and loading waves S::NL) at index i of its product's list.
@@ -304,7 +311,7 @@ struct TileLoads {
         lds0 = lds_byte(ring);
         K = p.K;
         ns = (int)((p.K + C::kSliceK - 1) / C::kSliceK);
-        kbytes = (int)(C::FP4 ? p.K / 2 : p.K * 2);                    // row operands
+        kbytes = (int)(C::FP4 ? p.K / 2 : C::TYPE == kInt8 ? p.K : p.K * 2);   // row operands
         lda = p.lda;
         ldb = p.ldb;
         abase = p.a + (C::CA ? (int64_t)m0 * 2 : (int64_t)m0 * p.lda);
@@ -466,24 +473,29 @@ struct TileFrags {
     }
 };
 
-template <bool FP4>
+// 8-bit operands: the accumulator's four registers hold 32-bit integers.
+template <TileType TYPE>
 __device__ __forceinline__ void tile_mfma(const u32x4& x, const u32x4& w, int sx, int sw, f32x4& c)
 {
-    if constexpr (FP4) {
+    if constexpr (TYPE == kFp4) {
         const i32x8 xv = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0};
         const i32x8 wv = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
         c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv, c, 4, 4, 0, sw, 0, sx);
+    } else if constexpr (TYPE == kInt8) {
+        c = __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, x),
+                                                                            __builtin_bit_cast(i32x4, c), 0, 0, 0));
     } else {
         c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), c, 0, 0, 0);
     }
 }
 
 // Zero what lies past the end of k: `valid` k values of this lane's eight
-// (bf16) or 32 (4-bit) belong to the problem.
-template <bool FP4>
+// (bf16), 16 (8-bit) or 32 (4-bit) belong to the problem.  K is a multiple of 32, so
+// that the lanes of narrow types have all of theirs or none.
+template <TileType TYPE>
 __device__ __forceinline__ u32x4 mask_k(u32x4 v, int64_t valid)
 {
-    if constexpr (FP4) {
+    if constexpr (TYPE != kBf16) {
         return valid > 0 ? v : u32x4{0u, 0u, 0u, 0u};
     } else {
         u32x4 o;
@@ -547,6 +559,18 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, const f32x4 (&acc)
                                            int r, int g)
 {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    // 8-bit operands: the columns' scales, four to a fragment (past the last column
+    // the last four again)
+    constexpr bool kScaled = C::TYPE == kInt8;
+    constexpr int kPF = C::kDeal == kPairs ? 2 : 1;
+    f32x4 colscale[kScaled ? C::FN : 1];
+    if constexpr (kScaled) {
+#pragma unroll
+        for (int f = 0; f < C::FN; ++f) {
+            const int n = n0 + (wn * (C::FN / kPF) + f / kPF) * 16 * kPF + 4 * kPF * g + 4 * (f % kPF);
+            colscale[f] = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p.sb) + min(n, p.N - 4));
+        }
+    }
     auto gated = [&](float gv, float uv) __attribute__((always_inline)) { return gv * kSigmaScale * gate_sigma8(gv, p.gate) * uv; };
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm) {
@@ -609,7 +633,10 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, const f32x4 (&acc)
             }
         } else {
             // kPairs: eight columns from two fragments; kSingle: four from one
-            constexpr int PF = C::kDeal == kPairs ? 2 : 1;
+            constexpr int PF = kPF;
+            float rowscale = 0.f;
+            if constexpr (kScaled)
+                rowscale = reinterpret_cast<const float*>(p.sa)[min(m, p.M - 1)];
 #pragma unroll
             for (int q2 = 0; q2 < C::FN / PF; ++q2) {
                 const int n = n0 + (wn * (C::FN / PF) + q2) * 16 * PF + 4 * PF * g;
@@ -618,6 +645,12 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, const f32x4 (&acc)
 #pragma unroll
                     for (int f = 0; f < PF; ++f) {
                         v[f] = acc[fm][q2 * PF + f];
+                        // the integer to fp32 (exact up to 2^24), then the row's scale, then the column's
+                        if constexpr (kScaled) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                v[f][q] = (float)__float_as_int(v[f][q]) * rowscale * colscale[q2 * PF + f][q];
+                        }
                         if (p.bias)
                             v[f] += *reinterpret_cast<const f32x4*>(p.bias + n + 4 * f);
                     }
@@ -650,10 +683,9 @@ __device__ __forceinline__ void tile_store(const TileArgs& p, const f32x4 (&acc)
 // per MFMA (8 KiB of fragments for every 8 MFMAs of a wave); it is taken where
 // larger tiles would leave compute units idle.
 template <typename C>
-__device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring, int block)
+__device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring, int tm, int tn)
 {
     constexpr int FM = C::FM, FN = C::FN, KB = C::KB, R = C::R;
-    constexpr bool FP4 = C::FP4;
     constexpr int kSliceK = C::kSliceK;
     using Loads = TileLoads<C, C::NW>;
     constexpr int LS = Loads::LS;
@@ -664,8 +696,6 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
     const int lane = threadIdx.x & 63, w = (int)uniform(threadIdx.x >> 6);
     const int wm = w / C::WN, wn = w % C::WN;
     const int r = lane & 15, g = lane >> 4;
-    int tn;
-    const int tm = tile_of(block, p.tiles_m, p.tiles_n, tn);
     const int m0 = tm * C::BM, n0 = tn * C::kOutN;
     const int ns = (int)((p.K + kSliceK - 1) / kSliceK);           // slices
     Loads loads;
@@ -716,12 +746,12 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
             const int64_t valid = p.K - (int64_t)s * kSliceK - g * (kSliceK / 4);
 #pragma unroll
             for (int f = 0; f < FM; ++f) {
-                xc[f] = mask_k<FP4>(xc[f], valid);
+                xc[f] = mask_k<C::TYPE>(xc[f], valid);
                 sxc[f] = valid > 0 ? sxc[f] : 127;
             }
 #pragma unroll
             for (int f = 0; f < FN; ++f) {
-                wf[f] = mask_k<FP4>(wf[f], valid);
+                wf[f] = mask_k<C::TYPE>(wf[f], valid);
                 swf[f] = valid > 0 ? swf[f] : 127;
             }
         }
@@ -752,7 +782,7 @@ __device__ __forceinline__ void tile_body(const TileArgs& p, unsigned char* ring
         for (int fn = 0; fn < FN; ++fn) {
 #pragma unroll
             for (int fm = 0; fm < FM; ++fm)
-                tile_mfma<FP4>(xc[fm], wf[fn], sxc[fm], swf[fn], acc[fm][fn]);
+                tile_mfma<C::TYPE>(xc[fm], wf[fn], sxc[fm], swf[fn], acc[fm][fn]);
             wf[fn] = frags.b(nat, nj, fn);
             swf[fn] = frags.sb(s + 1, fn);
             if (stage_end) {
@@ -811,7 +841,6 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
                                             int wm, int wn, int r, int g, f32x4 (&acc)[C::FM][C::FN])
 {
     constexpr int FM = C::FM, FN = C::FN;
-    constexpr bool FP4 = C::FP4;
     constexpr int kSliceK = C::kSliceK;
     constexpr int LS = TileLoads<C, C::NW>::LS, kFirst = LS / 2;   // group 0's loads: before and between its MFMAs
     TileFrags<C> frags;
@@ -836,12 +865,12 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
         const int64_t valid = p.K - (int64_t)s * kSliceK - g * (kSliceK / 4);
 #pragma unroll
         for (int f = 0; f < FM; ++f) {
-            xf[f] = mask_k<FP4>(xf[f], valid);
+            xf[f] = mask_k<C::TYPE>(xf[f], valid);
             sx[f] = valid > 0 ? sx[f] : 127;
         }
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
-            wf[f] = mask_k<FP4>(wf[f], valid);
+            wf[f] = mask_k<C::TYPE>(wf[f], valid);
             sw[f] = valid > 0 ? sw[f] : 127;
         }
     };
@@ -853,7 +882,7 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 0; i < FN * FM; ++i) {
-            tile_mfma<FP4>(xf[i % FM], wf[i / FM], sx[i % FM], sw[i / FM], acc[i % FM][i / FM]);
+            tile_mfma<C::TYPE>(xf[i % FM], wf[i / FM], sx[i % FM], sw[i / FM], acc[i % FM][i / FM]);
             if (i % kEvery == kEvery / 2 && i / kEvery < kLoads) {
                 __builtin_amdgcn_sched_barrier(0);
                 loads.template issue_one<decltype(whole_loads)::value>(st, decltype(t0)::value + i / kEvery);
@@ -912,14 +941,12 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
 }
 
 template <typename C>
-__device__ __forceinline__ void turns_body(const TileArgs& p, unsigned char* ring, int block)
+__device__ __forceinline__ void turns_body(const TileArgs& p, unsigned char* ring, int tm, int tn)
 {
     static_assert(C::KB == 2 && C::R == 2 && C::NW == 8, "eight waves, two stages of two slices");
     const int lane = threadIdx.x & 63, w = (int)uniform(threadIdx.x >> 6);
     const int wm = w / C::WN, wn = w % C::WN;
     const int r = lane & 15, g = lane >> 4;
-    int tn;
-    const int tm = tile_of(block, p.tiles_m, p.tiles_n, tn);
     const int m0 = tm * C::BM, n0 = tn * C::kOutN;
     const int ns = (int)((p.K + C::kSliceK - 1) / C::kSliceK);
     TileLoads<C, C::NW> loads;
@@ -951,19 +978,16 @@ __device__ __forceinline__ void turns_body(const TileArgs& p, unsigned char* rin
 // through H = 4096, I = 12288 (203 MB): 36 to 39 us, 5.2 to 5.6 TB/s, the rate of a
 // large copy.
 template <typename C, int NL>
-__device__ __forceinline__ void stream_body(const TileArgs& p, unsigned char* ring, int block)
+__device__ __forceinline__ void stream_body(const TileArgs& p, unsigned char* ring, int tm, int tn)
 {
     constexpr int FM = C::FM, FN = C::FN, KB = C::KB, R = C::R;
-    constexpr bool FP4 = C::FP4;
     constexpr int kSliceK = C::kSliceK;
-    static_assert(!FP4 || C::kGroupInStage, "a stage brings its own scales");
+    static_assert(!C::FP4 || C::kGroupInStage, "a stage brings its own scales");
     using Loads = TileLoads<C, NL>;
     constexpr int LS = Loads::LS;
     static_assert(R >= 2 && (R - 2) * LS < 64, "ring depth");
 
     const int lane = threadIdx.x & 63, w = (int)uniform(threadIdx.x >> 6);
-    int tn;
-    const int tm = tile_of(block, p.tiles_m, p.tiles_n, tn);
     const int m0 = tm * C::BM, n0 = tn * C::kOutN;
     const int ns = (int)((p.K + kSliceK - 1) / kSliceK);
     const int nst = (ns + KB - 1) / KB;                            // stages
@@ -1017,12 +1041,12 @@ __device__ __forceinline__ void stream_body(const TileArgs& p, unsigned char* ri
                 const int64_t valid = p.K - (int64_t)(st * KB + j) * kSliceK - g * (kSliceK / 4);
 #pragma unroll
                 for (int f = 0; f < FM; ++f) {
-                    x[j][f] = mask_k<FP4>(x[j][f], valid);
+                    x[j][f] = mask_k<C::TYPE>(x[j][f], valid);
                     sx[j][f] = valid > 0 ? sx[j][f] : 127;
                 }
 #pragma unroll
                 for (int f = 0; f < FN; ++f) {
-                    wf[j][f] = mask_k<FP4>(wf[j][f], valid);
+                    wf[j][f] = mask_k<C::TYPE>(wf[j][f], valid);
                     sw[j][f] = valid > 0 ? sw[j][f] : 127;
                 }
             }
@@ -1030,7 +1054,7 @@ __device__ __forceinline__ void stream_body(const TileArgs& p, unsigned char* ri
             for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
                 for (int fm = 0; fm < FM; ++fm)
-                    tile_mfma<FP4>(x[j][fm], wf[j][fn], sx[j][fm], sw[j][fn], acc[fm][fn]);
+                    tile_mfma<C::TYPE>(x[j][fm], wf[j][fn], sx[j][fm], sw[j][fn], acc[fm][fn]);
         }
     };
     const int whole = (int)(p.K / (kSliceK * KB));
@@ -1041,25 +1065,43 @@ __device__ __forceinline__ void stream_body(const TileArgs& p, unsigned char* ri
     tile_store<C>(p, acc, m0, n0, wm, wn, r, g);
 }
 
+// Shape S (its TileCfg S::C and loading waves S::NL): its body on tile (tm, tn).
+template <typename S>
+__device__ __forceinline__ void tile_any(const TileArgs& p, unsigned char* ring, int tm, int tn)
+{
+    if constexpr (S::NL > 0)
+        stream_body<typename S::C, S::NL>(p, ring, tm, tn);
+    else if constexpr (S::C::R == 2)
+        turns_body<typename S::C>(p, ring, tm, tn);
+    else
+        tile_body<typename S::C>(p, ring, tm, tn);
+}
+
 template <typename C>
 __global__ __launch_bounds__(C::NW * 64) void k_tile(TileArgs p)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char ring[C::kRing];
-    tile_body<C>(p, ring, (int)blockIdx.x);
+    int tn;
+    const int tm = tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tn);
+    tile_body<C>(p, ring, tm, tn);
 }
 
 template <typename C>
 __global__ __launch_bounds__(C::NW * 64) void k_turns(TileArgs p)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char ring[C::kRing];
-    turns_body<C>(p, ring, (int)blockIdx.x);
+    int tn;
+    const int tm = tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tn);
+    turns_body<C>(p, ring, tm, tn);
 }
 
 template <typename C, int NL>
 __global__ __launch_bounds__((C::NW + NL) * 64) void k_stream(TileArgs p)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char ring[C::kRing];
-    stream_body<C, NL>(p, ring, (int)blockIdx.x);
+    int tn;
+    const int tm = tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tn);
+    stream_body<C, NL>(p, ring, tm, tn);
 }
 
 }  // namespace bi

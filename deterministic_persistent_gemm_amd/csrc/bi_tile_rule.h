@@ -49,9 +49,9 @@ inline float tile_once(const TileShape& t, int64_t slices, bool f32_out)
     return t.per_tile + t.per_slice * (float)slices + (f32_out ? (float)(t.bm * t.bn) * 2.f / 18750.f : 0.f);
 }
 
-inline float tile_time(const TileShape& t, int64_t M, int64_t N, int64_t slices, bool f32_out, int cus)
+// A launch of so many tiles.
+inline float tiles_time(const TileShape& t, int64_t tiles, int64_t slices, bool f32_out, int cus)
 {
-    const int64_t tiles = tile_count(t, M, N);
     float rounds;
     if (t.share > 0.f) {
         rounds = (float)tiles / (float)cus * t.share;
@@ -60,6 +60,11 @@ inline float tile_time(const TileShape& t, int64_t M, int64_t N, int64_t slices,
         rounds = (float)((tiles + cus - 1) / cus);
     }
     return kTileLaunch + rounds * tile_once(t, slices, f32_out);
+}
+
+inline float tile_time(const TileShape& t, int64_t M, int64_t N, int64_t slices, bool f32_out, int cus)
+{
+    return tiles_time(t, tile_count(t, M, N), slices, f32_out, cus);
 }
 
 // The index of the fastest of n shapes.

@@ -320,6 +320,85 @@ bi_status_t bi_linear_mxfp4(const uint8_t* xq, int64_t ldxq, const uint8_t* xs, 
                             const float* bias, void* y, int32_t y_dtype, int64_t ldy,
                             int64_t M, int64_t N, int64_t K, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The experts of an MoE layer as operators of their own, trained in bf16 and
+ * served in 8-bit integers, and the layer norm in front of them.
+ *
+ * The conventions of the feed-forward calls hold (alignment, pitches in
+ * elements, what is refused), and their guarantee: a row of y or dx has the same
+ * bits in every batch; dw and db sum over the batch and repeat from run to run.
+ * ------------------------------------------------------------------------- */
+
+/* Layer norm of the rows of x [M, H] (bf16 or fp32):
+ *   m = sum x / H,  v = sum (x - m)^2 / H,  r = 1 / sqrt(v + eps)
+ *   y = (x - m) r w + b              fp32 math, one rounding to bf16 or none
+ * w, b: [H] fp32, or NULL for ones and zeros.  mean, rstd: [M] fp32 (4-byte
+ * aligned), which receive m and r for the backward pass, or NULL.  Requires
+ * H % 8 == 0, H <= 16384 (BI_EUNSUPPORTED otherwise) and a finite eps >= 0. */
+bi_status_t bi_layer_norm(const void* x, int32_t x_dtype, int64_t ldx, const float* w, const float* b, float eps,
+                          void* y, int32_t y_dtype, int64_t ldy, float* mean, float* rstd,
+                          int64_t M, int64_t H, hipStream_t stream);
+
+/* Its gradients at the statistics kept by the forward pass, n = (x - m) r:
+ *   g = dy w,  dx = r (g - (sum g + n sum(g n)) / H)     dx in x's type
+ *   dw = sum of dy n, db = sum of dy over the rows       [H] fp32
+ * Any of dx, dw, db may be NULL.  dy: bf16 or fp32.  M == 0 clears dw and db.  ws
+ * holds partial sums of dw and db: bi_layer_norm_bwd_workspace_size(M, H) bytes,
+ * unless neither is wanted. */
+bi_status_t bi_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t lddy, const void* x, int32_t x_dtype, int64_t ldx,
+                              const float* mean, const float* rstd, const float* w,
+                              void* dx, int64_t lddx, float* dw, float* db,
+                              int64_t M, int64_t H, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t bi_layer_norm_bwd_workspace_size(int64_t M, int64_t H);
+
+/* Products grouped by expert.  The T rows of x are sorted by expert: expert e's
+ * are ends[e-1] .. ends[e] - 1 (ends[-1] = 0), any number of them, none
+ * included.  ends: [E] int64 on the device (8-byte aligned), ascending, at most T;
+ * it is read by the kernels, so the call does not wait for the router.  (Ends that
+ * do not ascend are replaced by the largest so far, and held to 0 .. T: no call
+ * reads or writes out of range.)  Rows from ends[E-1] on belong to no expert:
+ * they are neither read nor written.  Expert e's weight w[e] [N, K] lies
+ * stride_w elements behind the one before (a multiple of 16 bytes; 0: one weight
+ * for all).  Requires 1 <= E <= 1024, N % 16 == 0, K % 32 == 0.
+ *   y[t,:] = x[t,:] . w[e]^T         bf16 operands, fp32 sums, bf16 or fp32 out */
+bi_status_t bi_grouped_linear_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw, int64_t stride_w,
+                                   const int64_t* ends, int64_t E, void* y, int32_t y_dtype, int64_t ldy,
+                                   int64_t T, int64_t N, int64_t K, hipStream_t stream);
+
+/* Its gradients: dx[t,:] = bf16( dy[t,:] . w[e] ) and dw[e] = the sum over the
+ * expert's rows of dy[t,:]^T x[t,:], bf16 or fp32, zero for an expert without
+ * rows.  dx or dw may be NULL, and w (read for dx only) or x (for dw only) with
+ * it.  T == 0 clears dw.  dw's experts lie stride_dw elements apart (at least one
+ * expert's rows: (N - 1) lddw + K). */
+bi_status_t bi_grouped_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
+                                       const uint16_t* w, int64_t ldw, int64_t stride_w, const int64_t* ends, int64_t E,
+                                       uint16_t* dx, int64_t lddx, void* dw, int32_t dw_dtype, int64_t lddw, int64_t stride_dw,
+                                       int64_t T, int64_t N, int64_t K, hipStream_t stream);
+
+/* Rows of x (bf16 or fp32) as 8-bit integers with one fp32 scale each:
+ *   s = max(max|x| / 127, 2^-126),  q = x / s rounded to the nearest integer,
+ * ties to even: in [-127, 127].  A row that holds an infinity or a NaN gets s = NaN
+ * and zero codes.  q: [rows, K] (pitch in bytes, a multiple of 16), s: [rows], 4-byte
+ * aligned.  Requires K % 32 == 0. */
+bi_status_t bi_quantize_int8(const void* x, int32_t x_dtype, int64_t ldx, int8_t* q, int64_t ldq, float* s,
+                             int64_t rows, int64_t K, hipStream_t stream);
+
+/* y[M,N] of operands in that form, xs: [M] (4-byte aligned), ws: [N]:
+ *   y = ((sum xq wq) xs) ws + bias   the sum exact in 32-bit integers, the rest in
+ *                                    fp32 in this order; bf16 or fp32 out
+ * Any code from -128 to 127 may occur.  Requires N % 16 == 0, K % 32 == 0 and
+ * K <= 131040, beyond which a sum could overflow (BI_EUNSUPPORTED). */
+bi_status_t bi_linear_int8(const int8_t* xq, int64_t ldxq, const float* xs, const int8_t* wq, int64_t ldwq, const float* ws,
+                           const float* bias, void* y, int32_t y_dtype, int64_t ldy,
+                           int64_t M, int64_t N, int64_t K, hipStream_t stream);
+
+/* The same grouped by expert: wq[e] [N, K], ws[e] [N], stride_ws elements (a
+ * multiple of 4) from expert to expert; no bias. */
+bi_status_t bi_grouped_linear_int8(const int8_t* xq, int64_t ldxq, const float* xs,
+                                   const int8_t* wq, int64_t ldwq, int64_t stride_wq, const float* ws, int64_t stride_ws,
+                                   const int64_t* ends, int64_t E, void* y, int32_t y_dtype, int64_t ldy,
+                                   int64_t T, int64_t N, int64_t K, hipStream_t stream);
+
 /* Workspace bytes the linear and MoE calls need for a given problem (0 if none, or if
  * the arguments are invalid).  For the linear layer the workspace holds the
  * counter region and the k tile partials of the decode kernel M selects
@@ -431,16 +510,22 @@ bi_status_t bi_lab_xcc_ids(uint32_t* out, int32_t grid_x, int32_t grid_y, hipStr
 bi_status_t bi_lab_plan(int32_t dtype, int64_t M, int64_t N, int64_t K, int32_t* path);
 
 /* The tile shape a feed-forward product of this size takes: bi_gated_linear_bf16
- * (N = I, K = H), bi_linear_mxfp4 with outputs of out_dtype, and dx or dw of
- * bi_linear_bf16_bwd where both are wanted and dw is of out_dtype.  info: host int32[8] = the shape's index in
+ * (N = I, K = H), bi_linear_mxfp4 or bi_linear_int8 with outputs of out_dtype, and dx or
+ * dw of bi_linear_bf16_bwd where both are wanted and dw is of out_dtype.  info: host int32[8] = the shape's index in
  * the product's list; the kernel (0: waves that load beside waves that compute,
  * 1: every wave loads and computes, 2: two groups of waves in turns); output
  * rows and columns per tile; k per slice; slices per stage; stages in the LDS
  * ring; groups of four slices' scales in theirs (0: no scales).  BI_EINVAL for
  * M <= 0, an unknown op or a NULL info, BI_EUNSUPPORTED for widths the product
  * does not serve. */
-typedef enum { BI_FFN_GATED = 0, BI_FFN_MXFP4 = 1, BI_FFN_DX = 2, BI_FFN_DW = 3 } bi_ffn_op_t;
+typedef enum { BI_FFN_GATED = 0, BI_FFN_MXFP4 = 1, BI_FFN_DX = 2, BI_FFN_DW = 3, BI_FFN_INT8 = 4 } bi_ffn_op_t;
 bi_status_t bi_lab_ffn_tile(int32_t op, int64_t M, int64_t N, int64_t K, int32_t out_dtype, int32_t* info);
+
+/* The same for a product grouped by expert: T rows, E experts (the shape follows
+ * from these, not from how the rows are split); dx and dw are those of
+ * bi_grouped_linear_bf16_bwd. */
+typedef enum { BI_GROUPED_BF16 = 0, BI_GROUPED_INT8 = 1, BI_GROUPED_DX = 2, BI_GROUPED_DW = 3 } bi_grouped_op_t;
+bi_status_t bi_lab_grouped_tile(int32_t op, int64_t T, int64_t E, int64_t N, int64_t K, int32_t out_dtype, int32_t* info);
 
 /* Where a MoE call of this shape keeps its storage points in the workspace,
  * for stage-wise checks of the layer (fused-MoE page, "What's included": the

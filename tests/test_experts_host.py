@@ -1,0 +1,221 @@
+"""Layer norm, products grouped by expert and 8-bit products on the host: what
+the C entry points and the binding refuse, workspace sizes, and the 64-bit
+references against differences and hand-worked values.  Nothing here needs a GPU."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import experts_ref as ref
+
+bi = pytest.importorskip("deterministic_persistent_gemm_amd")
+L = bi.lib()
+P = 0x10000          # aligned, never dereferenced by validation
+BIG = 1 << 62
+
+
+def norm(x=P, xt=1, ldx=64, w=P, b=P, eps=1e-5, y=P, yt=1, ldy=64, mean=P, rstd=P, M=4, H=64):
+    return L.bi_layer_norm(x, xt, ldx, w, b, eps, y, yt, ldy, mean, rstd, M, H, None)
+
+
+def norm_bwd(dy=P, dt=1, lddy=64, x=P, xt=1, ldx=64, mean=P, rstd=P, w=P, dx=P, lddx=64, dw=P, db=P, M=4, H=64, ws=P, n=1 << 24):
+    return L.bi_layer_norm_bwd(dy, dt, lddy, x, xt, ldx, mean, rstd, w, dx, lddx, dw, db, M, H, ws, n, None)
+
+
+def grouped(x=P, ldx=64, w=P, ldw=64, sw=2048, ends=P, E=4, y=P, yt=1, ldy=32, T=4, N=32, K=64):
+    return L.bi_grouped_linear_bf16(x, ldx, w, ldw, sw, ends, E, y, yt, ldy, T, N, K, None)
+
+
+def grouped_bwd(dy=P, lddy=32, x=P, ldx=64, w=P, ldw=64, sw=2048, ends=P, E=4, dx=P, lddx=64, dw=P, dt=1, lddw=64, sdw=2048,
+                T=4, N=32, K=64):
+    return L.bi_grouped_linear_bf16_bwd(dy, lddy, x, ldx, w, ldw, sw, ends, E, dx, lddx, dw, dt, lddw, sdw, T, N, K, None)
+
+
+def quantize(x=P, dt=1, ldx=64, q=P, ldq=64, s=P, rows=4, K=64):
+    return L.bi_quantize_int8(x, dt, ldx, q, ldq, s, rows, K, None)
+
+
+def int8(xq=P, ldxq=64, xs=P, wq=P, ldwq=64, ws=P, b=P, y=P, dt=1, ldy=32, M=4, N=32, K=64):
+    return L.bi_linear_int8(xq, ldxq, xs, wq, ldwq, ws, b, y, dt, ldy, M, N, K, None)
+
+
+def grouped_int8(xq=P, ldxq=64, xs=P, wq=P, ldwq=64, sw=2048, ws=P, ss=32, ends=P, E=4, y=P, dt=1, ldy=32, T=4, N=32, K=64):
+    return L.bi_grouped_linear_int8(xq, ldxq, xs, wq, ldwq, sw, ws, ss, ends, E, y, dt, ldy, T, N, K, None)
+
+
+INVALID = [
+    (norm, dict(x=None)), (norm, dict(y=None)), (norm, dict(x=P + 8)), (norm, dict(w=P + 4)), (norm, dict(b=P + 8)),
+    (norm, dict(mean=P + 2)), (norm, dict(rstd=P + 1)), (norm, dict(ldx=56)), (norm, dict(ldx=68)), (norm, dict(ldy=63)),
+    (norm, dict(xt=2)), (norm, dict(yt=-1)), (norm, dict(eps=-1e-9)), (norm, dict(eps=float("nan"))), (norm, dict(eps=float("inf"))),
+    (norm, dict(M=-1)), (norm, dict(H=-8)), (norm, dict(M=0, eps=-1.0)),
+    (norm_bwd, dict(dy=None)), (norm_bwd, dict(x=None)), (norm_bwd, dict(mean=None)), (norm_bwd, dict(rstd=None)),
+    (norm_bwd, dict(rstd=P + 2)), (norm_bwd, dict(dx=P + 8)), (norm_bwd, dict(dw=P + 4)), (norm_bwd, dict(db=P + 4)),
+    (norm_bwd, dict(lddx=60)), (norm_bwd, dict(lddy=32)), (norm_bwd, dict(dt=3)), (norm_bwd, dict(xt=3)), (norm_bwd, dict(w=P + 4)),
+    (norm_bwd, dict(M=0, dw=P + 4)),
+    (grouped, dict(x=None)), (grouped, dict(w=None)), (grouped, dict(ends=None)), (grouped, dict(ends=P + 4)), (grouped, dict(y=None)),
+    (grouped, dict(sw=-8)), (grouped, dict(sw=2044)), (grouped, dict(sw=BIG)), (grouped, dict(ldx=63)), (grouped, dict(ldw=56)),
+    (grouped, dict(ldy=16)), (grouped, dict(yt=2)), (grouped, dict(T=-1)), (grouped, dict(E=-1)), (grouped, dict(x=P + 2)),
+    (grouped_bwd, dict(dy=None)), (grouped_bwd, dict(x=None)), (grouped_bwd, dict(w=None)), (grouped_bwd, dict(ends=None)),
+    (grouped_bwd, dict(sw=4)), (grouped_bwd, dict(sdw=2040)), (grouped_bwd, dict(sdw=2050)), (grouped_bwd, dict(dt=7)),
+    (grouped_bwd, dict(lddx=56)), (grouped_bwd, dict(lddw=32)), (grouped_bwd, dict(lddy=8)), (grouped_bwd, dict(T=0, dw=P + 4)),
+    (grouped_bwd, dict(T=0, ends=None)), (grouped_bwd, dict(dx=P + 8)),
+    (quantize, dict(x=None)), (quantize, dict(q=None)), (quantize, dict(s=None)), (quantize, dict(s=P + 2)), (quantize, dict(q=P + 8)),
+    (quantize, dict(ldq=72)), (quantize, dict(ldq=48)), (quantize, dict(dt=4)), (quantize, dict(ldx=60)), (quantize, dict(rows=-2)),
+    (int8, dict(xq=None)), (int8, dict(xs=None)), (int8, dict(wq=None)), (int8, dict(ws=None)), (int8, dict(ws=P + 4)),
+    (int8, dict(xs=P + 2)), (int8, dict(b=P + 4)), (int8, dict(y=P + 8)), (int8, dict(ldxq=72)), (int8, dict(ldwq=32)),
+    (int8, dict(ldy=24)), (int8, dict(dt=2)), (int8, dict(M=-1)),
+    (grouped_int8, dict(xq=None)), (grouped_int8, dict(xs=None)), (grouped_int8, dict(ws=None)), (grouped_int8, dict(ends=None)),
+    (grouped_int8, dict(sw=2056)), (grouped_int8, dict(ss=30)), (grouped_int8, dict(ss=-4)), (grouped_int8, dict(ldy=8)),
+    (grouped_int8, dict(dt=2)), (grouped_int8, dict(E=-4)),
+]
+
+
+def ids(v):
+    return v.__name__ if callable(v) else "-".join(map(str, v))
+
+
+@pytest.mark.parametrize("fn,kw", INVALID, ids=ids)
+def test_invalid_arguments(fn, kw):
+    assert fn(**kw) == bi.BI_EINVAL
+
+
+UNSUPPORTED = [
+    (norm, dict(H=60)), (norm, dict(H=0)), (norm, dict(H=16392, ldx=16392, ldy=16392)), (norm, dict(M=(1 << 30) + 1)),
+    (norm_bwd, dict(H=4)), (norm_bwd, dict(H=16392)),
+    (grouped, dict(E=0)), (grouped, dict(E=1025)), (grouped, dict(N=24)), (grouped, dict(K=48)), (grouped, dict(N=0)),
+    (grouped, dict(T=(1 << 30) + 1)), (grouped, dict(ldx=1 << 32)), (grouped, dict(ldw=1 << 32)),
+    (grouped_bwd, dict(E=0)), (grouped_bwd, dict(E=2000)), (grouped_bwd, dict(N=8)), (grouped_bwd, dict(K=16)),
+    (grouped_bwd, dict(ldw=1 << 32)), (grouped_bwd, dict(ldx=1 << 32)), (grouped_bwd, dict(lddy=1 << 32)),
+    (quantize, dict(K=48)), (int8, dict(K=80)), (int8, dict(N=8)), (int8, dict(ldxq=1 << 32)),
+    (int8, dict(K=131072, ldxq=131072, ldwq=131072)), (grouped_int8, dict(K=131072, ldxq=131072, ldwq=131072)),
+    (grouped_int8, dict(E=0)), (grouped_int8, dict(E=1025)), (grouped_int8, dict(ldwq=1 << 32)),
+]
+
+
+@pytest.mark.parametrize("fn,kw", UNSUPPORTED, ids=ids)
+def test_unsupported_sizes(fn, kw):
+    assert fn(**kw) == bi.BI_EUNSUPPORTED
+
+
+def test_more_workgroups_than_a_launch_holds():
+    T = 1 << 30
+    assert int8(M=T, N=16, K=32, ldy=16) == bi.BI_EUNSUPPORTED
+    assert grouped(T=T, N=32, E=1024) == bi.BI_EUNSUPPORTED
+    assert grouped_int8(T=T, N=32, E=1024) == bi.BI_EUNSUPPORTED
+    assert grouped_bwd(T=T, dw=None) == bi.BI_EUNSUPPORTED
+    # dw alone: 1024 experts of 512 x 512 tiles of 256 x 256 and more
+    n = 1 << 18
+    assert grouped_bwd(dx=None, E=1024, N=n, K=n, lddy=n, ldx=n, lddw=n, sdw=n * n) == bi.BI_EUNSUPPORTED
+    # ... and beside a dx that would fit: nothing is enqueued, which without a GPU would be a HIP error
+    assert grouped_bwd(E=1024, N=n, K=n, lddy=n, ldx=n, ldw=n, lddx=n, lddw=n, sdw=n * n) == bi.BI_EUNSUPPORTED
+
+
+def test_nothing_to_do():
+    assert norm(M=0, x=None, y=None) == bi.BI_OK
+    assert norm_bwd(dx=None, dw=None, db=None) == norm_bwd(M=0, dw=None, db=None, ws=None) == bi.BI_OK
+    assert grouped(T=0, x=None, ends=None) == grouped_int8(T=0, xq=None, ends=None) == bi.BI_OK
+    assert grouped_bwd(dx=None, dw=None) == grouped_bwd(T=0, dw=None, ends=None) == bi.BI_OK
+    assert quantize(rows=0, x=None) == int8(M=0, xq=None) == bi.BI_OK
+
+
+def test_workspace_sizes_and_refusals():
+    need = L.bi_layer_norm_bwd_workspace_size(4, 64)
+    assert need > bi.WS_COUNTER_BYTES and (need - bi.WS_COUNTER_BYTES) % (2 * 64 * 4) == 0
+    assert norm_bwd(ws=None) == norm_bwd(n=need - 1) == norm_bwd(ws=P + 8) == bi.BI_EWORKSPACE
+    assert norm_bwd(dw=None, n=need - 1) == bi.BI_EWORKSPACE
+    for args in ((0, 64), (-1, 64), (4, 60), (4, 0), (4, 16392)):
+        assert L.bi_layer_norm_bwd_workspace_size(*args) == 0
+    # it does not grow with the batch for ever
+    assert L.bi_layer_norm_bwd_workspace_size(1 << 20, 4096) == L.bi_layer_norm_bwd_workspace_size(1 << 30, 4096)
+
+
+def test_tile_query_refusals():
+    out = (bi._I32 * 8)()
+    tile = L.bi_lab_grouped_tile
+    assert tile(4, 4, 4, 32, 64, 1, out) == tile(0, 0, 4, 32, 64, 1, out) == tile(0, 4, 4, 32, 64, 3, out) == bi.BI_EINVAL
+    assert tile(0, 4, 4, 32, 64, 1, None) == bi.BI_EINVAL
+    assert tile(0, 4, 4, 24, 64, 1, out) == tile(0, 4, 0, 32, 64, 1, out) == tile(0, 4, 1025, 32, 64, 1, out) == bi.BI_EUNSUPPORTED
+
+
+# ------------------------------------------------------------------- the binding
+
+
+def cpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def test_binding_refuses_before_it_enqueues():
+    x, w, ends = cpu(4, 64), cpu(2, 32, 64), cpu(2, dtype=torch.int64)
+    f, i8 = cpu(4, dtype=torch.float32), torch.int8
+    for call in (lambda: bi.bi_layer_norm(x),                                          # not on a GPU
+                 lambda: bi.bi_layer_norm(cpu(64)), lambda: bi.bi_layer_norm(cpu(4, 60)),
+                 lambda: bi.bi_layer_norm(cpu(4, 16392)), lambda: bi.bi_layer_norm(cpu(4, 0)),
+                 lambda: bi.bi_layer_norm_bwd(cpu(64), x, f, f), lambda: bi.bi_layer_norm_bwd(cpu(4, 12), cpu(4, 12), f, f),
+                 lambda: bi.bi_grouped_linear_bf16(x, w, ends),
+                 lambda: bi.bi_grouped_linear_bf16(x, cpu(32, 64), ends),              # 2-D w
+                 lambda: bi.bi_grouped_linear_bf16(cpu(64), w, ends),
+                 lambda: bi.bi_grouped_linear_bf16(x, cpu(0, 32, 64), ends),
+                 lambda: bi.bi_grouped_linear_bf16(x, cpu(2, 24, 64), ends),
+                 lambda: bi.bi_grouped_linear_bf16(cpu(4, 48), cpu(2, 32, 48), ends),
+                 lambda: bi.bi_grouped_linear_bf16_bwd(x, None, cpu(2, 64, 32), ends),          # dw without x
+                 lambda: bi.bi_grouped_linear_bf16_bwd(x, x, None, ends),                       # dx without w
+                 lambda: bi.bi_grouped_linear_bf16_bwd(x, x, cpu(64, 32), ends),
+                 lambda: bi.bi_grouped_linear_bf16_bwd(x, x, cpu(2, 64, 32), cpu(2, 1, dtype=torch.int64)),
+                 lambda: bi.bi_quantize_int8(x), lambda: bi.bi_quantize_int8(cpu(64)), lambda: bi.bi_quantize_int8(cpu(4, 48)),
+                 lambda: bi.bi_linear_int8(cpu(4, 64, dtype=i8), f, cpu(32, 64, dtype=i8), f),
+                 lambda: bi.bi_linear_int8(cpu(64, dtype=i8), f, cpu(32, 64, dtype=i8), f),
+                 lambda: bi.bi_linear_int8(cpu(1, 131072, dtype=i8), f, cpu(16, 131072, dtype=i8), f),
+                 lambda: bi.bi_grouped_linear_int8(cpu(4, 64, dtype=i8), f, cpu(2, 32, 64, dtype=i8), f, ends),
+                 lambda: bi.bi_grouped_linear_int8(cpu(4, 64, dtype=i8), f, cpu(32, 64, dtype=i8), f, ends)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: bi.bi_layer_norm(cpu(4, 64, dtype=torch.float16)),
+                 lambda: bi.bi_layer_norm(x, out_dtype=torch.float64),
+                 lambda: bi.bi_layer_norm_bwd(cpu(4, 64, dtype=torch.float64), x, f, f),
+                 lambda: bi.bi_grouped_linear_bf16_bwd(x, x, cpu(2, 64, 64), ends, dw_dtype=torch.float16),
+                 lambda: bi.bi_grouped_linear_bf16(x.float(), w, ends),
+                 lambda: bi.bi_quantize_int8(cpu(4, 64, dtype=torch.float16)),
+                 lambda: bi.bi_linear_int8(cpu(4, 64, dtype=i8), f, cpu(32, 64, dtype=i8), f, out_dtype=torch.int32)):
+        with pytest.raises(TypeError):
+            call()
+
+
+# ----------------------------------------------------------------- the references
+
+
+def test_norm_reference_against_differences():
+    g = torch.Generator().manual_seed(0)
+    M, H, eps = 3, 8, 1e-5
+    x, w, b, dy = (torch.randn(s, generator=g, dtype=torch.float64) for s in ((M, H), (H,), (H,), (M, H)))
+
+    def value():
+        return float((ref.norm(x, w, b, eps, torch.float32)[0] * dy).sum())
+
+    _, m, r, *_ = ref.norm(x, w, b, eps, torch.float32)
+    dx, dw, db, *_ = ref.norm_bwd(dy, x, m, r, w, torch.float32)
+    e = 1e-6
+    for t, grad in ((x, dx), (w, dw), (b, db)):
+        for i in range(t.numel()):
+            keep = float(t.view(-1)[i])
+            t.view(-1)[i] = keep + e
+            up = value()
+            t.view(-1)[i] = keep - e
+            down = value()
+            t.view(-1)[i] = keep
+            assert abs((up - down) / (2 * e) - float(grad.view(-1)[i])) < 1e-7
+
+
+def test_codes_by_hand():
+    x = torch.tensor([[127.0, 0.5, 1.5, -2.5, 2.500001, -0.49999, 126.5, -127.0],        # scale 1
+                      [0.0] * 8,
+                      [1.0, float("inf"), 0, 0, 0, 0, 0, 0],
+                      [2.0 ** -140, 0, 0, 0, 0, 0, 0, 0]])                                # far below the least scale
+    q, s = ref.codes(x)
+    assert q[0].tolist() == [127, 0, 2, -2, 3, 0, 126, -127] and s[0] == 1.0
+    assert not q[1].any() and s[1] == 2.0 ** -126
+    assert not q[2].any() and torch.isnan(s[2])
+    assert not q[3].any() and s[3] == 2.0 ** -126
+
+
+def test_spans_of_any_ends():
+    assert ref.spans([2, 2, 5], 6) == [(0, 2), (2, 2), (2, 5)]
+    assert ref.spans([3, 1, -7, 99], 6) == [(0, 3), (3, 3), (3, 3), (3, 6)]
