@@ -546,7 +546,8 @@ size_t bi_layer_norm_bwd_workspace_size(int64_t M, int64_t H)
 {
     if (check_norm(M, H, BI_F32, BI_F32) != BI_OK || M == 0)
         return 0;
-    return kDecodeCounterBytes + layer_norm_bwd_ws(M, H);
+    const size_t n = layer_norm_bwd_ws(M, H);
+    return n ? kDecodeCounterBytes + n : 0;
 }
 
 bi_status_t bi_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t lddy, const void* x, int32_t x_dtype, int64_t ldx,
@@ -568,10 +569,11 @@ bi_status_t bi_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t lddy, co
     if (!matrix_ok(dy, lddy, H, dtype_bytes(dy_dtype)) || !matrix_ok(x, ldx, H, xe) || !floats_ok(mean, 4) ||
         !floats_ok(rstd, 4) || (w && !aligned16(w)) || (dx && !matrix_ok(dx, lddx, H, xe)))
         return BI_EINVAL;
-    if ((dw || db) && (!ws || !aligned16(ws) || ws_bytes < bi_layer_norm_bwd_workspace_size(M, H)))
+    const size_t need = dw || db ? bi_layer_norm_bwd_workspace_size(M, H) : 0;
+    if (need && (!ws || !aligned16(ws) || ws_bytes < need))
         return BI_EWORKSPACE;
     return launch_layer_norm_bwd(dy, dy_dtype == BI_BF16, lddy, x, x_dtype == BI_BF16, ldx, mean, rstd, w, dx, lddx, dw, db, M, H,
-                                 reinterpret_cast<char*>(ws) + kDecodeCounterBytes, stream) == hipSuccess
+                                 need ? reinterpret_cast<char*>(ws) + kDecodeCounterBytes : nullptr, stream) == hipSuccess
                ? BI_OK
                : BI_EHIP;
 }

@@ -6,9 +6,16 @@
 //
 // A row stays in the registers of its team of T threads, so that it is read once
 // and the variance is taken about the mean (no difference of large sums).  T and
-// the P chunks of eight values per thread follow from H alone, and with them the
-// order of every sum over a row: a thread's values in ascending order, then the
+// the P chunks of eight values per thread follow from H and the types alone, and
+// with them the order of every sum over a row: a thread's chunks one by one, the
 // lanes of a wave as a butterfly, then the waves in order.
+//
+// Both passes are bound by memory as long as a row's loads are on their way while
+// the row before is worked on: loads are made by every lane (past the row's end of
+// its last chunk, past the last row of that row), since a load under a condition is
+// waited for where the condition ends.
+#include <type_traits>
+
 #include "bi_ffn.h"
 #include "bi_plan.h"
 #include "bi_tile.h"
@@ -21,7 +28,7 @@ struct RowRaw {
     static constexpr int V = BF ? 1 : 2;
     u32x4 v[P * V];
 
-    // thread t of T: chunks t, t + T, ...; zero past the row's end
+    // thread t of T: chunks t, t + T, ...
     template <int T>
     __device__ __forceinline__ void load(const void* x, int64_t at, int t, int chunks)
     {
@@ -29,11 +36,8 @@ struct RowRaw {
 #pragma unroll
         for (int i = 0; i < P; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[i * V + j] = u32x4{0u, 0u, 0u, 0u};
-                if (i * T + t < chunks)
-                    v[i * V + j] = p[(i * T + t) * V + j];
-            }
+            for (int j = 0; j < V; ++j)
+                v[i * V + j] = p[min(i * T + t, chunks - 1) * V + j];
     }
     __device__ __forceinline__ float at(int i, int j) const     // value j of chunk i
     {
@@ -44,19 +48,62 @@ struct RowRaw {
             return __uint_as_float(v[2 * i + (j >> 2)][j & 3]);
         }
     }
+    __device__ __forceinline__ void set(int i, const float (&f)[8])    // chunk i, rounded to nearest even
+    {
+        if constexpr (BF) {
+            v[i] = u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+        } else {
+            v[2 * i] = __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]});
+            v[2 * i + 1] = __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]});
+        }
+    }
+    template <int T>
+    __device__ __forceinline__ void store(void* y, int64_t at, int t, int chunks) const
+    {
+        u32x4* p = reinterpret_cast<u32x4*>(reinterpret_cast<unsigned char*>(y) + at * (BF ? 2 : 4));
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (i * T + t < chunks) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    p[(i * T + t) * V + j] = v[i * V + j];
+            }
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < P * V; ++i)
+            v[i] = u32x4{0u, 0u, 0u, 0u};
+    }
 };
 
-template <bool BF>
-__device__ __forceinline__ void store8(void* y, int64_t at, const float (&v)[8])
+// w or b of a thread's chunks; `none` where there is no such vector.
+template <int T, int P>
+__device__ __forceinline__ void load_vector(const float* w, float none, int t, int chunks, float (&v)[P][8])
 {
-    if constexpr (BF) {
-        *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(y) + at) =
-            u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
-    } else {
-        f32x4* p = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(y) + at);
-        p[0] = f32x4{v[0], v[1], v[2], v[3]};
-        p[1] = f32x4{v[4], v[5], v[6], v[7]};
-    }
+    RowRaw<false, P> raw;
+    if (w)
+        raw.template load<T>(w, 0, t, chunks);
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[i][j] = w ? raw.at(i, j) : none;
+}
+
+// The sum over a wave, in every lane: a butterfly within each row of 16 lanes, then
+// the four rows in pairs.
+__device__ __forceinline__ float wave_sum(float v)
+{
+    auto moved = [](float f, auto ctrl) __attribute__((always_inline)) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(f), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    v += moved(v, std::integral_constant<int, 0xB1>{});         // lanes 1 apart
+    v += moved(v, std::integral_constant<int, 0x4E>{});         // 2 apart
+    v += moved(v, std::integral_constant<int, 0x141>{});        // the other four of eight
+    v += moved(v, std::integral_constant<int, 0x140>{});        // the other eight of sixteen
+    auto row = [&](int r) __attribute__((always_inline)) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16 * r)); };
+    return (row(0) + row(1)) + (row(2) + row(3));
 }
 
 // Sums of K values over teams of T threads.  Two buffers in turn: a wave that
@@ -64,41 +111,40 @@ __device__ __forceinline__ void store8(void* y, int64_t at, const float (&v)[8])
 template <int T, int TEAMS, int K>
 struct TeamSum {
     static constexpr int W = T / 64;
-    float (*buf)[TEAMS][W][K];
+    float (*buf)[TEAMS][K][W];
     int turn = 0;
 
     __device__ __forceinline__ void operator()(float (&s)[K])
     {
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1)
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                s[k] += __shfl_xor(s[k], d);
+        for (int k = 0; k < K; ++k)
+            s[k] = wave_sum(s[k]);
         if constexpr (W > 1) {
             const int team = threadIdx.x / T, wave = threadIdx.x % T / 64;
             if ((threadIdx.x & 63) == 0) {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    buf[turn][team][wave][k] = s[k];
+                    buf[turn][team][k][wave] = s[k];
             }
-            __syncthreads();
+            // no __syncthreads: its fence would wait for the loads of the next row
+            wg_barrier_reads_done();
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                s[k] = buf[turn][team][0][k];
+            for (int k = 0; k < K; ++k) {
+                s[k] = buf[turn][team][k][0];
 #pragma unroll
-            for (int w = 1; w < W; ++w)
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    s[k] += buf[turn][team][w][k];
+                for (int w = 1; w < W; ++w)
+                    s[k] += buf[turn][team][k][w];
+            }
             turn ^= 1;
         }
     }
 };
 
-// Squares are added scaled by 1 / kNormMaxH, a power of two: their sum overflows
-// only where the variance itself does.
-constexpr float kSquareScale = 1.0f / 16384.0f;
-static_assert(kNormMaxH == 16384, "the scale");
+// Differences from the mean are held scaled by 2^-7, a power of two that loses
+// nothing: their squares then add up to the variance times H / 16384, which
+// overflows only where the variance itself does.
+constexpr float kDiffScale = 1.0f / 128.0f;
+static_assert(kNormMaxH == 128 * 128, "the scale");
 
 struct NormArgs {
     const void* x;
@@ -117,57 +163,58 @@ struct NormArgs {
 template <bool XB, bool YB, int T, int P, int TEAMS>
 __global__ __launch_bounds__(T * TEAMS) void k_layer_norm(NormArgs p)
 {
-    __shared__ float buf[2][TEAMS][T / 64][1];
+    __shared__ __attribute__((aligned(16))) float buf[2][TEAMS][1][T / 64];
     TeamSum<T, TEAMS, 1> sum{buf};
-    const int t = threadIdx.x % T, team = threadIdx.x / T, chunks = p.H / 8;
-    float w[P][8], b[P][8];
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const bool in = i * T + t < chunks;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            w[i][j] = p.w && in ? p.w[(i * T + t) * 8 + j] : 1.f;
-            b[i][j] = p.b && in ? p.b[(i * T + t) * 8 + j] : 0.f;
-        }
-    }
-    const float h = (float)p.H;
+    const int t = threadIdx.x % T, team = (int)uniform(threadIdx.x / T), chunks = p.H / 8;
     const int64_t step = (int64_t)gridDim.x * TEAMS;
     int64_t m = (int64_t)blockIdx.x * TEAMS + team;
     RowRaw<XB, P> cur, next;
     cur.template load<T>(p.x, min(m, p.M - 1) * p.ldx, t, chunks);
+    float w[P][8], b[P][8];
+    load_vector<T, P>(p.w, 1.f, t, chunks, w);
+    load_vector<T, P>(p.b, 0.f, t, chunks, b);
+    const float h = (float)p.H;
     for (int64_t m0 = (int64_t)blockIdx.x * TEAMS; m0 < p.M; m0 += step, m += step) {
-        if (m0 + step < p.M)
-            next.template load<T>(p.x, min(m + step, p.M - 1) * p.ldx, t, chunks);
+        next.template load<T>(p.x, min(m + step, p.M - 1) * p.ldx, t, chunks);
         float s[1] = {0.f};
 #pragma unroll
-        for (int i = 0; i < P; ++i)
+        for (int i = 0; i < P; ++i) {
+            float c = cur.at(i, 0);
+#pragma unroll
+            for (int j = 1; j < 8; ++j)
+                c += cur.at(i, j);
+            s[0] += i * T + t < chunks ? c : 0.f;
+        }
+        sum(s);
+        const float mean = s[0] / h, off = -mean * kDiffScale;
+        float q[1] = {0.f};
+        float d[P][8];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float c = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                d[i][j] = __builtin_fmaf(cur.at(i, j), kDiffScale, off);
+                c = __builtin_fmaf(d[i][j], d[i][j], c);
+            }
+            q[0] += i * T + t < chunks ? c : 0.f;
+        }
+        sum(q);
+        const float rstd = 1.f / sqrtf(q[0] / (h * (kDiffScale * kDiffScale)) + p.eps), back = rstd * (1.f / kDiffScale);
+        RowRaw<YB, P> out;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float o[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                s[0] += cur.at(i, j);
-        sum(s);
-        const float mean = s[0] / h;
-        float q[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (i * T + t < chunks) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float d = cur.at(i, j) - mean;
-                    q[0] += d * (d * kSquareScale);
-                }
-            }
-        sum(q);
-        const float rstd = 1.f / sqrtf(q[0] / (h * kSquareScale) + p.eps);
+                o[j] = __builtin_fmaf(d[i][j] * back, w[i][j], b[i][j]);
+            out.set(i, o);
+        }
+        // the next row is waited for here, before the stores, and not with them
+        cur = next;
+        __builtin_amdgcn_sched_barrier(0);
         if (m < p.M) {
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-                if (i * T + t < chunks) {
-                    float o[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        o[j] = (cur.at(i, j) - mean) * rstd * w[i][j] + b[i][j];
-                    store8<YB>(p.y, m * p.ldy + (i * T + t) * 8, o);
-                }
+            out.template store<T>(p.y, m * p.ldy, t, chunks);
             if (t == 0) {
                 if (p.mean)
                     p.mean[m] = mean;
@@ -175,7 +222,6 @@ __global__ __launch_bounds__(T * TEAMS) void k_layer_norm(NormArgs p)
                     p.rstd[m] = rstd;
             }
         }
-        cur = next;
     }
 }
 
@@ -190,6 +236,8 @@ struct NormBwdArgs {
     void* dx;                   // or nullptr
     int64_t lddx;
     float* part;                // [workgroup][2][H] sums of dy n and of dy, or nullptr
+    float* dw;                  // where one workgroup does it all: [H] or nullptr
+    float* db;
     int64_t M;
     int H;
 };
@@ -197,75 +245,81 @@ struct NormBwdArgs {
 template <bool DB, bool XB, int T, int P, int TEAMS>
 __global__ __launch_bounds__(T * TEAMS) void k_layer_norm_bwd(NormBwdArgs p)
 {
-    __shared__ float buf[2][TEAMS][T / 64][2];
+    __shared__ __attribute__((aligned(16))) float buf[2][TEAMS][2][T / 64];
     __shared__ float fold[TEAMS > 1 ? T * 8 * P : 1];
+    constexpr bool kAhead = P <= 2;                     // longer rows leave no registers for the next one
     TeamSum<T, TEAMS, 2> sum{buf};
-    const int t = threadIdx.x % T, team = threadIdx.x / T, chunks = p.H / 8;
-    float w[P][8], dw[P][8] = {}, db[P][8] = {};
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const bool in = i * T + t < chunks;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w[i][j] = p.w && in ? p.w[(i * T + t) * 8 + j] : 1.f;
-    }
-    const float h = (float)p.H;
+    const int t = threadIdx.x % T, team = (int)uniform(threadIdx.x / T), chunks = p.H / 8;
     const int64_t step = (int64_t)gridDim.x * TEAMS;
     int64_t m = (int64_t)blockIdx.x * TEAMS + team;
     RowRaw<XB, P> x, xn;
     RowRaw<DB, P> d, dn;
     float mean, rstd, meann, rstdn;
-    x.template load<T>(p.x, min(m, p.M - 1) * p.ldx, t, chunks);
-    d.template load<T>(p.dy, min(m, p.M - 1) * p.lddy, t, chunks);
-    mean = p.mean[min(m, p.M - 1)];
-    rstd = p.rstd[min(m, p.M - 1)];
+    auto load = [&](int64_t row, RowRaw<XB, P>& xr, RowRaw<DB, P>& dr, float& mr, float& rr) __attribute__((always_inline)) {
+        row = min(row, p.M - 1);
+        xr.template load<T>(p.x, row * p.ldx, t, chunks);
+        dr.template load<T>(p.dy, row * p.lddy, t, chunks);
+        mr = p.mean[row];
+        rr = p.rstd[row];
+    };
+    if constexpr (kAhead)
+        load(m, x, d, mean, rstd);
+    float w[P][8], dw[P][8] = {}, db[P][8] = {};
+    load_vector<T, P>(p.w, 1.f, t, chunks, w);
+    const float h = (float)p.H;
     for (int64_t m0 = (int64_t)blockIdx.x * TEAMS; m0 < p.M; m0 += step, m += step) {
-        if (m0 + step < p.M) {
-            const int64_t to = min(m + step, p.M - 1);
-            xn.template load<T>(p.x, to * p.ldx, t, chunks);
-            dn.template load<T>(p.dy, to * p.lddy, t, chunks);
-            meann = p.mean[to];
-            rstdn = p.rstd[to];
-        }
+        if constexpr (kAhead)
+            load(m + step, xn, dn, meann, rstdn);
+        else
+            load(m, x, d, mean, rstd);
+        // a team without a row works on zeros, which add nothing to dw and db
         const bool live = m < p.M;
+        if (!live) {
+            x.clear();
+            d.clear();
+            mean = rstd = 0.f;
+        }
         float s[2] = {0.f, 0.f};
+        auto norm = [&](int i, int j) __attribute__((always_inline)) { return (x.at(i, j) - mean) * rstd; };
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (i * T + t < chunks) {
+        for (int i = 0; i < P; ++i) {
+            float c0 = 0.f, c1 = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float dy = d.at(i, j), n = (x.at(i, j) - mean) * rstd, g = dy * w[i][j];
-                    s[0] += g;
-                    s[1] += g * n;
-                    if (live) {
-                        dw[i][j] += dy * n;
-                        db[i][j] += dy;
-                    }
-                }
+            for (int j = 0; j < 8; ++j) {
+                const float dy = d.at(i, j), g = dy * w[i][j], n = norm(i, j);
+                c0 += g;
+                c1 = __builtin_fmaf(g, n, c1);
+                dw[i][j] = __builtin_fmaf(dy, n, dw[i][j]);
+                db[i][j] += dy;
             }
+            s[0] += i * T + t < chunks ? c0 : 0.f;
+            s[1] += i * T + t < chunks ? c1 : 0.f;
+        }
+        RowRaw<XB, P> out;
         if (p.dx) {
             sum(s);
             const float c0 = s[0] / h, c1 = s[1] / h;
-            if (live) {
 #pragma unroll
-                for (int i = 0; i < P; ++i)
-                    if (i * T + t < chunks) {
-                        float o[8];
+            for (int i = 0; i < P; ++i) {
+                float o[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float n = (x.at(i, j) - mean) * rstd;
-                            o[j] = rstd * (d.at(i, j) * w[i][j] - (c0 + n * c1));
-                        }
-                        store8<XB>(p.dx, m * p.lddx + (i * T + t) * 8, o);
-                    }
+                for (int j = 0; j < 8; ++j)
+                    o[j] = rstd * (d.at(i, j) * w[i][j] - __builtin_fmaf(norm(i, j), c1, c0));
+                out.set(i, o);
             }
         }
-        x = xn;
-        d = dn;
-        mean = meann;
-        rstd = rstdn;
+        // the next row is waited for here, before the stores, and not with them
+        if constexpr (kAhead) {
+            x = xn;
+            d = dn;
+            mean = meann;
+            rstd = rstdn;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (p.dx && live)
+            out.template store<T>(p.dx, m * p.lddx, t, chunks);
     }
-    if (!p.part)
+    if (!p.part && !p.dw && !p.db)
         return;
     // the teams' sums in order, then the workgroup's partial
     auto out = [&](float (&a)[P][8], int which) __attribute__((always_inline)) {
@@ -290,36 +344,46 @@ __global__ __launch_bounds__(T * TEAMS) void k_layer_norm_bwd(NormBwdArgs p)
             }
         }
         if (team == 0) {
+            RowRaw<false, P> sums;
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                if (i * T + t < chunks)
-                    store8<false>(p.part, ((int64_t)blockIdx.x * 2 + which) * p.H + (i * T + t) * 8, a[i]);
+                sums.set(i, a[i]);
+            if (p.part)
+                sums.template store<T>(p.part, ((int64_t)blockIdx.x * 2 + which) * p.H, t, chunks);
+            else if (float* to = which ? p.db : p.dw)
+                sums.template store<T>(to, 0, t, chunks);
         }
     };
     out(dw, 0);
     out(db, 1);
 }
 
-// dw and db from G partials: a workgroup takes 64 of the 2 H columns, 16 threads
-// of four columns by 16 slices of the partials; a slice's partials are added in
-// order, then the slices.
+// dw and db from G <= 256 partials: a workgroup takes 32 of the 2 H columns, 8
+// threads of four columns by 32 slices of the partials; a slice's partials (all on
+// their way at once) are added in order, then the slices.
+constexpr int kFoldSlices = 32, kFoldPer = 256 / kFoldSlices;
+
 __global__ __launch_bounds__(256) void k_layer_norm_fold(const float* __restrict__ part, float* __restrict__ dw,
                                                          float* __restrict__ db, int G, int H)
 {
-    __shared__ f32x4 acc[16][16];
-    const int cl = threadIdx.x & 15, sl = threadIdx.x >> 4;
-    const int c = blockIdx.x * 64 + cl * 4;
+    __shared__ f32x4 acc[kFoldSlices][8];
+    const int cl = threadIdx.x & 7, sl = threadIdx.x >> 3;
+    const int c = blockIdx.x * 32 + cl * 4, at = min(c, 2 * H - 4);
+    const int per = (G + kFoldSlices - 1) / kFoldSlices, first = sl * per;
+    f32x4 v[kFoldPer];
+#pragma unroll
+    for (int k = 0; k < kFoldPer; ++k)
+        v[k] = *reinterpret_cast<const f32x4*>(part + (int64_t)min(first + k, G - 1) * 2 * H + at);
     f32x4 a = {0.f, 0.f, 0.f, 0.f};
-    if (c < 2 * H) {
-        const int per = (G + 15) / 16, to = min((sl + 1) * per, G);
-#pragma unroll 4
-        for (int k = sl * per; k < to; ++k)
-            a += *reinterpret_cast<const f32x4*>(part + (int64_t)k * 2 * H + c);
-    }
+#pragma unroll
+    for (int k = 0; k < kFoldPer; ++k)
+        if (k < per && first + k < G)
+            a += v[k];
     acc[sl][cl] = a;
     __syncthreads();
     if (sl == 0 && c < 2 * H) {
-        for (int k = 1; k < 16; ++k)
+#pragma unroll
+        for (int k = 1; k < kFoldSlices; ++k)
             a += acc[k][cl];
         float* to = c < H ? dw : db;
         if (to)
@@ -327,21 +391,23 @@ __global__ __launch_bounds__(256) void k_layer_norm_fold(const float* __restrict
     }
 }
 
-// f(T, P, rows per workgroup) of a row length
+// f(T, P) of a row length
 template <typename F>
 static void norm_shape(int64_t H, F f)
 {
     using std::integral_constant;
     if (H <= 512)
-        f(integral_constant<int, 64>{}, integral_constant<int, 1>{}, integral_constant<int, 4>{});
+        f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (H <= 1024)
+        f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
     else if (H <= 2048)
-        f(integral_constant<int, 256>{}, integral_constant<int, 1>{}, integral_constant<int, 1>{});
+        f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
     else if (H <= 4096)
-        f(integral_constant<int, 256>{}, integral_constant<int, 2>{}, integral_constant<int, 1>{});
+        f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
     else if (H <= 8192)
-        f(integral_constant<int, 512>{}, integral_constant<int, 2>{}, integral_constant<int, 1>{});
+        f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
     else
-        f(integral_constant<int, 1024>{}, integral_constant<int, 2>{}, integral_constant<int, 1>{});
+        f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
 }
 
 template <typename F>
@@ -358,8 +424,9 @@ hipError_t launch_layer_norm(const void* x, int x_bf16, int64_t ldx, const float
 {
     const NormArgs p{x, ldx, w, b, eps, y, ldy, mean, rstd, M, (int)H};
     two_types(x_bf16, y_bf16, [&](auto xb, auto yb) {
-        norm_shape(H, [&](auto T, auto P, auto R) {
-            const int64_t groups = (M + R - 1) / R, most = (int64_t)device_cu_count() * (2048 / (T * R));
+        norm_shape(H, [&](auto T, auto P) {
+            constexpr int R = T < 256 ? 256 / T : 1;
+            const int64_t groups = (M + R - 1) / R, most = (int64_t)device_cu_count() * (1536 / (T * R));
             k_layer_norm<decltype(xb)::value, decltype(yb)::value, T, P, R>
                 <<<(unsigned)(groups < most ? groups : most), T * R, 0, s>>>(p);
         });
@@ -367,36 +434,47 @@ hipError_t launch_layer_norm(const void* x, int x_bf16, int64_t ldx, const float
     return hipGetLastError();
 }
 
-// Workgroups of the backward pass, each with a partial of dw and db.
+// The backward pass runs on at most 256 workgroups of 512 threads, one per compute
+// unit, each with a partial of dw and db.  Up to four rows a team are left to one
+// workgroup, which needs no second launch (4 us) to add partials.
+constexpr int kBwdThreads = 512;
+
 static int64_t bwd_groups(int64_t M, int64_t rows)
 {
     const int64_t groups = (M + rows - 1) / rows;
-    return groups < 256 ? groups : 256;
+    return groups <= 4 ? 1 : groups < 256 ? groups : 256;
 }
 
-static int64_t bwd_rows(int64_t H)
+size_t layer_norm_bwd_ws(int64_t M, int64_t H)
 {
-    return H <= 512 ? 16 : H <= 4096 ? 4 : H <= 8192 ? 2 : 1;
+    int64_t groups = 0;
+    norm_shape(H, [&](auto T, auto) { groups = bwd_groups(M, kBwdThreads / T); });
+    return groups > 1 ? (size_t)groups * 2 * (size_t)H * 4 : 0;
 }
-
-size_t layer_norm_bwd_ws(int64_t M, int64_t H) { return (size_t)bwd_groups(M, bwd_rows(H)) * 2 * (size_t)H * 4; }
 
 hipError_t launch_layer_norm_bwd(const void* dy, int dy_bf16, int64_t lddy, const void* x, int x_bf16, int64_t ldx,
                                  const float* mean, const float* rstd, const float* w, void* dx, int64_t lddx, float* dw, float* db,
                                  int64_t M, int64_t H, void* ws, hipStream_t s)
 {
-    const bool sums = dw || db;
-    const NormBwdArgs p{dy, lddy, x, ldx, mean, rstd, w, dx, lddx, sums ? reinterpret_cast<float*>(ws) : nullptr, M, (int)H};
+    NormBwdArgs p{dy, lddy, x, ldx, mean, rstd, w, dx, lddx, nullptr, nullptr, nullptr, M, (int)H};
     int64_t groups = 0;
+    bool fold = false;
     two_types(dy_bf16, x_bf16, [&](auto yb, auto xb) {
-        norm_shape(H, [&](auto T, auto P, auto) {
-            constexpr int R = 1024 / T;
+        norm_shape(H, [&](auto T, auto P) {
+            constexpr int R = kBwdThreads / T;
             groups = bwd_groups(M, R);
-            k_layer_norm_bwd<decltype(yb)::value, decltype(xb)::value, T, P, R><<<(unsigned)groups, 1024, 0, s>>>(p);
+            fold = groups > 1 && (dw || db);
+            if (fold) {
+                p.part = reinterpret_cast<float*>(ws);
+            } else {
+                p.dw = dw;
+                p.db = db;
+            }
+            k_layer_norm_bwd<decltype(yb)::value, decltype(xb)::value, T, P, R><<<(unsigned)groups, kBwdThreads, 0, s>>>(p);
         });
     });
-    if (sums)
-        k_layer_norm_fold<<<(unsigned)((2 * H + 63) / 64), 256, 0, s>>>(p.part, dw, db, (int)groups, (int)H);
+    if (fold)
+        k_layer_norm_fold<<<(unsigned)((2 * H + 31) / 32), 256, 0, s>>>(p.part, dw, db, (int)groups, (int)H);
     return hipGetLastError();
 }
 

@@ -166,12 +166,13 @@ def test_outputs_in_place_and_untouched_surroundings(bi):
 def test_refusals_on_the_gpu(bi):
     x = rows(4, 64, 1, BF)
     s = torch.zeros(4, device="cuda")
+    many, ms = rows(100, 64, 1, BF), torch.zeros(100, device="cuda")        # enough rows to need a workspace
     for call in (lambda: bi.bi_layer_norm(x, vec(32, 1)), lambda: bi.bi_layer_norm(x, vec(64, 1).cpu()),
                  lambda: bi.bi_layer_norm(x, vec(128, 1)[::2]), lambda: bi.bi_layer_norm(x, vec(72, 1)[1:65]),
                  lambda: bi.bi_layer_norm(x, out=x[:3]), lambda: bi.bi_layer_norm(x.t().contiguous().t()),
                  lambda: bi.bi_layer_norm_bwd(x, x[:3], s, s), lambda: bi.bi_layer_norm_bwd(x, x, s[:3], s),
                  lambda: bi.bi_layer_norm_bwd(x, x.cpu(), s, s),
-                 lambda: bi.bi_layer_norm_bwd(x, x, s, s, ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))):
+                 lambda: bi.bi_layer_norm_bwd(many, many, ms, ms, ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(ValueError):
             call()
     for call in (lambda: bi.bi_layer_norm(x, vec(64, 1).to(BF)), lambda: bi.bi_layer_norm_bwd(x, x, s.double(), s)):
