@@ -32,25 +32,48 @@ __device__ __forceinline__ int wave_incl_max(int v, int lane)
     return max(max(v, row >= 1 ? r0 : 0), max(row >= 2 ? r1 : 0, row >= 3 ? r2 : 0));
 }
 
-// The end of expert e's rows as given, held to 0 .. T; 0 past the last expert.
-__device__ __forceinline__ int group_end(const GroupArgs& q, int e)
-{
-    if (e >= q.E)
-        return 0;
-    const int64_t v = q.ends[e];
-    return v < 0 ? 0 : v > q.T ? q.T : (int)v;
-}
+// The experts' rows, NE experts in a row to a lane: where the lane's first begins and
+// where each of its ends.  All of `ends` is asked for at once: a workgroup has nothing
+// to do until it knows its tile.  Ends are held to 0 .. T, and the running maximum makes
+// a partition of any values, so that none read or write out of range.
+template <int NE>
+struct GroupRows {
+    int from, end[NE];
 
-// 64 experts from e0 on, one to a lane: their first row and their number of
-// rows.  `from`: where the experts before them ended; moved on.  The running
-// maximum makes a partition of any values, so that no ends read or write out of range.
-__device__ __forceinline__ void group_rows(const GroupArgs& q, int e0, int lane, int& from, int& first, int& rows)
+    __device__ __forceinline__ GroupRows(const GroupArgs& q, int lane)
+    {
+        int64_t v[NE];
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            v[i] = q.ends[min(lane * NE + i, q.E - 1)];         // past the last expert: no rows
+        int top = 0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            top = max(top, (int)max(min(v[i], (int64_t)q.T), (int64_t)0));
+            end[i] = top;
+        }
+        const int before = __shfl_up(wave_incl_max(top, lane), 1);
+        from = lane == 0 ? 0 : before;
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            end[i] = max(end[i], from);
+    }
+    __device__ __forceinline__ int first(int i) const { return i == 0 ? from : end[i - 1]; }
+    __device__ __forceinline__ int rows(int i) const { return end[i] - first(i); }
+};
+
+// f(NE) of the fewest experts to a lane that hold E in a wave
+template <typename F>
+__device__ __forceinline__ void with_lanes(int E, F f)
 {
-    const int end = max(wave_incl_max(group_end(q, e0 + lane), lane), from);
-    const int before = __shfl_up(end, 1);
-    first = lane == 0 ? from : before;
-    rows = end - first;
-    from = __builtin_amdgcn_readlane(end, 63);
+    if (E <= 64)
+        f(std::integral_constant<int, 1>{});
+    else if (E <= 128)
+        f(std::integral_constant<int, 2>{});
+    else if (E <= 256)
+        f(std::integral_constant<int, 4>{});
+    else
+        f(std::integral_constant<int, kMaxExperts / 64>{});
 }
 
 struct GroupTile {
@@ -58,40 +81,70 @@ struct GroupTile {
     int tm, tn;                 // tile among the expert's
 };
 
-// The tile of workgroup w among all experts' BM-row tiles x tiles_n, dealt to the
-// XCDs as tile_of does; false where there is none.
+// The tile of workgroup w among all experts' BM-row tiles x tiles_n; false where there
+// is none.  Each XCD takes one contiguous eighth of the list, which goes expert by
+// expert, four row tiles at a time, column by column: tiles that share rows of A or of
+// the weight are then started one after the other, within the few microseconds for
+// which a line stays in the L2.  (Eight row tiles of several experts at a time, as
+// tile_of has it for one product, 32768 rows of 128 experts, 1536 x 2048: 316 us.)
 template <int BM>
 __device__ __forceinline__ bool find_tile(const GroupArgs& q, int tiles_n, int w, GroupTile& t)
 {
     const int lane = threadIdx.x & 63;
-    int from = 0, first, rows, total = 0;
-    for (int e0 = 0; e0 < q.E; e0 += 64) {
-        group_rows(q, e0, lane, from, first, rows);
-        total += __builtin_amdgcn_readlane((int)wave_incl_scan((uint32_t)((rows + BM - 1) / BM), lane), 63);
-    }
-    const int tiles = total * tiles_n;
-    const int x = w & 7, j = w >> 3;
-    const int per = tiles >> 3, more = tiles & 7;
-    if (j >= per + (x < more ? 1 : 0))
-        return false;
-    const int tr = tile_at(x * per + min(x, more) + j, total, tiles_n, t.tn);
-    int upto = 0;
-    from = 0;
-    for (int e0 = 0;; e0 += 64) {
-        group_rows(q, e0, lane, from, first, rows);
-        const int mine = (rows + BM - 1) / BM;
-        const int incl = upto + (int)wave_incl_scan((uint32_t)mine, lane);
-        const uint64_t past = __ballot(incl > tr);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            t.e = e0 + l;
-            t.first = __builtin_amdgcn_readlane(first, l);
-            t.rows = __builtin_amdgcn_readlane(rows, l);
-            t.tm = tr - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(mine, l));
-            return true;
+    bool found = false;
+    with_lanes(q.E, [&](auto ne) __attribute__((always_inline)) {
+        constexpr int NE = decltype(ne)::value;
+        const GroupRows<NE> r(q, lane);
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            mine += (r.rows(i) + BM - 1) / BM;
+        const int incl = (int)wave_incl_scan((uint32_t)mine, lane);
+        const int total = __builtin_amdgcn_readlane(incl, 63), tiles = total * tiles_n;
+        const int x = w & 7, j = w >> 3;
+        const int per = tiles >> 3, more = tiles & 7;
+        found = j < per + (x < more ? 1 : 0);
+        if (!found)
+            return;
+        const int at_tile = x * per + min(x, more) + j, tr = at_tile / tiles_n;
+        const int l = __builtin_ctzll(__ballot(incl > tr));     // the lane of the tile's expert
+        int at = incl - mine, e = 0, first = 0, rows = 0, before = 0;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int n = (r.rows(i) + BM - 1) / BM;
+            if (tr >= at && tr < at + n) {
+                e = lane * NE + i;
+                first = r.first(i);
+                rows = r.rows(i);
+                before = at;
+            }
+            at += n;
         }
-        upto = __builtin_amdgcn_readlane(incl, 63);
-    }
+        t.e = __builtin_amdgcn_readlane(e, l);
+        t.first = __builtin_amdgcn_readlane(first, l);
+        t.rows = __builtin_amdgcn_readlane(rows, l);
+        t.tm = tile_at<4>(at_tile - __builtin_amdgcn_readlane(before, l) * tiles_n, (t.rows + BM - 1) / BM, tiles_n, t.tn);
+    });
+    return found;
+}
+
+// Expert e's rows.
+__device__ __forceinline__ void rows_of(const GroupArgs& q, int e, int& first, int& rows)
+{
+    const int lane = threadIdx.x & 63;
+    with_lanes(q.E, [&](auto ne) __attribute__((always_inline)) {
+        constexpr int NE = decltype(ne)::value;
+        const GroupRows<NE> r(q, lane);
+        int f = r.first(0), n = r.rows(0);
+#pragma unroll
+        for (int i = 1; i < NE; ++i)
+            if (e % NE == i) {
+                f = r.first(i);
+                n = r.rows(i);
+            }
+        first = __builtin_amdgcn_readlane(f, e / NE);
+        rows = __builtin_amdgcn_readlane(n, e / NE);
+    });
 }
 
 // p at its expert's rows and weight
@@ -124,14 +177,13 @@ __global__ __launch_bounds__((S::C::NW + S::NL) * 64) void k_grouped_dw(TileArgs
     using C = typename S::C;
     __shared__ __attribute__((aligned(1024))) unsigned char ring[C::kRing];
     int tn;
-    const int tr = tile_of((int)blockIdx.x, q.E * p.tiles_m, p.tiles_n, tn);
-    const int e = tr / p.tiles_m, tm = tr - e * p.tiles_m;
-    const int lane = threadIdx.x & 63;
-    int from = 0, first, rows;
-    for (int e0 = 0; e0 <= e; e0 += 64)
-        group_rows(q, e0, lane, from, first, rows);
-    first = __builtin_amdgcn_readlane(first, e & 63);
-    rows = __builtin_amdgcn_readlane(rows, e & 63);
+    const int tiles = p.tiles_m * p.tiles_n, per = (tiles + 7) >> 3;
+    const int j = (int)blockIdx.x >> 3, e = j / per, t = (((int)blockIdx.x + e) & 7) * per + j - e * per;
+    if (t >= tiles)
+        return;
+    const int tm = tile_at(t, p.tiles_m, p.tiles_n, tn);
+    int first, rows;
+    rows_of(q, e, first, rows);
     const int es = p.y_bf16 ? 2 : 4;
     p.y = reinterpret_cast<unsigned char*>(p.y) + (int64_t)e * q.stride_b;
     if (rows == 0) {
@@ -154,24 +206,33 @@ __global__ __launch_bounds__((S::C::NW + S::NL) * 64) void k_grouped_dw(TileArgs
 
 template <int BM, int BN, int WM, int WN, int KB, int R, int NL_, bool CA, bool CB, TileType TYPE>
 struct GroupShape {
-    using C = TileCfg<BM, BN, WM, WN, KB, R, CA, CB, TYPE, kEpiLinear>;
+    using C = TileCfg<BM, BN, WM, WN, KB, R, CA, CB, TYPE, kEpiLinear, true>;
     static constexpr int NL = NL_;
 };
 
 enum GroupOp { kGroupBf16, kGroupInt8, kGroupDx, kGroupDw };
 
-// the costs are explained in bi_tile_rule.h; a slice is 32 k, in 8 bits 64
+// Costs as in bi_tile_rule.h (a slice is 32 k, in 8 bits 64), fitted to timings of 320
+// problems drawn over 1 to 128 experts, 1 to 32768 rows split evenly or not, widths 128 ..
+// 4096 and k 256 .. 4096: the shapes chosen take 1.013 to 1.018 times the fastest one's
+// time on average (fitted to one half of them, 1.018 to 1.032 on the other).  Each shape
+// left out of its list costs 0.4 to 10 percent on average and up to 12 to 150 at worst.
 static const TileShape kRowShapes[] = {
-    {16, 16, 0.67f, 0.037f, 1.10f}, {16, 32, 0.29f, 0.063f, 1.10f}, {32, 32, 0.64f, 0.072f, 1.10f}, {64, 32, 0.90f, 0.088f, 0.f},
-    {128, 64, 0.65f, 0.204f, 0.f},  {128, 128, 0.72f, 0.277f, 0.f}, {256, 256, 1.87f, 0.688f, 0.f},
+    {16, 16, 3.04f, 0.035f, 1.36f}, {16, 32, 2.18f, 0.072f, 0.85f}, {32, 64, 1.99f, 0.097f, 1.14f}, {32, 128, 1.83f, 0.125f, 1.32f},
+    {64, 128, 2.11f, 0.163f, 0.f},  {128, 128, 3.19f, 0.460f, 0.71f}, {256, 256, 3.89f, 0.753f, 0.f},
+};
+static const TileShape kRow8Shapes[] = {
+    {16, 16, 3.66f, 0.047f, 1.03f}, {16, 32, 2.65f, 0.086f, 0.66f}, {32, 64, 4.47f, 0.113f, 0.56f}, {32, 128, 2.81f, 0.182f, 0.99f},
+    {64, 128, 2.81f, 0.209f, 0.f},  {128, 128, 4.89f, 0.612f, 0.59f}, {256, 256, 7.00f, 0.875f, 0.f},
 };
 static const TileShape kDxShapes[] = {
-    {16, 32, 1.00f, 0.047f, 1.76f}, {32, 32, 1.17f, 0.054f, 1.13f}, {32, 64, 1.71f, 0.075f, 1.05f},
-    {128, 64, 1.38f, 0.154f, 0.f},  {128, 128, 1.61f, 0.231f, 0.f}, {256, 256, 3.29f, 0.554f, 0.f},
+    {16, 64, 3.48f, 0.103f, 0.96f}, {32, 32, 2.02f, 0.101f, 0.98f},  {64, 64, 1.98f, 0.128f, 1.14f},
+    {64, 128, 2.47f, 0.135f, 0.f},  {128, 128, 4.17f, 0.401f, 0.71f}, {256, 256, 8.38f, 0.694f, 0.f},
 };
 static const TileShape kDwShapes[] = {
-    {64, 64, 1.61f, 0.113f, 1.04f}, {128, 64, 2.34f, 0.165f, 0.f}, {128, 128, 2.88f, 0.235f, 0.f}, {256, 256, 6.22f, 0.590f, 0.f},
+    {64, 64, 3.52f, 0.209f, 0.56f}, {128, 128, 3.59f, 0.622f, 0.60f}, {256, 256, 7.84f, 0.973f, 0.f},
 };
+constexpr int kNumRowShapes = 7, kNumDxShapes = 6, kNumDwShapes = 3;
 
 // f of the shape at an index of the operator's list
 template <GroupOp OP, typename F>
@@ -182,26 +243,25 @@ static auto group_shape(int i, F f)
         switch (i) {
         case 0: return f(GroupShape<16, 16, 1, 1, 8, 4, 4, false, false, T>{});
         case 1: return f(GroupShape<16, 32, 1, 1, 4, 4, 4, false, false, T>{});
-        case 2: return f(GroupShape<32, 32, 2, 1, 4, 4, 4, false, false, T>{});
-        case 3: return f(GroupShape<64, 32, 4, 1, 4, 4, 4, false, false, T>{});
-        case 4: return f(GroupShape<128, 64, 4, 1, 2, 4, 0, false, false, T>{});
-        case 5: return f(GroupShape<128, 128, 4, 2, 2, 4, 0, false, false, T>{});
+        case 2: return f(GroupShape<32, 64, 2, 2, 4, 3, 4, false, false, T>{});
+        case 3: return f(GroupShape<32, 128, 1, 4, 2, 4, 4, false, false, T>{});
+        case 4: return f(GroupShape<64, 128, 2, 2, 2, 3, 4, false, false, T>{});
+        case 5: return f(GroupShape<128, 128, 4, 2, 2, 2, 0, false, false, T>{});
         default: return f(GroupShape<256, 256, 4, 2, 2, 2, 0, false, false, T>{});
         }
     } else if constexpr (OP == kGroupDx) {
         switch (i) {
-        case 0: return f(GroupShape<16, 32, 1, 2, 4, 4, 4, false, true, kBf16>{});
+        case 0: return f(GroupShape<16, 64, 1, 2, 4, 4, 4, false, true, kBf16>{});
         case 1: return f(GroupShape<32, 32, 2, 2, 4, 4, 4, false, true, kBf16>{});
-        case 2: return f(GroupShape<32, 64, 2, 2, 4, 3, 4, false, true, kBf16>{});
-        case 3: return f(GroupShape<128, 64, 4, 2, 2, 4, 0, false, true, kBf16>{});
-        case 4: return f(GroupShape<128, 128, 4, 2, 2, 4, 0, false, true, kBf16>{});
+        case 2: return f(GroupShape<64, 64, 2, 2, 2, 4, 4, false, true, kBf16>{});
+        case 3: return f(GroupShape<64, 128, 2, 2, 2, 3, 4, false, true, kBf16>{});
+        case 4: return f(GroupShape<128, 128, 2, 4, 2, 2, 0, false, true, kBf16>{});
         default: return f(GroupShape<256, 256, 2, 4, 2, 2, 0, false, true, kBf16>{});
         }
     } else {
         switch (i) {
         case 0: return f(GroupShape<64, 64, 4, 2, 2, 4, 0, true, true, kBf16>{});
-        case 1: return f(GroupShape<128, 64, 4, 2, 2, 4, 0, true, true, kBf16>{});
-        case 2: return f(GroupShape<128, 128, 4, 2, 2, 4, 0, true, true, kBf16>{});
+        case 1: return f(GroupShape<128, 128, 2, 2, 1, 4, 0, true, true, kBf16>{});
         default: return f(GroupShape<256, 256, 4, 2, 2, 2, 0, true, true, kBf16>{});
         }
     }
@@ -225,8 +285,8 @@ static int64_t likely_row_tiles(int64_t T, int64_t E, int bm)
 
 static int pick_group(GroupOp op, int64_t T, int64_t E, int64_t N, int64_t K, bool f32_out)
 {
-    const TileShape* t = op == kGroupDx ? kDxShapes : op == kGroupDw ? kDwShapes : kRowShapes;
-    const int n = op == kGroupDx ? 6 : op == kGroupDw ? 4 : 7, cus = device_cu_count();
+    const TileShape* t = op == kGroupDx ? kDxShapes : op == kGroupDw ? kDwShapes : op == kGroupInt8 ? kRow8Shapes : kRowShapes;
+    const int n = op == kGroupDx ? kNumDxShapes : op == kGroupDw ? kNumDwShapes : kNumRowShapes, cus = device_cu_count();
     int best = 0;
     float best_time = 0.f;
     for (int i = 0; i < n; ++i) {
@@ -286,7 +346,7 @@ static hipError_t run_dw(TileArgs a, const GroupArgs& q, int shape, hipStream_t 
         using C = typename S::C;
         a.tiles_m = (a.M + C::BM - 1) / C::BM;
         a.tiles_n = (a.N + C::BN - 1) / C::BN;
-        const int64_t tiles = (int64_t)q.E * a.tiles_m * a.tiles_n;
+        const int64_t tiles = ((int64_t)a.tiles_m * a.tiles_n + 7) / 8 * 8 * q.E;
         if (!grid_ok(tiles))
             return hipErrorInvalidConfiguration;
         if (dry)

@@ -14,68 +14,11 @@
 // the row before is worked on: loads are made by every lane (past the row's end of
 // its last chunk, past the last row of that row), since a load under a condition is
 // waited for where the condition ends.
-#include <type_traits>
-
 #include "bi_ffn.h"
 #include "bi_plan.h"
-#include "bi_tile.h"
+#include "bi_rows.h"
 
 namespace bi {
-
-// P chunks of eight values as they lie in memory.
-template <bool BF, int P>
-struct RowRaw {
-    static constexpr int V = BF ? 1 : 2;
-    u32x4 v[P * V];
-
-    // thread t of T: chunks t, t + T, ...
-    template <int T>
-    __device__ __forceinline__ void load(const void* x, int64_t at, int t, int chunks)
-    {
-        const u32x4* p = reinterpret_cast<const u32x4*>(reinterpret_cast<const unsigned char*>(x) + at * (BF ? 2 : 4));
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                v[i * V + j] = p[min(i * T + t, chunks - 1) * V + j];
-    }
-    __device__ __forceinline__ float at(int i, int j) const     // value j of chunk i
-    {
-        if constexpr (BF) {
-            const uint32_t u = v[i][j >> 1];
-            return __uint_as_float(j & 1 ? u & 0xffff0000u : u << 16);
-        } else {
-            return __uint_as_float(v[2 * i + (j >> 2)][j & 3]);
-        }
-    }
-    __device__ __forceinline__ void set(int i, const float (&f)[8])    // chunk i, rounded to nearest even
-    {
-        if constexpr (BF) {
-            v[i] = u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
-        } else {
-            v[2 * i] = __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]});
-            v[2 * i + 1] = __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]});
-        }
-    }
-    template <int T>
-    __device__ __forceinline__ void store(void* y, int64_t at, int t, int chunks) const
-    {
-        u32x4* p = reinterpret_cast<u32x4*>(reinterpret_cast<unsigned char*>(y) + at * (BF ? 2 : 4));
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (i * T + t < chunks) {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    p[(i * T + t) * V + j] = v[i * V + j];
-            }
-    }
-    __device__ __forceinline__ void clear()
-    {
-#pragma unroll
-        for (int i = 0; i < P * V; ++i)
-            v[i] = u32x4{0u, 0u, 0u, 0u};
-    }
-};
 
 // w or b of a thread's chunks; `none` where there is no such vector.
 template <int T, int P>
@@ -89,21 +32,6 @@ __device__ __forceinline__ void load_vector(const float* w, float none, int t, i
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             v[i][j] = w ? raw.at(i, j) : none;
-}
-
-// The sum over a wave, in every lane: a butterfly within each row of 16 lanes, then
-// the four rows in pairs.
-__device__ __forceinline__ float wave_sum(float v)
-{
-    auto moved = [](float f, auto ctrl) __attribute__((always_inline)) {
-        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(f), decltype(ctrl)::value, 0xF, 0xF, false));
-    };
-    v += moved(v, std::integral_constant<int, 0xB1>{});         // lanes 1 apart
-    v += moved(v, std::integral_constant<int, 0x4E>{});         // 2 apart
-    v += moved(v, std::integral_constant<int, 0x141>{});        // the other four of eight
-    v += moved(v, std::integral_constant<int, 0x140>{});        // the other eight of sixteen
-    auto row = [&](int r) __attribute__((always_inline)) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16 * r)); };
-    return (row(0) + row(1)) + (row(2) + row(3));
 }
 
 // Sums of K values over teams of T threads.  Two buffers in turn: a wave that

@@ -91,9 +91,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 // Workgroup w runs on XCD w % 8.  Each XCD takes one contiguous eighth of the
 // tiles in an order that walks groups of 8 tile rows column by column, so that
 // the tiles an XCD works on at one time share rows of A and of B in its L2.
+template <int kGroup = 8>
 __device__ __forceinline__ int tile_at(int t, int tiles_m, int tiles_n, int& tn)
 {
-    constexpr int kGroup = 8;
     const int group = t / (kGroup * tiles_n);
     const int m0 = group * kGroup;
     const int rows = min(kGroup, tiles_m - m0);
@@ -227,13 +227,16 @@ constexpr int scale_ring_groups(int kb, int r)
 // A tile: BM x BN outputs (gated: BN weight rows, BN / 2 outputs) on WM x WN
 // computing waves, R ring stages of KB slices.  CA, CB: operand A / B stored by
 // columns.
-template <int BM_, int BN_, int WM_, int WN_, int KB_, int R_, bool CA_, bool CB_, TileType TYPE_, int EPI_>
+// RAGGED: many tiles have fewer rows than BM (products grouped by expert): the largest
+// tiles then leave out the loads and matrix instructions of rows that are not there.
+template <int BM_, int BN_, int WM_, int WN_, int KB_, int R_, bool CA_, bool CB_, TileType TYPE_, int EPI_, bool RAGGED_ = false>
 struct TileCfg {
+    static constexpr bool kRagged = RAGGED_ && !CA_;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, R = R_, EPI = EPI_;
     static constexpr TileType TYPE = TYPE_;
     static constexpr bool CA = CA_, CB = CB_, FP4 = TYPE == kFp4;
     static constexpr int NW = WM * WN;
-    static constexpr bool kSums = CA && BM_ < 256;
+    static constexpr bool kSums = CA && BM_ < 256 && KB_ == 2;         // column sums of A can be taken along
     static constexpr int FM = BM / (WM * 16), FN = BN / (WN * 16);
     static constexpr TileDeal kDeal = tile_deal<FN, EPI>();
     // 128 bytes of a row at a time: 17 to 32 percent off a 128 x 128 bf16 tile's
@@ -303,6 +306,7 @@ struct TileLoads {
     int64_t lda, ldb, K;
     int ns, kbytes, wl, lane;
     uint32_t lds0;
+    int rows;                                                          // of A that there are, where C::kRagged
 
     __device__ __forceinline__ void init(const TileArgs& p, unsigned char* ring, int wl_, int lane_, int m0, int n0)
     {
@@ -314,6 +318,7 @@ struct TileLoads {
         kbytes = (int)(C::FP4 ? p.K / 2 : C::TYPE == kInt8 ? p.K : p.K * 2);   // row operands
         lda = p.lda;
         ldb = p.ldb;
+        rows = p.M - m0;
         abase = p.a + (C::CA ? (int64_t)m0 * 2 : (int64_t)m0 * p.lda);
         bbase = p.b + (C::CB ? (int64_t)n0 * 2 : (int64_t)n0 * p.ldb);
 #pragma unroll
@@ -381,6 +386,13 @@ struct TileLoads {
                 for (int t = 0; t < LSC; ++t)
                     issue_scale(0, part, t);
         }
+    }
+
+    // Load t is of rows of A that are not there.  Only where every wait is for all
+    // loads may it be left out.
+    __device__ __forceinline__ bool past(int t) const
+    {
+        return C::kRagged && t < LA && (wl * LA + t) % (C::BM / A::kLoadRows) * A::kLoadRows >= rows;
     }
 
     // Load t of stage st.  WHOLE: every slice of the stage lies inside k, so
@@ -847,9 +859,12 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
     frags.init(ring, wm, wn, r, g);
     u32x4 xf[FM], wf[FN];
     int sx[FM], sw[FN];
+    const bool busy = !C::kRagged || wm * FM * 16 < loads.rows;    // this wave has rows
 
     auto read = [&](int st, int j) __attribute__((always_inline)) {
         const int at = (st % 2) * C::kStage;
+        if (!busy)
+            return;
 #pragma unroll
         for (int f = 0; f < FN; ++f) {
             wf[f] = frags.b(at, j, f);
@@ -878,6 +893,13 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
     auto compute = [&](auto whole_loads, int st, auto t0, auto t1) __attribute__((always_inline)) {
         constexpr int kLoads = decltype(t1)::value - decltype(t0)::value;
         constexpr int kEvery = FM * FN / (kLoads > 0 ? kLoads : 1);
+        if (!busy) {
+#pragma unroll
+            for (int t = decltype(t0)::value; t < decltype(t1)::value; ++t)
+                if (!loads.past(t))
+                    loads.template issue_one<decltype(whole_loads)::value>(st, t);
+            return;
+        }
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
@@ -885,7 +907,8 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
             tile_mfma<C::TYPE>(xf[i % FM], wf[i / FM], sx[i % FM], sw[i / FM], acc[i % FM][i / FM]);
             if (i % kEvery == kEvery / 2 && i / kEvery < kLoads) {
                 __builtin_amdgcn_sched_barrier(0);
-                loads.template issue_one<decltype(whole_loads)::value>(st, decltype(t0)::value + i / kEvery);
+                if (!loads.past(decltype(t0)::value + i / kEvery))
+                    loads.template issue_one<decltype(whole_loads)::value>(st, decltype(t0)::value + i / kEvery);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -898,7 +921,8 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
         if constexpr (!SECOND) {
 #pragma unroll
             for (int t = 0; t < kFirst; ++t)
-                loads.template issue_one<decltype(whole_loads)::value>(st + 1, t);
+                if (!loads.past(t))
+                    loads.template issue_one<decltype(whole_loads)::value>(st + 1, t);
         }
         wg_barrier_reads_done();
         if constexpr (decltype(tail)::value)

@@ -376,8 +376,8 @@ bi_status_t bi_grouped_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const u
                                        int64_t T, int64_t N, int64_t K, hipStream_t stream);
 
 /* Rows of x (bf16 or fp32) as 8-bit integers with one fp32 scale each:
- *   s = max(max|x| / 127, 2^-126),  q = x / s rounded to the nearest integer,
- * ties to even: in [-127, 127].  A row that holds an infinity or a NaN gets s = NaN
+ *   s = max(max|x| * c, 2^-126), c = 1/127 in fp32,  q = x / s rounded to the
+ * nearest integer, ties to even: in [-127, 127].  A row that holds an infinity or a NaN gets s = NaN
  * and zero codes.  q: [rows, K] (pitch in bytes, a multiple of 16), s: [rows], 4-byte
  * aligned.  Requires K % 32 == 0. */
 bi_status_t bi_quantize_int8(const void* x, int32_t x_dtype, int64_t ldx, int8_t* q, int64_t ldq, float* s,

@@ -79,7 +79,7 @@ def codes(x):
     x = x.double().cpu()
     bad = ~torch.isfinite(x).all(dim=1)
     top = torch.where(bad, torch.zeros(x.shape[0], dtype=torch.float64), x.abs().amax(dim=1))
-    s = torch.clamp((top / 127.0).float(), min=2.0 ** -126)
+    s = torch.clamp(top.float() * torch.tensor(1.0 / 127.0), min=2.0 ** -126)        # fp32's 1/127, one rounding
     q = torch.round(torch.where(bad[:, None], torch.zeros_like(x), x) / s.double()[:, None])      # torch.round: ties to even
     s = torch.where(bad, torch.full_like(s, float("nan")), s)
     return q.to(torch.int8), s

@@ -244,7 +244,7 @@ def test_quantize_on_the_border(bi):
     x = torch.zeros((len(tops), 1024), dtype=F32)
     half = torch.arange(-127, 127).double() + 0.5
     for i, top in enumerate(tops):
-        s = torch.clamp(top / 127, min=2.0 ** -126)
+        s = torch.clamp(top * torch.tensor(1.0 / 127.0), min=2.0 ** -126)
         at = (half * s.double()).float()
         at = at[at.abs() <= top]
         n = len(at)

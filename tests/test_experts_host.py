@@ -99,9 +99,10 @@ def test_unsupported_sizes(fn, kw):
 def test_more_workgroups_than_a_launch_holds():
     T = 1 << 30
     assert int8(M=T, N=16, K=32, ldy=16) == bi.BI_EUNSUPPORTED
-    assert grouped(T=T, N=32, E=1024) == bi.BI_EUNSUPPORTED
-    assert grouped_int8(T=T, N=32, E=1024) == bi.BI_EUNSUPPORTED
-    assert grouped_bwd(T=T, dw=None) == bi.BI_EUNSUPPORTED
+    # 2^22 row tiles and more even of the largest shape, four columns of them
+    assert grouped(T=T, N=1024, E=1024, ldy=1024) == bi.BI_EUNSUPPORTED
+    assert grouped_int8(T=T, N=1024, E=1024, ldy=1024) == bi.BI_EUNSUPPORTED
+    assert grouped_bwd(T=T, N=32, K=1024, ldx=1024, ldw=1024, lddx=1024, dw=None) == bi.BI_EUNSUPPORTED
     # dw alone: 1024 experts of 512 x 512 tiles of 256 x 256 and more
     n = 1 << 18
     assert grouped_bwd(dx=None, E=1024, N=n, K=n, lddy=n, ldx=n, lddw=n, sdw=n * n) == bi.BI_EUNSUPPORTED
