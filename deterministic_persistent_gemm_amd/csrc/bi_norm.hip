@@ -164,21 +164,72 @@ struct NormBwdArgs {
     void* dx;                   // or nullptr
     int64_t lddx;
     float* part;                // [workgroup][2][H] sums of dy n and of dy, or nullptr
-    float* dw;                  // where one workgroup does it all: [H] or nullptr
+    float* dw;                  // few rows: [H] or nullptr, summed by columns beside the rows
     float* db;
+    int row_groups;             // workgroups that take rows; the others take columns
     int64_t M;
     int H;
 };
 
+// dw and db of 64 columns: 8 threads of eight columns by 64 row lanes; a lane adds its
+// rows in ascending order, 16 lanes are added in order, then the four sixteens.  The
+// statistics are there already, so nothing of this waits for the rows' own sums.
+constexpr int kBwdThreads = 512, kSumCols = 64, kSumLanes = kBwdThreads / 8;
+
+template <bool DB, bool XB>
+__device__ __forceinline__ void column_sums(const NormBwdArgs& p, int block, float (*part)[2 * kSumCols + 1])
+{
+    const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3, c = block * kSumCols + cg * 8;
+    float dw[8] = {}, db[8] = {};
+    if (c < p.H) {
+#pragma unroll 4
+        for (int64_t m = rl; m < p.M; m += kSumLanes) {
+            RowRaw<XB, 1> x;
+            RowRaw<DB, 1> d;
+            x.template load<0>(p.x, m * p.ldx, c / 8, p.H / 8);
+            d.template load<0>(p.dy, m * p.lddy, c / 8, p.H / 8);
+            const float mean = p.mean[m], rstd = p.rstd[m];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dw[j] = __builtin_fmaf(d.at(0, j), (x.at(0, j) - mean) * rstd, dw[j]);
+                db[j] += d.at(0, j);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        part[rl][cg * 8 + j] = dw[j];
+        part[rl][kSumCols + cg * 8 + j] = db[j];
+    }
+    __syncthreads();
+    const int col = threadIdx.x & (2 * kSumCols - 1), quarter = threadIdx.x / (2 * kSumCols);
+    float t = part[quarter * 16][col];
+#pragma unroll
+    for (int l = 1; l < 16; ++l)
+        t += part[quarter * 16 + l][col];
+    __syncthreads();
+    part[quarter][col] = t;
+    __syncthreads();
+    const int at = block * kSumCols + (col & (kSumCols - 1));
+    float* to = col < kSumCols ? p.dw : p.db;
+    if (quarter == 0 && to && at < p.H)
+        to[at] = ((part[0][col] + part[1][col]) + part[2][col]) + part[3][col];
+}
+
 template <bool DB, bool XB, int T, int P, int TEAMS>
 __global__ __launch_bounds__(T * TEAMS) void k_layer_norm_bwd(NormBwdArgs p)
 {
+    static_assert(T * TEAMS == kBwdThreads, "one workgroup size");
     __shared__ __attribute__((aligned(16))) float buf[2][TEAMS][2][T / 64];
-    __shared__ float fold[TEAMS > 1 ? T * 8 * P : 1];
+    __shared__ float fold[TEAMS > 1 && T * 8 * P > kSumLanes * (2 * kSumCols + 1) ? T * 8 * P : kSumLanes * (2 * kSumCols + 1)];
+    if ((int)blockIdx.x >= p.row_groups) {
+        column_sums<DB, XB>(p, (int)blockIdx.x - p.row_groups, reinterpret_cast<float(*)[2 * kSumCols + 1]>(fold));
+        return;
+    }
     constexpr bool kAhead = P <= 2;                     // longer rows leave no registers for the next one
     TeamSum<T, TEAMS, 2> sum{buf};
     const int t = threadIdx.x % T, team = (int)uniform(threadIdx.x / T), chunks = p.H / 8;
-    const int64_t step = (int64_t)gridDim.x * TEAMS;
+    const int64_t step = (int64_t)p.row_groups * TEAMS;
     int64_t m = (int64_t)blockIdx.x * TEAMS + team;
     RowRaw<XB, P> x, xn;
     RowRaw<DB, P> d, dn;
@@ -247,7 +298,7 @@ __global__ __launch_bounds__(T * TEAMS) void k_layer_norm_bwd(NormBwdArgs p)
         if (p.dx && live)
             out.template store<T>(p.dx, m * p.lddx, t, chunks);
     }
-    if (!p.part && !p.dw && !p.db)
+    if (!p.part)
         return;
     // the teams' sums in order, then the workgroup's partial
     auto out = [&](float (&a)[P][8], int which) __attribute__((always_inline)) {
@@ -276,10 +327,7 @@ __global__ __launch_bounds__(T * TEAMS) void k_layer_norm_bwd(NormBwdArgs p)
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 sums.set(i, a[i]);
-            if (p.part)
-                sums.template store<T>(p.part, ((int64_t)blockIdx.x * 2 + which) * p.H, t, chunks);
-            else if (float* to = which ? p.db : p.dw)
-                sums.template store<T>(to, 0, t, chunks);
+            sums.template store<T>(p.part, ((int64_t)blockIdx.x * 2 + which) * p.H, t, chunks);
         }
     };
     out(dw, 0);
@@ -362,47 +410,43 @@ hipError_t launch_layer_norm(const void* x, int x_bf16, int64_t ldx, const float
     return hipGetLastError();
 }
 
-// The backward pass runs on at most 256 workgroups of 512 threads, one per compute
-// unit, each with a partial of dw and db.  Up to four rows a team are left to one
-// workgroup, which needs no second launch (4 us) to add partials.
-constexpr int kBwdThreads = 512;
+// Rows are taken by at most 256 workgroups, one per compute unit.  Over many rows each
+// leaves a partial of dw and db, which a second launch adds; up to kColumnRows
+// rows, workgroups beside them sum the columns, which reads x and dy twice but needs no
+// second launch and no workspace.
+constexpr int64_t kColumnRows = 1024;
 
 static int64_t bwd_groups(int64_t M, int64_t rows)
 {
     const int64_t groups = (M + rows - 1) / rows;
-    return groups <= 4 ? 1 : groups < 256 ? groups : 256;
+    return groups < 256 ? groups : 256;
 }
 
 size_t layer_norm_bwd_ws(int64_t M, int64_t H)
 {
     int64_t groups = 0;
     norm_shape(H, [&](auto T, auto) { groups = bwd_groups(M, kBwdThreads / T); });
-    return groups > 1 ? (size_t)groups * 2 * (size_t)H * 4 : 0;
+    return M > kColumnRows ? (size_t)groups * 2 * (size_t)H * 4 : 0;
 }
 
 hipError_t launch_layer_norm_bwd(const void* dy, int dy_bf16, int64_t lddy, const void* x, int x_bf16, int64_t ldx,
                                  const float* mean, const float* rstd, const float* w, void* dx, int64_t lddx, float* dw, float* db,
                                  int64_t M, int64_t H, void* ws, hipStream_t s)
 {
-    NormBwdArgs p{dy, lddy, x, ldx, mean, rstd, w, dx, lddx, nullptr, nullptr, nullptr, M, (int)H};
-    int64_t groups = 0;
-    bool fold = false;
+    NormBwdArgs p{dy, lddy, x, ldx, mean, rstd, w, dx, lddx, nullptr, dw, db, 0, M, (int)H};
+    const bool sums = dw || db, columns = sums && M <= kColumnRows, fold = sums && !columns;
+    if (fold)
+        p.part = reinterpret_cast<float*>(ws);
     two_types(dy_bf16, x_bf16, [&](auto yb, auto xb) {
         norm_shape(H, [&](auto T, auto P) {
             constexpr int R = kBwdThreads / T;
-            groups = bwd_groups(M, R);
-            fold = groups > 1 && (dw || db);
-            if (fold) {
-                p.part = reinterpret_cast<float*>(ws);
-            } else {
-                p.dw = dw;
-                p.db = db;
-            }
+            p.row_groups = dx || fold ? (int)bwd_groups(M, R) : 0;
+            const int groups = p.row_groups + (columns ? (int)((H + kSumCols - 1) / kSumCols) : 0);
             k_layer_norm_bwd<decltype(yb)::value, decltype(xb)::value, T, P, R><<<(unsigned)groups, kBwdThreads, 0, s>>>(p);
         });
     });
     if (fold)
-        k_layer_norm_fold<<<(unsigned)((2 * H + 31) / 32), 256, 0, s>>>(p.part, dw, db, (int)groups, (int)H);
+        k_layer_norm_fold<<<(unsigned)((2 * H + 31) / 32), 256, 0, s>>>(p.part, dw, db, p.row_groups, (int)H);
     return hipGetLastError();
 }
 

@@ -55,9 +55,9 @@ def norm_bwd(dy, x, mean, rstd, w, x_dtype):
     e1 = (ROW_DEPTH + 5) * U * (g * n).abs().mean(dim=1, keepdim=True) * k
     inner = eg + e0 + n.abs() * e1 + c1.abs() * en + 3 * U * (g.abs() + c0.abs() + (n * c1).abs())
     edx = r * inner * k + U * dx.abs()
-    # rows: a team's in order (at most four, or a 256th of all), 8 teams, 8 partials of
-    # a slice, 32 slices
-    depth = M // 256 + 4 + 8 + 8 + 32
+    # many rows: a team's in order, 8 teams, 8 partials of a slice, 32 slices; up to 1024
+    # rows: a 64th in order, 16 lanes, four sixteens
+    depth = max(M // 256 + 1 + 8 + 8 + 32, min(M, 1024) // 64 + 1 + 16 + 4)
     t = dy * n
     edw = ((depth + 3) * U * t.abs()).sum(dim=0) * k
     edb = (depth * U * dy.abs()).sum(dim=0)

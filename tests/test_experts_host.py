@@ -119,12 +119,12 @@ def test_nothing_to_do():
 
 
 def test_workspace_sizes_and_refusals():
-    need = L.bi_layer_norm_bwd_workspace_size(100, 64)
+    need = L.bi_layer_norm_bwd_workspace_size(5000, 64)
     assert need > bi.WS_COUNTER_BYTES and (need - bi.WS_COUNTER_BYTES) % (2 * 64 * 4) == 0
-    assert norm_bwd(M=100, ws=None) == norm_bwd(M=100, n=need - 1) == norm_bwd(M=100, ws=P + 8) == bi.BI_EWORKSPACE
-    assert norm_bwd(M=100, dw=None, n=need - 1) == bi.BI_EWORKSPACE
+    assert norm_bwd(M=5000, ws=None) == norm_bwd(M=5000, n=need - 1) == norm_bwd(M=5000, ws=P + 8) == bi.BI_EWORKSPACE
+    assert norm_bwd(M=5000, dw=None, n=need - 1) == bi.BI_EWORKSPACE
     # a few rows need none; nor do sizes that are refused
-    for args in ((1, 64), (0, 64), (-1, 64), (100, 60), (100, 0), (100, 16392)):
+    for args in ((1, 64), (0, 64), (-1, 64), (5000, 60), (5000, 0), (5000, 16392)):
         assert L.bi_layer_norm_bwd_workspace_size(*args) == 0
     # it does not grow with the batch for ever
     assert L.bi_layer_norm_bwd_workspace_size(1 << 20, 4096) == L.bi_layer_norm_bwd_workspace_size(1 << 30, 4096)
