@@ -158,37 +158,39 @@ __device__ __forceinline__ void at_group(TileArgs& p, const GroupArgs& q, const 
     p.M = t.rows;
 }
 
+// Workgroup w of a product over the experts' rows.
 template <typename S>
-__global__ __launch_bounds__((S::C::NW + S::NL) * 64) void k_grouped(TileArgs p, GroupArgs q)
+__device__ __forceinline__ void rows_body(TileArgs& p, const GroupArgs& q, unsigned char* ring, int w)
 {
-    __shared__ __attribute__((aligned(1024))) unsigned char ring[S::C::kRing];
     GroupTile t;
-    if (!find_tile<S::C::BM>(q, p.tiles_n, (int)blockIdx.x, t))
+    if (!find_tile<S::C::BM>(q, p.tiles_n, w, t))
         return;
     at_group(p, q, t);
     tile_any<S>(p, ring, t.tm, t.tn);
 }
 
-// dw of one expert per tile: the sum runs over its rows.  An expert without rows
-// gets zeros.
+// Workgroup w of dw: a tile of one expert, whose sum runs over its rows.  An expert
+// without rows gets zeros.  An expert's tiles are dealt to all XCDs, as one
+// expert may have many times the rows of another (an eighth of the experts to
+// each XCD: 525 us instead of 441 where demand is uneven); which of them gets one
+// more goes round from expert to expert.
 template <typename S>
-__global__ __launch_bounds__((S::C::NW + S::NL) * 64) void k_grouped_dw(TileArgs p, GroupArgs q)
+__device__ __forceinline__ void dw_body(TileArgs& p, const GroupArgs& q, unsigned char* ring, int w)
 {
     using C = typename S::C;
-    __shared__ __attribute__((aligned(1024))) unsigned char ring[C::kRing];
-    int tn;
     const int tiles = p.tiles_m * p.tiles_n, per = (tiles + 7) >> 3;
-    const int j = (int)blockIdx.x >> 3, e = j / per, t = (((int)blockIdx.x + e) & 7) * per + j - e * per;
+    const int j = w >> 3, e = j / per, t = ((w + e) & 7) * per + j - e * per;
     if (t >= tiles)
         return;
+    int tn;
     const int tm = tile_at(t, p.tiles_m, p.tiles_n, tn);
     int first, rows;
     rows_of(q, e, first, rows);
-    const int es = p.y_bf16 ? 2 : 4;
     p.y = reinterpret_cast<unsigned char*>(p.y) + (int64_t)e * q.stride_b;
     if (rows == 0) {
+        const int es = p.y_bf16 ? 2 : 4;
         const int units = C::BN * es / 16, have = (p.N - tn * C::BN) * es / 16;
-        for (int i = threadIdx.x; i < C::BM * units; i += C::NW * 64) {
+        for (int i = threadIdx.x; i < C::BM * units; i += (C::NW + S::NL) * 64) {
             const int m = tm * C::BM + i / units, u = i % units;
             if (m < p.M && u < have)
                 reinterpret_cast<u32x4*>(reinterpret_cast<unsigned char*>(p.y) + ((int64_t)m * p.ldy + tn * C::BN) * es)[u] =
@@ -200,6 +202,39 @@ __global__ __launch_bounds__((S::C::NW + S::NL) * 64) void k_grouped_dw(TileArgs
     p.b += (int64_t)first * p.ldb;
     p.K = rows;
     tile_any<S>(p, ring, tm, tn);
+}
+
+template <typename S>
+__global__ __launch_bounds__((S::C::NW + S::NL) * 64) void k_grouped(TileArgs p, GroupArgs q)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char ring[S::C::kRing];
+    rows_body<S>(p, q, ring, (int)blockIdx.x);
+}
+
+template <typename S>
+__global__ __launch_bounds__((S::C::NW + S::NL) * 64) void k_grouped_dw(TileArgs p, GroupArgs q)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char ring[S::C::kRing];
+    dw_body<S>(p, q, ring, (int)blockIdx.x);
+}
+
+// Both gradients: workgroups 0 .. ndx - 1 (a multiple of 8) take dx, the rest dw.
+constexpr int kBothThreads = 512;
+
+template <typename SX, typename SW>
+__global__ __launch_bounds__(kBothThreads) void k_grouped_both(TileArgs dx, GroupArgs qx, TileArgs dw, GroupArgs qw, int ndx)
+{
+    constexpr int kX = (SX::C::NW + SX::NL) * 64, kW = (SW::C::NW + SW::NL) * 64;
+    static_assert(kX <= kBothThreads && kW <= kBothThreads, "one workgroup size");
+    __shared__ __attribute__((aligned(1024))) unsigned char ring[SX::C::kRing > SW::C::kRing ? SX::C::kRing : SW::C::kRing];
+    const int b = (int)blockIdx.x;
+    // waves that a shape does not need leave before its first barrier, which counts those that are left
+    if (b < ndx) {
+        if ((int)threadIdx.x < kX)
+            rows_body<SX>(dx, qx, ring, b);
+    } else if ((int)threadIdx.x < kW) {
+        dw_body<SW>(dw, qw, ring, b - ndx);
+    }
 }
 
 // --------------------------------------------------------------------- shapes
@@ -267,6 +302,18 @@ static auto group_shape(int i, F f)
     }
 }
 
+// dw's tiles where dx's are beside them in one launch: 128 x 128 on as many waves and
+// registers as dx's tiles have, so that two workgroups still share a compute unit.
+template <typename F>
+static auto both_dw_shape(int i, F f)
+{
+    if (i == 0)
+        return f(GroupShape<64, 64, 4, 2, 2, 4, 0, true, true, kBf16>{});
+    if (i == 1)
+        return f(GroupShape<128, 128, 4, 2, 1, 4, 0, true, true, kBf16>{});
+    return f(GroupShape<256, 256, 4, 2, 2, 2, 0, true, true, kBf16>{});
+}
+
 // Row tiles of any split of T rows over E experts, at most.
 static int64_t most_row_tiles(int64_t T, int64_t E, int bm)
 {
@@ -308,6 +355,26 @@ static int pick_group(GroupOp op, int64_t T, int64_t E, int64_t N, int64_t K, bo
     return best;
 }
 
+// The shapes of a backward pass with both gradients, and whether one launch takes them.
+// Side by side in one launch small tiles take 0.78 of the time of two launches (55
+// problems, 0.62 to 1.00), the largest of both 0.94 (9 problems, 0.90 to 0.98).  Where
+// only dw's are the largest, its second largest beside small tiles of dx (0.94), or the
+// largest of both (dx's being 64 x 128 or 128 x 128: 0.92); where only dx's are, one
+// launch is the slower one (1.12 to 1.39).
+struct GroupBwdPlan {
+    int dx, dw;
+    bool together;
+};
+
+static GroupBwdPlan plan_grouped_bwd(int64_t T, int64_t E, int64_t N, int64_t K, bool dw_f32)
+{
+    constexpr int kMostDx = kNumDxShapes - 1, kMostDw = kNumDwShapes - 1;
+    const int dx = pick_group(kGroupDx, T, E, N, K, false), dw = pick_group(kGroupDw, T, E, N, K, dw_f32);
+    if (dw < kMostDw)
+        return {dx, dw, dx < kMostDx};
+    return dx >= 3 ? GroupBwdPlan{kMostDx, kMostDw, true} : GroupBwdPlan{dx, kMostDw - 1, true};
+}
+
 bool grouped_fits(int64_t lda, int64_t ldw, int es, int64_t T, int64_t N, int64_t K, int64_t E)
 {
     const int64_t lim = int64_t(1) << 32;
@@ -322,37 +389,66 @@ bool grouped_bwd_fits(int64_t lddy, int64_t ldx, int64_t ldw, int64_t T, int64_t
            N < (int64_t(1) << 29) && E <= kMaxExperts;
 }
 
+// Workgroups of a product over rows, and of dw; both fill in the tile counts.
+template <typename C>
+static int64_t rows_groups(TileArgs& a, const GroupArgs& q)
+{
+    a.tiles_n = (a.N + C::BN - 1) / C::BN;
+    return most_row_tiles(q.T, q.E, C::BM) * a.tiles_n;
+}
+
+template <typename C>
+static int64_t dw_groups(TileArgs& a, const GroupArgs& q)
+{
+    a.tiles_m = (a.M + C::BM - 1) / C::BM;
+    a.tiles_n = (a.N + C::BN - 1) / C::BN;
+    return ((int64_t)a.tiles_m * a.tiles_n + 7) / 8 * 8 * q.E;
+}
+
+// dry: only whether a launch can hold the grid
 template <GroupOp OP>
-static hipError_t run_rows(TileArgs a, const GroupArgs& q, int shape, hipStream_t s, bool dry)
+static hipError_t run_rows(TileArgs a, const GroupArgs& q, int shape, hipStream_t s, bool dry = false)
 {
     return group_shape<OP>(shape, [&](auto sh) {
         using S = decltype(sh);
-        using C = typename S::C;
-        a.tiles_n = (a.N + C::BN - 1) / C::BN;
-        const int64_t tiles = most_row_tiles(q.T, q.E, C::BM) * a.tiles_n;
-        if (!grid_ok(tiles))
+        const int64_t groups = rows_groups<typename S::C>(a, q);
+        if (!grid_ok(groups))
             return hipErrorInvalidConfiguration;
         if (dry)
             return hipSuccess;
-        k_grouped<S><<<(unsigned)tiles, (C::NW + S::NL) * 64, 0, s>>>(a, q);
+        k_grouped<S><<<(unsigned)groups, (S::C::NW + S::NL) * 64, 0, s>>>(a, q);
         return hipGetLastError();
     });
 }
 
-static hipError_t run_dw(TileArgs a, const GroupArgs& q, int shape, hipStream_t s, bool dry)
+static hipError_t run_dw(TileArgs a, const GroupArgs& q, int shape, hipStream_t s, bool dry = false)
 {
     return group_shape<kGroupDw>(shape, [&](auto sh) {
         using S = decltype(sh);
-        using C = typename S::C;
-        a.tiles_m = (a.M + C::BM - 1) / C::BM;
-        a.tiles_n = (a.N + C::BN - 1) / C::BN;
-        const int64_t tiles = ((int64_t)a.tiles_m * a.tiles_n + 7) / 8 * 8 * q.E;
-        if (!grid_ok(tiles))
+        const int64_t groups = dw_groups<typename S::C>(a, q);
+        if (!grid_ok(groups))
             return hipErrorInvalidConfiguration;
         if (dry)
             return hipSuccess;
-        k_grouped_dw<S><<<(unsigned)tiles, (C::NW + S::NL) * 64, 0, s>>>(a, q);
+        k_grouped_dw<S><<<(unsigned)groups, (S::C::NW + S::NL) * 64, 0, s>>>(a, q);
         return hipGetLastError();
+    });
+}
+
+static hipError_t run_both(TileArgs a, const GroupArgs& qx, int sx, TileArgs b, const GroupArgs& qw, int sw, hipStream_t s)
+{
+    return group_shape<kGroupDx>(sx, [&](auto x) {
+        return both_dw_shape(sw, [&](auto w) {
+            using SX = decltype(x);
+            using SW = decltype(w);
+            if constexpr ((SX::C::BM == 256) == (SW::C::BM == 256)) {
+                const int64_t ndx = (rows_groups<typename SX::C>(a, qx) + 7) / 8 * 8, groups = ndx + dw_groups<typename SW::C>(b, qw);
+                if (!grid_ok(groups))
+                    return hipErrorInvalidConfiguration;
+                k_grouped_both<SX, SW><<<(unsigned)groups, kBothThreads, 0, s>>>(a, qx, b, qw, (int)ndx);
+            }
+            return hipGetLastError();
+        });
     });
 }
 
@@ -371,7 +467,7 @@ hipError_t launch_grouped_bf16(const uint16_t* x, int64_t ldx, const uint16_t* w
     a.N = (int)N;
     a.K = K;
     const GroupArgs q{ends, (int)E, (int)T, stride_w * 2, 0};
-    return run_rows<kGroupBf16>(a, q, pick_group(kGroupBf16, T, E, N, K, !y_bf16), s, false);
+    return run_rows<kGroupBf16>(a, q, pick_group(kGroupBf16, T, E, N, K, !y_bf16), s);
 }
 
 hipError_t launch_grouped_int8(const int8_t* xq, int64_t ldx, const float* xs, const int8_t* wq, int64_t ldw, int64_t stride_w,
@@ -391,7 +487,7 @@ hipError_t launch_grouped_int8(const int8_t* xq, int64_t ldx, const float* xs, c
     a.N = (int)N;
     a.K = K;
     const GroupArgs q{ends, (int)E, (int)T, stride_w, stride_ws * 4};
-    return run_rows<kGroupInt8>(a, q, pick_group(kGroupInt8, T, E, N, K, !y_bf16), s, false);
+    return run_rows<kGroupInt8>(a, q, pick_group(kGroupInt8, T, E, N, K, !y_bf16), s);
 }
 
 hipError_t launch_grouped_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* w, int64_t ldw,
@@ -417,13 +513,19 @@ hipError_t launch_grouped_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* 
     b.N = (int)K;
     const GroupArgs qx{ends, (int)E, (int)T, stride_w * 2, 0};
     const GroupArgs qw{ends, (int)E, (int)T, stride_dw * (dw_bf16 ? 2 : 4), 0};
-    const int sx = pick_group(kGroupDx, T, E, N, K, false), sw = pick_group(kGroupDw, T, E, N, K, !dw_bf16);
     const bool do_dx = dx && T > 0;
+    if (!do_dx)
+        return dw ? run_dw(b, qw, pick_group(kGroupDw, T, E, N, K, !dw_bf16), s) : hipSuccess;
+    if (!dw)
+        return run_rows<kGroupDx>(a, qx, pick_group(kGroupDx, T, E, N, K, false), s);
+    const GroupBwdPlan plan = plan_grouped_bwd(T, E, N, K, !dw_bf16);
+    if (plan.together)
+        return run_both(a, qx, plan.dx, b, qw, plan.dw, s);
     // both grids are checked before either launch: a refused call enqueues nothing
     for (const bool dry : {true, false}) {
-        hipError_t e = do_dx ? run_rows<kGroupDx>(a, qx, sx, s, dry) : hipSuccess;
-        if (e == hipSuccess && dw)
-            e = run_dw(b, qw, sw, s, dry);
+        hipError_t e = run_rows<kGroupDx>(a, qx, plan.dx, s, dry);
+        if (e == hipSuccess)
+            e = run_dw(b, qw, plan.dw, s, dry);
         if (e != hipSuccess)
             return e;
     }
@@ -433,13 +535,14 @@ hipError_t launch_grouped_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* 
 TileInfo grouped_tile_info(int op, int64_t T, int64_t E, int64_t N, int64_t K, int out_bf16)
 {
     const auto info = [](int i) { return [i](auto shape) { return tile_info<decltype(shape)>(i); }; };
-    const int i = pick_group((GroupOp)op, T, E, N, K, !out_bf16);
-    switch (op) {
-    case kGroupBf16: return group_shape<kGroupBf16>(i, info(i));
-    case kGroupInt8: return group_shape<kGroupInt8>(i, info(i));
-    case kGroupDx: return group_shape<kGroupDx>(i, info(i));
-    default: return group_shape<kGroupDw>(i, info(i));
+    if (op == kGroupBf16 || op == kGroupInt8) {
+        const int i = pick_group((GroupOp)op, T, E, N, K, !out_bf16);
+        return op == kGroupBf16 ? group_shape<kGroupBf16>(i, info(i)) : group_shape<kGroupInt8>(i, info(i));
     }
+    const GroupBwdPlan plan = plan_grouped_bwd(T, E, N, K, !out_bf16);
+    if (op == kGroupDx)
+        return group_shape<kGroupDx>(plan.dx, info(plan.dx));
+    return plan.together ? both_dw_shape(plan.dw, info(plan.dw)) : group_shape<kGroupDw>(plan.dw, info(plan.dw));
 }
 
 }  // namespace bi

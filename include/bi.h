@@ -523,7 +523,7 @@ bi_status_t bi_lab_ffn_tile(int32_t op, int64_t M, int64_t N, int64_t K, int32_t
 
 /* The same for a product grouped by expert: T rows, E experts (the shape follows
  * from these, not from how the rows are split); dx and dw are those of
- * bi_grouped_linear_bf16_bwd. */
+ * bi_grouped_linear_bf16_bwd where both are wanted and dw is of out_dtype. */
 typedef enum { BI_GROUPED_BF16 = 0, BI_GROUPED_INT8 = 1, BI_GROUPED_DX = 2, BI_GROUPED_DW = 3 } bi_grouped_op_t;
 bi_status_t bi_lab_grouped_tile(int32_t op, int64_t T, int64_t E, int64_t N, int64_t K, int32_t out_dtype, int32_t* info);
 
