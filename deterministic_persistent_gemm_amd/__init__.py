@@ -882,7 +882,7 @@ def moe_layout(M: int, H: int, E: int, I: int, topk: int) -> dict:
 
 
 BI_FFN_GATED, BI_FFN_MXFP4, BI_FFN_DX, BI_FFN_DW, BI_FFN_INT8 = 0, 1, 2, 3, 4
-BI_GROUPED_BF16, BI_GROUPED_INT8, BI_GROUPED_DX, BI_GROUPED_DW = 0, 1, 2, 3
+BI_GROUPED_BF16, BI_GROUPED_INT8, BI_GROUPED_DX, BI_GROUPED_DW, BI_GROUPED_DX_ALONE, BI_GROUPED_DW_ALONE = range(6)
 _TILE_FIELDS = ("shape", "kernel", "rows", "cols", "slice_k", "stage_slices", "ring_stages", "scale_groups")
 
 

@@ -685,7 +685,7 @@ bi_status_t bi_lab_ffn_tile(int32_t op, int64_t M, int64_t N, int64_t K, int32_t
 
 bi_status_t bi_lab_grouped_tile(int32_t op, int64_t T, int64_t E, int64_t N, int64_t K, int32_t out_dtype, int32_t* info)
 {
-    if (op < BI_GROUPED_BF16 || op > BI_GROUPED_DW || !dtype_ok(out_dtype) || T <= 0 || !info)
+    if (op < BI_GROUPED_BF16 || op > BI_GROUPED_DW_ALONE || !dtype_ok(out_dtype) || T <= 0 || !info)
         return BI_EINVAL;
     const bi_status_t st = check_grouped(T, N, K, E);
     if (st != BI_OK)

@@ -535,12 +535,16 @@ hipError_t launch_grouped_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* 
 TileInfo grouped_tile_info(int op, int64_t T, int64_t E, int64_t N, int64_t K, int out_bf16)
 {
     const auto info = [](int i) { return [i](auto shape) { return tile_info<decltype(shape)>(i); }; };
-    if (op == kGroupBf16 || op == kGroupInt8) {
-        const int i = pick_group((GroupOp)op, T, E, N, K, !out_bf16);
-        return op == kGroupBf16 ? group_shape<kGroupBf16>(i, info(i)) : group_shape<kGroupInt8>(i, info(i));
+    const auto alone = [&](GroupOp o) { return pick_group(o, T, E, N, K, !out_bf16 && o != kGroupDx); };
+    switch (op) {
+    case BI_GROUPED_BF16: return group_shape<kGroupBf16>(alone(kGroupBf16), info(alone(kGroupBf16)));
+    case BI_GROUPED_INT8: return group_shape<kGroupInt8>(alone(kGroupInt8), info(alone(kGroupInt8)));
+    case BI_GROUPED_DX_ALONE: return group_shape<kGroupDx>(alone(kGroupDx), info(alone(kGroupDx)));
+    case BI_GROUPED_DW_ALONE: return group_shape<kGroupDw>(alone(kGroupDw), info(alone(kGroupDw)));
+    default: break;
     }
     const GroupBwdPlan plan = plan_grouped_bwd(T, E, N, K, !out_bf16);
-    if (op == kGroupDx)
+    if (op == BI_GROUPED_DX)
         return group_shape<kGroupDx>(plan.dx, info(plan.dx));
     return plan.together ? both_dw_shape(plan.dw, info(plan.dw)) : group_shape<kGroupDw>(plan.dw, info(plan.dw));
 }

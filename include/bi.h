@@ -522,9 +522,10 @@ typedef enum { BI_FFN_GATED = 0, BI_FFN_MXFP4 = 1, BI_FFN_DX = 2, BI_FFN_DW = 3,
 bi_status_t bi_lab_ffn_tile(int32_t op, int64_t M, int64_t N, int64_t K, int32_t out_dtype, int32_t* info);
 
 /* The same for a product grouped by expert: T rows, E experts (the shape follows
- * from these, not from how the rows are split); dx and dw are those of
- * bi_grouped_linear_bf16_bwd where both are wanted and dw is of out_dtype. */
-typedef enum { BI_GROUPED_BF16 = 0, BI_GROUPED_INT8 = 1, BI_GROUPED_DX = 2, BI_GROUPED_DW = 3 } bi_grouped_op_t;
+ * from these, not from how the rows are split); dx and dw of
+ * bi_grouped_linear_bf16_bwd with dw of out_dtype, where both are wanted or one alone. */
+typedef enum { BI_GROUPED_BF16 = 0, BI_GROUPED_INT8 = 1, BI_GROUPED_DX = 2, BI_GROUPED_DW = 3,
+               BI_GROUPED_DX_ALONE = 4, BI_GROUPED_DW_ALONE = 5 } bi_grouped_op_t;
 bi_status_t bi_lab_grouped_tile(int32_t op, int64_t T, int64_t E, int64_t N, int64_t K, int32_t out_dtype, int32_t* info);
 
 /* Where a MoE call of this shape keeps its storage points in the workspace,

@@ -5,6 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests import experts_ref as ref
+from tests import experts_shapes as shapes
 from tests import ffn_ref
 from tests.gpu_util import banner
 
@@ -320,6 +321,91 @@ def test_int8_is_near_the_product_it_stands_for(bi):
     bound = ex * wd.abs().sum(1) + xd.abs().sum(1, keepdim=True) * ew + K * ex * ew
     want = xd @ wd.t()
     assert ((y - want).abs() <= bound * (1 + 1e-6) + 4 * ref.U * want.abs()).all()
+
+
+# -------------------------------------------------- every tile shape past its ring
+
+
+@pytest.mark.parametrize("M,N,K", shapes.INT8)
+def test_int8_tile_shapes(bi, M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    xq, wq = (torch.randint(-128, 128, s, generator=g, device="cuda", dtype=torch.int8) for s in ((M, K), (N, K)))
+    xs, ws, b = (torch.rand(n, generator=g, device="cuda") for n in (M, N, N))
+    acc = torch.mm(xq.double(), wq.double().t()).float()
+    want = acc * xs[:, None] * ws + b
+    for dt in (BF, F32):
+        banner(f"int8 shapes {M} {N} {K} {dt}")
+        assert torch.equal(bi.bi_linear_int8(xq, xs, wq, ws, b, out_dtype=dt), want.to(dt))
+
+
+@pytest.mark.parametrize("T,E,N,K", shapes.GROUPED)
+def test_grouped_tile_shapes(bi, T, E, N, K):
+    counts = shapes.counts(T, E)
+    x, w, ends = ints((T, K), 1), ints((E, N, K), 2), ends_of(counts)
+    xq, wq = x.to(torch.int8), w.to(torch.int8)
+    xs, ws = torch.rand(T, device="cuda"), torch.rand((E, N), device="cuda")
+    want = torch.zeros((T, N), dtype=torch.float64, device="cuda")
+    scale = torch.zeros((T, N), device="cuda")
+    for e, (a, b) in enumerate(ref.spans(ends.tolist(), T)):
+        want[a:b] = x[a:b].double() @ w[e].double().t()
+        scale[a:b] = ws[e]
+    for dt in (BF, F32):
+        banner(f"grouped shapes {T} {E} {N} {K} {dt}")
+        assert torch.equal(bi.bi_grouped_linear_bf16(x, w, ends, out_dtype=dt), want.to(dt))
+        y8 = bi.bi_grouped_linear_int8(xq, xs, wq, ws, ends, out_dtype=dt)
+        assert torch.equal(y8, (want.float() * xs[:, None] * scale).to(dt))
+
+
+@pytest.mark.parametrize("T,E,N,K", shapes.GROUPED_BWD)
+def test_grouped_backward_tile_shapes(bi, T, E, N, K):
+    counts = shapes.counts(T, E)
+    x, w, dy, ends = ints((T, K), 1), ints((E, N, K), 2), ints((T, N), 3), ends_of(counts)
+    want_dx = torch.zeros((T, K), dtype=torch.float64, device="cuda")
+    want_dw = torch.zeros((E, N, K), dtype=torch.float64, device="cuda")
+    for e, (a, b) in enumerate(ref.spans(ends.tolist(), T)):
+        want_dx[a:b] = dy[a:b].double() @ w[e].double()
+        want_dw[e] = dy[a:b].double().t().contiguous() @ x[a:b].double()
+    for dt in (BF, F32):
+        for dx_too, dw_too in ((True, True), (True, False), (False, True)):
+            banner(f"grouped backward shapes {T} {E} {N} {K} {dt} {dx_too} {dw_too}")
+            dx, dw = bi.bi_grouped_linear_bf16_bwd(dy, x, w, ends, need_dx=dx_too, need_dw=dw_too, dw_dtype=dt)
+            assert dx is None or torch.equal(dx, want_dx.to(BF))
+            assert dw is None or torch.equal(dw, want_dw.to(dt))
+
+
+def test_operands_past_4_gib(bi):
+    """Rows, experts and outputs whose offsets pass 32 bits."""
+    T, E, N, K = 70000, 2, 64, 32768                       # x: 4.6e9 bytes in bf16
+    x = torch.zeros((T, K), dtype=BF, device="cuda")
+    w = torch.zeros((E, N, K), dtype=BF, device="cuda")
+    probe = ints((16, K), 1)
+    w[0], w[1] = ints((N, K), 2), ints((N, K), 3)
+    x[-16:] = probe
+    ends = ends_of([T - 16, 16])
+    banner("grouped rows past 4 GiB")
+    y = bi.bi_grouped_linear_bf16(x, w, ends, out_dtype=F32)
+    assert torch.equal(y[-16:].double(), probe.double() @ w[1].double().t())
+    assert not y[:-16].any()
+    dy = torch.zeros((T, N), dtype=BF, device="cuda")
+    dy[-16:] = ints((16, N), 4)
+    dx, dw = bi.bi_grouped_linear_bf16_bwd(dy, x, w, ends, dw_dtype=F32)
+    assert torch.equal(dx[-16:].double(), (dy[-16:].double() @ w[1].double()).to(BF).double()) and not dx[:-16].any()
+    assert torch.equal(dw[1].double(), dy[-16:].double().t().contiguous() @ probe.double()) and not dw[0].any()
+    banner("8-bit rows past 4 GiB")
+    del dx, dw
+    xq = torch.zeros((140000, K), dtype=torch.int8, device="cuda")
+    xq[-16:] = probe.to(torch.int8)
+    xs, ws = torch.ones(140000, device="cuda"), torch.ones(N, device="cuda")
+    y = bi.bi_linear_int8(xq, xs, w[1].to(torch.int8), ws, out_dtype=F32)
+    assert torch.equal(y[-16:].double(), probe.double() @ w[1].double().t()) and not y[:-16].any()
+    q, s = bi.bi_quantize_int8(x)
+    assert torch.equal(q[-16:].float(), torch.round(probe.float() / s[-16:, None])) and not q[:-16].any()
+    banner("layer norm rows past 4 GiB")
+    z = torch.zeros((280000, 8192), dtype=BF, device="cuda")
+    z[-4:] = normal((4, 8192), 5)
+    n, m, r = bi.bi_layer_norm(z, save_stats=True)
+    assert torch.equal(n[-4:], bi.bi_layer_norm(z[-4:].clone())) and not n[:-4].any()
+    assert torch.equal(bi.bi_layer_norm_bwd(z, z, m, r)[0][-4:], bi.bi_layer_norm_bwd(z[-4:].clone(), z[-4:].clone(), m[-4:].clone(), r[-4:].clone())[0])
 
 
 # ---------------------------------------------------------------- a run of them

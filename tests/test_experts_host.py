@@ -6,6 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests import experts_ref as ref
+from tests import experts_shapes as shapes
 
 bi = pytest.importorskip("deterministic_persistent_gemm_amd")
 L = bi.lib()
@@ -133,7 +134,7 @@ def test_workspace_sizes_and_refusals():
 def test_tile_query_refusals():
     out = (bi._I32 * 8)()
     tile = L.bi_lab_grouped_tile
-    assert tile(4, 4, 4, 32, 64, 1, out) == tile(0, 0, 4, 32, 64, 1, out) == tile(0, 4, 4, 32, 64, 3, out) == bi.BI_EINVAL
+    assert tile(6, 4, 4, 32, 64, 1, out) == tile(0, 0, 4, 32, 64, 1, out) == tile(0, 4, 4, 32, 64, 3, out) == bi.BI_EINVAL
     assert tile(0, 4, 4, 32, 64, 1, None) == bi.BI_EINVAL
     assert tile(0, 4, 4, 24, 64, 1, out) == tile(0, 4, 0, 32, 64, 1, out) == tile(0, 4, 1025, 32, 64, 1, out) == bi.BI_EUNSUPPORTED
 
@@ -221,3 +222,44 @@ def test_codes_by_hand():
 def test_spans_of_any_ends():
     assert ref.spans([2, 2, 5], 6) == [(0, 2), (2, 2), (2, 5)]
     assert ref.spans([3, 1, -7, 99], 6) == [(0, 3), (3, 3), (3, 3), (3, 6)]
+
+
+# ------------------------------------------------------------------ the tile shapes
+
+
+def steady(t, k):
+    """At least two stages past the ring."""
+    return -(-k // t["slice_k"]) >= (t["ring_stages"] + 1) * t["stage_slices"] + 1
+
+
+def test_every_int8_shape_is_tested_past_its_ring():
+    seen = set()
+    for M, N, K in shapes.INT8:
+        for dt in (bi.BI_BF16, bi.BI_F32):
+            t = bi.ffn_tile(bi.BI_FFN_INT8, M, N, K, dt)
+            if steady(t, K):
+                seen.add((t["shape"], dt))
+    assert seen == {(i, dt) for i in range(9) for dt in (bi.BI_BF16, bi.BI_F32)}
+
+
+@pytest.mark.parametrize("op,n,sizes", [
+    (bi.BI_GROUPED_BF16, 7, shapes.GROUPED), (bi.BI_GROUPED_INT8, 7, shapes.GROUPED),
+    (bi.BI_GROUPED_DX, 6, shapes.GROUPED_BWD), (bi.BI_GROUPED_DX_ALONE, 6, shapes.GROUPED_BWD),
+    (bi.BI_GROUPED_DW, 3, shapes.GROUPED_BWD), (bi.BI_GROUPED_DW_ALONE, 3, shapes.GROUPED_BWD)],
+    ids=["bf16", "int8", "dx", "dx-alone", "dw", "dw-alone"])
+def test_every_grouped_shape_is_tested_past_its_ring(op, n, sizes):
+    dx, dw = op in (bi.BI_GROUPED_DX, bi.BI_GROUPED_DX_ALONE), op in (bi.BI_GROUPED_DW, bi.BI_GROUPED_DW_ALONE)
+    dts = (bi.BI_BF16,) if dx else (bi.BI_BF16, bi.BI_F32)
+    seen = set()
+    for T, E, N, K in sizes:
+        for dt in dts:
+            t = bi.grouped_tile(op, T, E, N, K, dt)
+            if steady(t, N if dx else max(shapes.counts(T, E)) if dw else K):
+                seen.add((t["shape"], dt))
+    assert seen == {(i, dt) for i in range(n) for dt in dts}
+
+
+def test_counts_add_up():
+    for T, E, _, _ in shapes.GROUPED + shapes.GROUPED_BWD:
+        c = shapes.counts(T, E)
+        assert len(c) == E and sum(c) == T and min(c) >= 0
