@@ -169,39 +169,174 @@ __device__ __forceinline__ void rows_body(TileArgs& p, const GroupArgs& q, unsig
     tile_any<S>(p, ring, t.tm, t.tn);
 }
 
-// Workgroup w of dw: a tile of one expert, whose sum runs over its rows.  An expert
-// without rows gets zeros.  An expert's tiles are dealt to all XCDs, as one
-// expert may have many times the rows of another (an eighth of the experts to
-// each XCD: 525 us instead of 441 where demand is uneven); which of them gets one
-// more goes round from expert to expert.
+// p of expert e's dw, whose sum runs over its rows.
+__device__ __forceinline__ void at_expert(TileArgs& p, const GroupArgs& q, int e, int first, int rows)
+{
+    p.y = reinterpret_cast<unsigned char*>(p.y) + (int64_t)e * q.stride_b;
+    p.a += (int64_t)first * p.lda;
+    p.b += (int64_t)first * p.ldb;
+    p.K = rows;
+}
+
+// Zeros for tile (tm, tn): an expert without rows.
+template <typename S>
+__device__ __forceinline__ void zero_tile(const TileArgs& p, int tm, int tn)
+{
+    using C = typename S::C;
+    const int es = p.y_bf16 ? 2 : 4;
+    const int units = C::BN * es / 16, have = (p.N - tn * C::BN) * es / 16;
+    for (int i = threadIdx.x; i < C::BM * units; i += (C::NW + S::NL) * 64) {
+        const int m = tm * C::BM + i / units, u = i % units;
+        if (m < p.M && u < have)
+            reinterpret_cast<u32x4*>(reinterpret_cast<unsigned char*>(p.y) + ((int64_t)m * p.ldy + tn * C::BN) * es)[u] =
+                u32x4{0u, 0u, 0u, 0u};
+    }
+}
+
+// Workgroup w of dw, one tile.  An expert's tiles are dealt to all XCDs, as one expert
+// may have many times the rows of another; which of them gets one more goes round
+// from expert to expert.
 template <typename S>
 __device__ __forceinline__ void dw_body(TileArgs& p, const GroupArgs& q, unsigned char* ring, int w)
 {
-    using C = typename S::C;
     const int tiles = p.tiles_m * p.tiles_n, per = (tiles + 7) >> 3;
     const int j = w >> 3, e = j / per, t = ((w + e) & 7) * per + j - e * per;
     if (t >= tiles)
         return;
-    int tn;
-    const int tm = tile_at(t, p.tiles_m, p.tiles_n, tn);
-    int first, rows;
+    int first, rows, tn;
     rows_of(q, e, first, rows);
-    p.y = reinterpret_cast<unsigned char*>(p.y) + (int64_t)e * q.stride_b;
-    if (rows == 0) {
-        const int es = p.y_bf16 ? 2 : 4;
-        const int units = C::BN * es / 16, have = (p.N - tn * C::BN) * es / 16;
-        for (int i = threadIdx.x; i < C::BM * units; i += (C::NW + S::NL) * 64) {
-            const int m = tm * C::BM + i / units, u = i % units;
-            if (m < p.M && u < have)
-                reinterpret_cast<u32x4*>(reinterpret_cast<unsigned char*>(p.y) + ((int64_t)m * p.ldy + tn * C::BN) * es)[u] =
-                    u32x4{0u, 0u, 0u, 0u};
-        }
-        return;
+    at_expert(p, q, e, first, rows);
+    const int tm = tile_at(t, p.tiles_m, p.tiles_n, tn);
+    if (rows == 0)
+        zero_tile<S>(p, tm, tn);
+    else
+        tile_any<S>(p, ring, tm, tn);
+}
+
+// The largest tiles: a workgroup on every compute unit takes tile after tile.  Each XCD
+// has a range of experts of equal cost, and its workgroups take the range's tiles in
+// turn, so that an expert's rows are read into one L2 once.  32768 rows of 128 experts,
+// 1536 x 2048: 424 us where demand is uneven, 408 where it is not.  (One workgroup a
+// tile, an expert's tiles on all XCDs: 441 and 433; an eighth of the experts to each XCD:
+// 525 and 428.)
+struct GroupTable {
+    int first[kMaxExperts + 1];     // where the experts' rows begin
+    int cost[kMaxExperts + 1];      // and their costs, in slices a tile
+};
+
+// What a tile costs besides its slices: its first loads and its stores; its zeros,
+// where there are no rows.
+constexpr int kDwTileCost = 6, kDwZeroCost = 3;
+
+// Filled by the first wave.
+__device__ __forceinline__ void fill_table(GroupTable& tab, const GroupArgs& q)
+{
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x;
+        if (lane == 0)
+            tab.first[0] = tab.cost[0] = 0;
+        with_lanes(q.E, [&](auto ne) __attribute__((always_inline)) {
+            constexpr int NE = decltype(ne)::value;
+            const GroupRows<NE> r(q, lane);
+            int sum[NE], mine = 0;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const int rows = r.rows(i);
+                mine += lane * NE + i >= q.E ? 0 : rows > 0 ? (rows + 31) / 32 + kDwTileCost : kDwZeroCost;
+                sum[i] = mine;
+            }
+            const int before = (int)wave_incl_scan((uint32_t)mine, lane) - mine;
+#pragma unroll
+            for (int i = 0; i < NE; ++i)
+                if (lane * NE + i < q.E) {
+                    tab.first[lane * NE + i + 1] = r.end[i];
+                    tab.cost[lane * NE + i + 1] = before + sum[i];
+                }
+        });
     }
-    p.a += (int64_t)first * p.lda;
-    p.b += (int64_t)first * p.ldb;
-    p.K = rows;
-    tile_any<S>(p, ring, tm, tn);
+    __syncthreads();
+}
+
+// The first tile of XCD x's range: costs before it make x eighths of all.
+__device__ __forceinline__ int range_start(const GroupTable& tab, int E, int tiles, int x)
+{
+    if (x == 8)
+        return E * tiles;
+    const int64_t at = (int64_t)tab.cost[E] * x;
+    int e = 0;                                          // the last expert with 8 cost[e] <= at
+    for (int step = 512; step > 0; step >>= 1)
+        if (e + step < E && 8 * (int64_t)tab.cost[e + step] <= at)
+            e += step;
+    const int64_t into = at - 8 * (int64_t)tab.cost[e], cost = 8 * (int64_t)(tab.cost[e + 1] - tab.cost[e]);
+    return e * tiles + (int)(into * tiles / cost);
+}
+
+// A tile's first loads are issued before the tile before it is stored, and need not
+// wait for its stores: the counter of both falls in order.
+template <typename S>
+__device__ __forceinline__ void dw_all(const TileArgs& p, const GroupArgs& q, unsigned char* ring, GroupTable& tab, int w, int groups)
+{
+    using C = typename S::C;
+    static_assert(C::kGrouped && C::R == 2 && S::NL == 0, "no loads are under way at a tile's end");
+    fill_table(tab, q);
+    const int lane = threadIdx.x & 63, wave = (int)uniform(threadIdx.x >> 6);
+    const int tiles = p.tiles_m * p.tiles_n, x = w & 7, step = groups >> 3;
+    const int end = (int)uniform((uint32_t)range_start(tab, q.E, tiles, x + 1));
+    int t = (int)uniform((uint32_t)range_start(tab, q.E, tiles, x)) + (w >> 3);
+
+    TileArgs now = p, next = p;                         // of the tile at work and of the one that comes
+    int m0 = 0, n0 = 0, next_m0 = 0, next_n0 = 0;
+    // the next tile with rows from t on, zeros for those without; false at the end
+    auto advance = [&]() __attribute__((always_inline)) {
+        for (; t < end; t += step) {
+            const int e = t / tiles;
+            const int first = (int)uniform((uint32_t)tab.first[e]), rows = (int)uniform((uint32_t)tab.first[e + 1]) - first;
+            int tn;
+            const int tm = tile_at(t - e * tiles, p.tiles_m, p.tiles_n, tn);
+            next = p;
+            at_expert(next, q, e, first, rows);
+            if (rows > 0) {
+                next_m0 = tm * C::BM;
+                next_n0 = tn * C::BN;
+                t += step;
+                return true;
+            }
+            zero_tile<S>(next, tm, tn);
+        }
+        return false;
+    };
+    if (!advance())
+        return;
+    TileLoads<C, C::NW> loads;
+    loads.init(next, ring, wave, lane, next_m0, next_n0);
+    loads.issue(0);
+    constexpr int kStores = C::FM * C::FN / 2;          // of a whole bf16 tile, per wave
+    int stores = 0;
+    for (bool more = true; more;) {
+        now = next;
+        m0 = next_m0;
+        n0 = next_n0;
+        asm volatile("" : : : "memory");                // no store moves down past the wait that counts it
+        if (stores == kStores)
+            async_wait<kStores>();
+        else if (stores == 2 * kStores)
+            async_wait<2 * kStores>();
+        else
+            async_wait<0>();
+        wg_barrier();
+        f32x4 acc[C::FM][C::FN];
+        turns_sums<C>(now, ring, loads, wave, lane, acc);
+        // every wave is past its last read of the ring here (turns_group's last barrier)
+        more = advance();
+        if (more) {
+            loads.init(next, ring, wave, lane, next_m0, next_n0);
+            loads.issue(0);
+        }
+        // zeros written on the way are stores ahead of those loads: no harm.  Only a tile
+        // without ragged edges has all of its stores issued by every wave
+        stores = m0 + C::BM <= p.M && n0 + C::BN <= p.N ? (p.y_bf16 ? kStores : 2 * kStores) : 0;
+        tile_store<C>(now, acc, m0, n0, wave / C::WN, wave % C::WN, lane & 15, lane >> 4);
+    }
 }
 
 template <typename S>
@@ -211,29 +346,46 @@ __global__ __launch_bounds__((S::C::NW + S::NL) * 64) void k_grouped(TileArgs p,
     rows_body<S>(p, q, ring, (int)blockIdx.x);
 }
 
+template <typename S> constexpr bool takes_all() { return S::C::BM == 256; }
+
 template <typename S>
 __global__ __launch_bounds__((S::C::NW + S::NL) * 64) void k_grouped_dw(TileArgs p, GroupArgs q)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char ring[S::C::kRing];
-    dw_body<S>(p, q, ring, (int)blockIdx.x);
+    if constexpr (takes_all<S>()) {
+        __shared__ GroupTable tab;
+        dw_all<S>(p, q, ring, tab, (int)blockIdx.x, (int)gridDim.x);
+    } else {
+        dw_body<S>(p, q, ring, (int)blockIdx.x);
+    }
 }
 
-// Both gradients: workgroups 0 .. ndx - 1 (a multiple of 8) take dx, the rest dw.
+// Both gradients: workgroups 0 .. first - 1 (a multiple of 8) take dx, the rest dw; the
+// largest tiles the other way round, so that dx's fill the compute units as dw's
+// workgroups end.
 constexpr int kBothThreads = 512;
 
 template <typename SX, typename SW>
-__global__ __launch_bounds__(kBothThreads) void k_grouped_both(TileArgs dx, GroupArgs qx, TileArgs dw, GroupArgs qw, int ndx)
+__global__ __launch_bounds__(kBothThreads) void k_grouped_both(TileArgs dx, GroupArgs qx, TileArgs dw, GroupArgs qw, int first)
 {
     constexpr int kX = (SX::C::NW + SX::NL) * 64, kW = (SW::C::NW + SW::NL) * 64;
     static_assert(kX <= kBothThreads && kW <= kBothThreads, "one workgroup size");
     __shared__ __attribute__((aligned(1024))) unsigned char ring[SX::C::kRing > SW::C::kRing ? SX::C::kRing : SW::C::kRing];
     const int b = (int)blockIdx.x;
-    // waves that a shape does not need leave before its first barrier, which counts those that are left
-    if (b < ndx) {
-        if ((int)threadIdx.x < kX)
-            rows_body<SX>(dx, qx, ring, b);
-    } else if ((int)threadIdx.x < kW) {
-        dw_body<SW>(dw, qw, ring, b - ndx);
+    if constexpr (takes_all<SW>()) {
+        __shared__ GroupTable tab;
+        if (b < first)
+            dw_all<SW>(dw, qw, ring, tab, b, first);
+        else
+            rows_body<SX>(dx, qx, ring, b - first);
+    } else {
+        // waves that a shape does not need leave before its first barrier, which counts those that are left
+        if (b < first) {
+            if ((int)threadIdx.x < kX)
+                rows_body<SX>(dx, qx, ring, b);
+        } else if ((int)threadIdx.x < kW) {
+            dw_body<SW>(dw, qw, ring, b - first);
+        }
     }
 }
 
@@ -397,12 +549,17 @@ static int64_t rows_groups(TileArgs& a, const GroupArgs& q)
     return most_row_tiles(q.T, q.E, C::BM) * a.tiles_n;
 }
 
-template <typename C>
+template <typename S>
 static int64_t dw_groups(TileArgs& a, const GroupArgs& q)
 {
-    a.tiles_m = (a.M + C::BM - 1) / C::BM;
-    a.tiles_n = (a.N + C::BN - 1) / C::BN;
-    return ((int64_t)a.tiles_m * a.tiles_n + 7) / 8 * 8 * q.E;
+    a.tiles_m = (a.M + S::C::BM - 1) / S::C::BM;
+    a.tiles_n = (a.N + S::C::BN - 1) / S::C::BN;
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    if (!takes_all<S>())
+        return (tiles + 7) / 8 * 8 * q.E;
+    // one workgroup for every compute unit, a multiple of 8
+    const int cus = device_cu_count();
+    return tiles * q.E < (int64_t(1) << 31) ? (cus < 8 ? 8 : cus / 8 * 8) : int64_t(1) << 31;
 }
 
 // dry: only whether a launch can hold the grid
@@ -425,7 +582,7 @@ static hipError_t run_dw(TileArgs a, const GroupArgs& q, int shape, hipStream_t 
 {
     return group_shape<kGroupDw>(shape, [&](auto sh) {
         using S = decltype(sh);
-        const int64_t groups = dw_groups<typename S::C>(a, q);
+        const int64_t groups = dw_groups<S>(a, q);
         if (!grid_ok(groups))
             return hipErrorInvalidConfiguration;
         if (dry)
@@ -442,10 +599,10 @@ static hipError_t run_both(TileArgs a, const GroupArgs& qx, int sx, TileArgs b, 
             using SX = decltype(x);
             using SW = decltype(w);
             if constexpr ((SX::C::BM == 256) == (SW::C::BM == 256)) {
-                const int64_t ndx = (rows_groups<typename SX::C>(a, qx) + 7) / 8 * 8, groups = ndx + dw_groups<typename SW::C>(b, qw);
-                if (!grid_ok(groups))
+                const int64_t ndx = (rows_groups<typename SX::C>(a, qx) + 7) / 8 * 8, ndw = dw_groups<SW>(b, qw);
+                if (!grid_ok(ndx + ndw))
                     return hipErrorInvalidConfiguration;
-                k_grouped_both<SX, SW><<<(unsigned)groups, kBothThreads, 0, s>>>(a, qx, b, qw, (int)ndx);
+                k_grouped_both<SX, SW><<<(unsigned)(ndx + ndw), kBothThreads, 0, s>>>(a, qx, b, qw, (int)(takes_all<SW>() ? ndw : ndx));
             }
             return hipGetLastError();
         });

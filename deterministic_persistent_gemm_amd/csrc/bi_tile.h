@@ -227,11 +227,12 @@ constexpr int scale_ring_groups(int kb, int r)
 // A tile: BM x BN outputs (gated: BN weight rows, BN / 2 outputs) on WM x WN
 // computing waves, R ring stages of KB slices.  CA, CB: operand A / B stored by
 // columns.
-// RAGGED: many tiles have fewer rows than BM (products grouped by expert): the largest
-// tiles then leave out the loads and matrix instructions of rows that are not there.
-template <int BM_, int BN_, int WM_, int WN_, int KB_, int R_, bool CA_, bool CB_, TileType TYPE_, int EPI_, bool RAGGED_ = false>
+// GROUPED: many tiles have fewer rows than BM or a short sum (products grouped by
+// expert): tiles in turns then leave out the loads and matrix instructions of rows
+// that are not there, and the loads past the last stage.
+template <int BM_, int BN_, int WM_, int WN_, int KB_, int R_, bool CA_, bool CB_, TileType TYPE_, int EPI_, bool GROUPED_ = false>
 struct TileCfg {
-    static constexpr bool kRagged = RAGGED_ && !CA_;
+    static constexpr bool kGrouped = GROUPED_, kRagged = GROUPED_ && !CA_;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KB = KB_, R = R_, EPI = EPI_;
     static constexpr TileType TYPE = TYPE_;
     static constexpr bool CA = CA_, CB = CB_, FP4 = TYPE == kFp4;
@@ -890,14 +891,19 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
         }
     };
     // the MFMAs of a slice with loads t0 .. t1-1 of stage st spread among them
+    const int nst = (ns + 1) / 2;
+    auto load = [&](auto whole_loads, int st, int t) __attribute__((always_inline)) {
+        if (loads.past(t) || (C::kGrouped && !decltype(whole_loads)::value && st >= nst))
+            return;
+        loads.template issue_one<decltype(whole_loads)::value>(st, t);
+    };
     auto compute = [&](auto whole_loads, int st, auto t0, auto t1) __attribute__((always_inline)) {
         constexpr int kLoads = decltype(t1)::value - decltype(t0)::value;
         constexpr int kEvery = FM * FN / (kLoads > 0 ? kLoads : 1);
         if (!busy) {
 #pragma unroll
             for (int t = decltype(t0)::value; t < decltype(t1)::value; ++t)
-                if (!loads.past(t))
-                    loads.template issue_one<decltype(whole_loads)::value>(st, t);
+                load(whole_loads, st, t);
             return;
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -907,8 +913,7 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
             tile_mfma<C::TYPE>(xf[i % FM], wf[i / FM], sx[i % FM], sw[i / FM], acc[i % FM][i / FM]);
             if (i % kEvery == kEvery / 2 && i / kEvery < kLoads) {
                 __builtin_amdgcn_sched_barrier(0);
-                if (!loads.past(decltype(t0)::value + i / kEvery))
-                    loads.template issue_one<decltype(whole_loads)::value>(st, decltype(t0)::value + i / kEvery);
+                load(whole_loads, st, decltype(t0)::value + i / kEvery);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -921,8 +926,7 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
         if constexpr (!SECOND) {
 #pragma unroll
             for (int t = 0; t < kFirst; ++t)
-                if (!loads.past(t))
-                    loads.template issue_one<decltype(whole_loads)::value>(st + 1, t);
+                load(whole_loads, st + 1, t);
         }
         wg_barrier_reads_done();
         if constexpr (decltype(tail)::value)
@@ -950,7 +954,7 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
         loads.issue(1);
         wg_barrier();
     }
-    const int inside = (int)(p.K / (2 * kSliceK)), nst = (ns + 1) / 2;
+    const int inside = (int)(p.K / (2 * kSliceK));
     constexpr int kAhead = SECOND ? 2 : 1;
     int st = 0;
     for (; st + kAhead < inside; ++st)
@@ -964,32 +968,40 @@ __device__ __forceinline__ void turns_group(const TileArgs& p, unsigned char* ri
     async_wait<0>();
 }
 
+// A tile's sums, its stage 0 having landed for every wave.
 template <typename C>
-__device__ __forceinline__ void turns_body(const TileArgs& p, unsigned char* ring, int tm, int tn)
+__device__ __forceinline__ void turns_sums(const TileArgs& p, unsigned char* ring, const TileLoads<C, C::NW>& loads, int w, int lane,
+                                           f32x4 (&acc)[C::FM][C::FN])
 {
     static_assert(C::KB == 2 && C::R == 2 && C::NW == 8, "eight waves, two stages of two slices");
-    const int lane = threadIdx.x & 63, w = (int)uniform(threadIdx.x >> 6);
     const int wm = w / C::WN, wn = w % C::WN;
     const int r = lane & 15, g = lane >> 4;
-    const int m0 = tm * C::BM, n0 = tn * C::kOutN;
     const int ns = (int)((p.K + C::kSliceK - 1) / C::kSliceK);
-    TileLoads<C, C::NW> loads;
-    loads.init(p, ring, w, lane, m0, n0);
-    f32x4 acc[C::FM][C::FN];
 #pragma unroll
     for (int fm = 0; fm < C::FM; ++fm)
 #pragma unroll
         for (int fn = 0; fn < C::FN; ++fn)
             acc[fm][fn] = f32x4{0.f, 0.f, 0.f, 0.f};
-    loads.issue_first_scales();
-    loads.issue(0);
-    async_wait<0>();
-    wg_barrier();
     if (w < 4)
         turns_group<C, false>(p, ring, loads, ns, wm, wn, r, g, acc);
     else
         turns_group<C, true>(p, ring, loads, ns, wm, wn, r, g, acc);
-    tile_store<C>(p, acc, m0, n0, wm, wn, r, g);
+}
+
+template <typename C>
+__device__ __forceinline__ void turns_body(const TileArgs& p, unsigned char* ring, int tm, int tn)
+{
+    const int lane = threadIdx.x & 63, w = (int)uniform(threadIdx.x >> 6);
+    const int m0 = tm * C::BM, n0 = tn * C::kOutN;
+    TileLoads<C, C::NW> loads;
+    loads.init(p, ring, w, lane, m0, n0);
+    f32x4 acc[C::FM][C::FN];
+    loads.issue_first_scales();
+    loads.issue(0);
+    async_wait<0>();
+    wg_barrier();
+    turns_sums<C>(p, ring, loads, w, lane, acc);
+    tile_store<C>(p, acc, m0, n0, w / C::WN, w % C::WN, lane & 15, lane >> 4);
 }
 
 // Small tiles, where a wave has too few MFMAs per slice to hide the latency of

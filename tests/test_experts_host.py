@@ -104,8 +104,8 @@ def test_more_workgroups_than_a_launch_holds():
     assert grouped(T=T, N=1024, E=1024, ldy=1024) == bi.BI_EUNSUPPORTED
     assert grouped_int8(T=T, N=1024, E=1024, ldy=1024) == bi.BI_EUNSUPPORTED
     assert grouped_bwd(T=T, N=32, K=1024, ldx=1024, ldw=1024, lddx=1024, dw=None) == bi.BI_EUNSUPPORTED
-    # dw alone: 1024 experts of 512 x 512 tiles of 256 x 256 and more
-    n = 1 << 18
+    # dw alone: 2^32 tiles of 256 x 256
+    n = 1 << 19
     assert grouped_bwd(dx=None, E=1024, N=n, K=n, lddy=n, ldx=n, lddw=n, sdw=n * n) == bi.BI_EUNSUPPORTED
     # ... and beside a dx that would fit: nothing is enqueued, which without a GPU would be a HIP error
     assert grouped_bwd(E=1024, N=n, K=n, lddy=n, ldx=n, ldw=n, lddx=n, lddw=n, sdw=n * n) == bi.BI_EUNSUPPORTED
