@@ -373,6 +373,39 @@ def test_grouped_backward_tile_shapes(bi, T, E, N, K):
             assert dw is None or torch.equal(dw, want_dw.to(dt))
 
 
+def _skewed(T, E, kind):
+    if kind == "one":
+        return [0] * (E // 2) + [T] + [0] * (E - E // 2 - 1)
+    if kind == "last":
+        return [0] * (E - 1) + [T]
+    if kind == "few":                                   # many more experts without rows than with
+        c = [T // 7 if e % (E // 7 + 1) == 3 else 0 for e in range(E)]
+        c[0] += T - sum(c)
+        return c
+    return shapes.counts(T, E)
+
+
+@pytest.mark.parametrize("kind", ["half", "one", "last", "few"])
+@pytest.mark.parametrize("T,E,N,K", [(9000, 40, 768, 1024), (3001, 300, 512, 512), (9000, 40, 1008, 1504)])
+def test_largest_weight_gradient_tiles(bi, T, E, N, K, kind):
+    """Several tiles to a workgroup, whole and ragged ones, with experts without rows
+    between, before and behind them."""
+    assert bi.grouped_tile(bi.BI_GROUPED_DW_ALONE, T, E, N, K)["rows"] == 256
+    x, w, dy, ends = ints((T, K), 1), ints((E, N, K), 2), ints((T, N), 3), ends_of(_skewed(T, E, kind))
+    want_dx = torch.zeros((T, K), dtype=torch.float64, device="cuda")
+    want = torch.zeros((E, N, K), dtype=torch.float64, device="cuda")
+    for e, (a, b) in enumerate(ref.spans(ends.tolist(), T)):
+        if b > a:
+            want_dx[a:b] = dy[a:b].double() @ w[e].double()
+            want[e] = dy[a:b].double().t().contiguous() @ x[a:b].double()
+    for dt in (BF, F32):
+        banner(f"largest dw {T} {E} {N} {K} {kind} {dt}")
+        for _ in range(3):
+            assert torch.equal(bi.bi_grouped_linear_bf16_bwd(dy, x, None, ends, need_dx=False, dw_dtype=dt)[1], want.to(dt))
+            dx, dw = bi.bi_grouped_linear_bf16_bwd(dy, x, w, ends, dw_dtype=dt)
+            assert torch.equal(dw, want.to(dt)) and torch.equal(dx, want_dx.to(BF))
+
+
 def test_operands_past_4_gib(bi):
     """Rows, experts and outputs whose offsets pass 32 bits."""
     T, E, N, K = 70000, 2, 64, 32768                       # x: 4.6e9 bytes in bf16
