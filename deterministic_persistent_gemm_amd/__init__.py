@@ -442,13 +442,16 @@ def _scratch(nbytes, device, given, name):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _call(fn, name, dev, *args):
     """Enqueue on GPU `dev`, on its current stream."""
-    if torch._C._cuda_getDevice() == dev:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if _current_device() == dev:
+        st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+            st = fn(*args, _raw_stream(dev))
     if st != BI_OK:
         raise BIError(st, name)
 
@@ -627,16 +630,31 @@ def bi_linear_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: to
 
 
 # -------------------------- experts as operators of their own, layer norm, int8
+#
+# These calls are as short as their launches (4 us), so a tensor in the usual layout
+# is taken at one test; `_rows` looks at the others and names what is wrong.
+
+
+def _matrix(t, dtype, rows, cols, dev, name, what):
+    """Address and row pitch (in elements) of a [rows, cols] tensor on GPU `dev`.  The
+    widths are multiples of 16 bytes."""
+    p = t.data_ptr()
+    if t.is_contiguous() and t.dtype is dtype and t.get_device() == dev and dev >= 0 and t.shape == (rows, cols) and p % 16 == 0:
+        return p, cols
+    return p, _rows(t, dtype, rows, cols, dev, name, what)
 
 
 def _vector(t, dtype, n, dev, name, what, align=16):
-    """A contiguous vector of n elements on GPU `dev` (None passes)."""
+    """Address of a contiguous vector of n elements on GPU `dev`; None passes."""
     if t is None:
-        return
+        return None
+    p = t.data_ptr()
+    if t.dtype is dtype and t.dim() == 1 and t.numel() == n and t.is_contiguous() and t.get_device() == dev and dev >= 0 \
+            and p % align == 0:
+        return p
     if t.dtype != dtype:
         raise TypeError(f"{name}: {what} must be {dtype}, got {t.dtype}")
-    if t.shape != (n,) or not t.is_contiguous() or dev < 0 or t.get_device() != dev or t.data_ptr() % align:
-        raise ValueError(f"{name}: {what} must be a contiguous, {align}-byte aligned [{n}] tensor on the other tensors' GPU")
+    raise ValueError(f"{name}: {what} must be a contiguous, {align}-byte aligned [{n}] tensor on the other tensors' GPU")
 
 
 def _norm_sizes(name, H):
@@ -655,24 +673,28 @@ def bi_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: tor
     if x.dim() != 2:
         raise ValueError(f"{name}: x is [M, H]")
     M, H = x.shape
-    xcode = _dtype_code(x.dtype, name, "x")
-    ydt = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
-    ycode = _dtype_code(ydt, name, "out")
-    _norm_sizes(name, H)
+    xdt = x.dtype
+    ydt = out.dtype if out is not None else xdt if out_dtype is None else out_dtype
+    xcode, ycode = _DT.get(xdt), _DT.get(ydt)
+    if xcode is None or ycode is None:
+        _dtype_code(xdt, name, "x"), _dtype_code(ydt, name, "out")
+    if H % 8 or not 0 < H <= 16384:
+        _norm_sizes(name, H)
     dev = x.get_device()
-    ldx = _rows(x, x.dtype, M, H, dev, name, "x")
-    _vector(weight, torch.float32, H, dev, name, "weight")
-    _vector(bias, torch.float32, H, dev, name, "bias")
+    xp, ldx = _matrix(x, xdt, M, H, dev, name, "x")
+    wp = _vector(weight, torch.float32, H, dev, name, "weight")
+    bp = _vector(bias, torch.float32, H, dev, name, "bias")
     if out is None:
         out, ldy = x.new_empty(M, H, dtype=ydt), H
+        yp = out.data_ptr()
     else:
-        ldy = _rows(out, ydt, M, H, dev, name, "out")
-    mean = rstd = None
+        yp, ldy = _matrix(out, ydt, M, H, dev, name, "out")
     if save_stats:
         mean, rstd = x.new_empty(M, dtype=torch.float32), x.new_empty(M, dtype=torch.float32)
-    _call(_lib.bi_layer_norm, name, dev, x.data_ptr(), xcode, ldx, _dp(weight), _dp(bias), eps, out.data_ptr(), ycode, ldy,
-          _dp(mean), _dp(rstd), M, H)
-    return (out, mean, rstd) if save_stats else out
+        _call(_lib.bi_layer_norm, name, dev, xp, xcode, ldx, wp, bp, eps, yp, ycode, ldy, mean.data_ptr(), rstd.data_ptr(), M, H)
+        return out, mean, rstd
+    _call(_lib.bi_layer_norm, name, dev, xp, xcode, ldx, wp, bp, eps, yp, ycode, ldy, None, None, M, H)
+    return out
 
 
 def bi_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -685,41 +707,51 @@ def bi_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rst
     if dy.dim() != 2:
         raise ValueError(f"{name}: dy is [M, H]")
     M, H = dy.shape
-    dcode, xcode = _dtype_code(dy.dtype, name, "dy"), _dtype_code(x.dtype, name, "x")
-    _norm_sizes(name, H)
+    ddt, xdt = dy.dtype, x.dtype
+    dcode, xcode = _DT.get(ddt), _DT.get(xdt)
+    if dcode is None or xcode is None:
+        _dtype_code(ddt, name, "dy"), _dtype_code(xdt, name, "x")
+    if H % 8 or not 0 < H <= 16384:
+        _norm_sizes(name, H)
     dev = dy.get_device()
-    lddy = _rows(dy, dy.dtype, M, H, dev, name, "dy")
-    ldx = _rows(x, x.dtype, M, H, dev, name, "x")
-    _vector(mean, torch.float32, M, dev, name, "mean", 4)
-    _vector(rstd, torch.float32, M, dev, name, "rstd", 4)
-    _vector(weight, torch.float32, H, dev, name, "weight")
+    dyp, lddy = _matrix(dy, ddt, M, H, dev, name, "dy")
+    xp, ldx = _matrix(x, xdt, M, H, dev, name, "x")
+    mp = _vector(mean, torch.float32, M, dev, name, "mean", 4)
+    rp = _vector(rstd, torch.float32, M, dev, name, "rstd", 4)
+    wp = _vector(weight, torch.float32, H, dev, name, "weight")
     dx = x.new_empty(M, H) if need_dx else None
     dw = x.new_empty(H, dtype=torch.float32) if need_dw else None
     db = x.new_empty(H, dtype=torch.float32) if need_db else None
-    ws = _scratch(_lib.bi_layer_norm_bwd_workspace_size(M, H) if need_dw or need_db else 0, dy.device, ws, name)
-    _call(_lib.bi_layer_norm_bwd, name, dev, dy.data_ptr(), dcode, lddy, x.data_ptr(), xcode, ldx, mean.data_ptr(),
-          rstd.data_ptr(), _dp(weight), _dp(dx), H, _dp(dw), _dp(db), M, H, _dp(ws), 0 if ws is None else ws.numel())
+    need = _lib.bi_layer_norm_bwd_workspace_size(M, H) if need_dw or need_db else 0
+    if need or ws is not None:
+        ws = _scratch(need, dy.device, ws, name)
+    _call(_lib.bi_layer_norm_bwd, name, dev, dyp, dcode, lddy, xp, xcode, ldx, mp, rp, wp, _dp(dx), H, _dp(dw), _dp(db), M, H,
+          _dp(ws), 0 if ws is None else ws.numel())
     return dx, dw, db
 
 
 def _experts(w, dtype, E, N, K, dev, name, what):
-    """Row pitch and expert stride (elements) of weights [E, N, K]."""
+    """Address, row pitch and expert stride (elements) of weights [E, N, K]."""
+    p = w.data_ptr()
+    if w.is_contiguous() and w.dtype is dtype and w.get_device() == dev and dev >= 0 and w.shape == (E, N, K) and p % 16 == 0:
+        return p, K, N * K
     if w.dim() != 3 or w.shape != (E, N, K):
         raise ValueError(f"{name}: {what} must have shape {(E, N, K)}, got {tuple(w.shape)}")
     ldw = _rows(w[0], dtype, N, K, dev, name, what)
     step = w.stride(0) if E > 1 else 0
     if step < 0 or step * _ELEM[dtype] % 16:
         raise ValueError(f"{name}: {what}'s experts must lie a multiple of 16 bytes apart; its strides are {w.stride()}")
-    return ldw, step
+    return p, ldw, step
 
 
 def _grouped_sizes(name, w, what):
     if w.dim() != 3:
         raise ValueError(f"{name}: {what} is [E, N, K]")
     E, N, K = w.shape
-    if E == 0 or E > 1024:
+    if not 0 < E <= 1024:
         raise ValueError(f"{name}: needs 1 to 1024 experts, got {E}")
-    _sizes(name, N, K)
+    if N % 16 or K % 32 or not N or not K:
+        _sizes(name, N, K)
     return E, N, K
 
 
@@ -736,16 +768,19 @@ def bi_grouped_linear_bf16(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor,
     E, N, K = _grouped_sizes(name, w, "w")
     T = x.shape[0]
     dev = x.get_device()
-    ldx = _rows(x, torch.bfloat16, T, K, dev, name, "x")
-    ldw, step = _experts(w, torch.bfloat16, E, N, K, dev, name, "w")
-    _vector(ends, torch.int64, E, dev, name, "ends", 8)
-    code = _dtype_code(out_dtype if out is None else out.dtype, name, "out")
+    xp, ldx = _matrix(x, torch.bfloat16, T, K, dev, name, "x")
+    wp, ldw, step = _experts(w, torch.bfloat16, E, N, K, dev, name, "w")
+    ep = _vector(ends, torch.int64, E, dev, name, "ends", 8)
+    ydt = out_dtype if out is None else out.dtype
+    code = _DT.get(ydt)
+    if code is None:
+        _dtype_code(ydt, name, "out")
     if out is None:
-        out, ldy = x.new_empty(T, N, dtype=out_dtype), N
+        out, ldy = x.new_empty(T, N, dtype=ydt), N
+        yp = out.data_ptr()
     else:
-        ldy = _rows(out, out.dtype, T, N, dev, name, "out")
-    _call(_lib.bi_grouped_linear_bf16, name, dev, x.data_ptr(), ldx, w.data_ptr(), ldw, step, ends.data_ptr(), E, out.data_ptr(),
-          code, ldy, T, N, K)
+        yp, ldy = _matrix(out, ydt, T, N, dev, name, "out")
+    _call(_lib.bi_grouped_linear_bf16, name, dev, xp, ldx, wp, ldw, step, ep, E, yp, code, ldy, T, N, K)
     return out
 
 
@@ -762,24 +797,32 @@ def bi_grouped_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, w: torc
     T, N = dy.shape
     E = ends.shape[0] if ends.dim() == 1 else 0
     K = w.shape[2] if need_dx else x.shape[1] if need_dw else 32
-    if E == 0 or E > 1024:
+    if not 0 < E <= 1024:
         raise ValueError(f"{name}: ends is [E], for 1 to 1024 experts")
-    code = _dtype_code(dw_dtype, name, "dw_dtype")
-    _sizes(name, N, K)
+    code = _DT.get(dw_dtype)
+    if code is None:
+        _dtype_code(dw_dtype, name, "dw_dtype")
+    if N % 16 or K % 32 or not N or not K:
+        _sizes(name, N, K)
     dev = dy.get_device()
-    lddy = _rows(dy, torch.bfloat16, T, N, dev, name, "dy")
-    _vector(ends, torch.int64, E, dev, name, "ends", 8)
-    dx = dw = None
+    dyp, lddy = _matrix(dy, torch.bfloat16, T, N, dev, name, "dy")
+    ep = _vector(ends, torch.int64, E, dev, name, "ends", 8)
+    dx = dw = xp = wp = dxp = dwp = None
     ldx = ldw = step = lddx = 0
     if need_dx:
-        ldw, step = _experts(w, torch.bfloat16, E, N, K, dev, name, "w")
-        dx = dy.new_empty(T, K) if out_dx is None else out_dx
-        lddx = _rows(dx, torch.bfloat16, T, K, dev, name, "out_dx")
+        wp, ldw, step = _experts(w, torch.bfloat16, E, N, K, dev, name, "w")
+        if out_dx is None:
+            dx, lddx = dy.new_empty(T, K), K
+            dxp = dx.data_ptr()
+        else:
+            dx = out_dx
+            dxp, lddx = _matrix(dx, torch.bfloat16, T, K, dev, name, "out_dx")
     if need_dw:
-        ldx = _rows(x, torch.bfloat16, T, K, dev, name, "x")
+        xp, ldx = _matrix(x, torch.bfloat16, T, K, dev, name, "x")
         dw = dy.new_empty(E, N, K, dtype=dw_dtype)
-    _call(_lib.bi_grouped_linear_bf16_bwd, name, dev, dy.data_ptr(), lddy, _dp(x) if need_dw else None, ldx,
-          _dp(w) if need_dx else None, ldw, step, ends.data_ptr(), E, _dp(dx), lddx, _dp(dw), code, K, N * K, T, N, K)
+        dwp = dw.data_ptr()
+    _call(_lib.bi_grouped_linear_bf16_bwd, name, dev, dyp, lddy, xp, ldx, wp, ldw, step, ep, E, dxp, lddx, dwp, code, K, N * K, T,
+          N, K)
     return dx, dw
 
 
@@ -787,22 +830,25 @@ def bi_quantize_int8(x: torch.Tensor):
     """Rows of x [rows, K] (bf16 or fp32) as 8-bit integers: (codes int8 [rows, K] in
     [-127, 127], scales fp32 [rows]), x = codes * scale up to rounding."""
     name = "bi_quantize_int8"
-    code = _dtype_code(x.dtype, name, "x")
+    xdt = x.dtype
+    code = _DT.get(xdt)
+    if code is None:
+        _dtype_code(xdt, name, "x")
     if x.dim() != 2:
         raise ValueError(f"{name}: x is [rows, K]")
     rows, K = x.shape
-    _sizes(name, 16, K)
+    if K % 32 or not K:
+        _sizes(name, 16, K)
     dev = x.get_device()
-    ldx = _rows(x, x.dtype, rows, K, dev, name, "x")
+    xp, ldx = _matrix(x, xdt, rows, K, dev, name, "x")
     q, s = x.new_empty(rows, K, dtype=torch.int8), x.new_empty(rows, dtype=torch.float32)
-    _call(_lib.bi_quantize_int8, name, dev, x.data_ptr(), code, ldx, q.data_ptr(), K, s.data_ptr(), rows, K)
+    _call(_lib.bi_quantize_int8, name, dev, xp, code, ldx, q.data_ptr(), K, s.data_ptr(), rows, K)
     return q, s
 
 
 def _int8_sizes(name, N, K):
     _sizes(name, N, K)
-    if K > 131040:
-        raise ValueError(f"{name}: k of {K} could overflow 32-bit sums; at most 131040")
+    raise ValueError(f"{name}: k of {K} could overflow 32-bit sums; at most 131040")
 
 
 def bi_linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, bias: torch.Tensor | None = None,
@@ -813,21 +859,25 @@ def bi_linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: tor
     name = "bi_linear_int8"
     if xq.dim() != 2 or wq.dim() != 2:
         raise ValueError(f"{name}: xq is [M, K] and wq is [N, K]")
-    code = _dtype_code(out_dtype if out is None else out.dtype, name, "out")
+    ydt = out_dtype if out is None else out.dtype
+    code = _DT.get(ydt)
+    if code is None:
+        _dtype_code(ydt, name, "out")
     (M, K), N = xq.shape, wq.shape[0]
-    _int8_sizes(name, N, K)
+    if N % 16 or K % 32 or not N or not 0 < K <= 131040:
+        _int8_sizes(name, N, K)
     dev = xq.get_device()
-    ldx = _rows(xq, torch.int8, M, K, dev, name, "xq")
-    ldw = _rows(wq, torch.int8, N, K, dev, name, "wq")
-    _vector(xs, torch.float32, M, dev, name, "xs", 4)
-    _vector(ws, torch.float32, N, dev, name, "ws")
-    _vector(bias, torch.float32, N, dev, name, "bias")
+    xp, ldx = _matrix(xq, torch.int8, M, K, dev, name, "xq")
+    wp, ldw = _matrix(wq, torch.int8, N, K, dev, name, "wq")
+    xsp = _vector(xs, torch.float32, M, dev, name, "xs", 4)
+    wsp = _vector(ws, torch.float32, N, dev, name, "ws")
+    bp = _vector(bias, torch.float32, N, dev, name, "bias")
     if out is None:
-        out, ldy = xq.new_empty(M, N, dtype=out_dtype), N
+        out, ldy = xq.new_empty(M, N, dtype=ydt), N
+        yp = out.data_ptr()
     else:
-        ldy = _rows(out, out.dtype, M, N, dev, name, "out")
-    _call(_lib.bi_linear_int8, name, dev, xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), _dp(bias),
-          out.data_ptr(), code, ldy, M, N, K)
+        yp, ldy = _matrix(out, ydt, M, N, dev, name, "out")
+    _call(_lib.bi_linear_int8, name, dev, xp, ldx, xsp, wp, ldw, wsp, bp, yp, code, ldy, M, N, K)
     return out
 
 
@@ -839,21 +889,26 @@ def bi_grouped_linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor,
     if xq.dim() != 2:
         raise ValueError(f"{name}: xq is [T, K]")
     E, N, K = _grouped_sizes(name, wq, "wq")
-    _int8_sizes(name, N, K)
+    if K > 131040:
+        _int8_sizes(name, N, K)
     T = xq.shape[0]
     dev = xq.get_device()
-    ldx = _rows(xq, torch.int8, T, K, dev, name, "xq")
-    ldw, step = _experts(wq, torch.int8, E, N, K, dev, name, "wq")
-    _vector(xs, torch.float32, T, dev, name, "xs", 4)
-    lds = _rows(ws, torch.float32, E, N, dev, name, "ws")
-    _vector(ends, torch.int64, E, dev, name, "ends", 8)
-    code = _dtype_code(out_dtype if out is None else out.dtype, name, "out")
+    xp, ldx = _matrix(xq, torch.int8, T, K, dev, name, "xq")
+    wp, ldw, step = _experts(wq, torch.int8, E, N, K, dev, name, "wq")
+    xsp = _vector(xs, torch.float32, T, dev, name, "xs", 4)
+    wsp, lds = _matrix(ws, torch.float32, E, N, dev, name, "ws")
+    ep = _vector(ends, torch.int64, E, dev, name, "ends", 8)
+    ydt = out_dtype if out is None else out.dtype
+    code = _DT.get(ydt)
+    if code is None:
+        _dtype_code(ydt, name, "out")
     if out is None:
-        out, ldy = xq.new_empty(T, N, dtype=out_dtype), N
+        out, ldy = xq.new_empty(T, N, dtype=ydt), N
+        yp = out.data_ptr()
     else:
-        ldy = _rows(out, out.dtype, T, N, dev, name, "out")
-    _call(_lib.bi_grouped_linear_int8, name, dev, xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, step, ws.data_ptr(),
-          lds if E > 1 else 0, ends.data_ptr(), E, out.data_ptr(), code, ldy, T, N, K)
+        yp, ldy = _matrix(out, ydt, T, N, dev, name, "out")
+    _call(_lib.bi_grouped_linear_int8, name, dev, xp, ldx, xsp, wp, ldw, step, wsp, lds if E > 1 else 0, ep, E, yp, code, ldy, T, N,
+          K)
     return out
 
 
