@@ -399,25 +399,27 @@ struct GroupShape {
 
 enum GroupOp { kGroupBf16, kGroupInt8, kGroupDx, kGroupDw };
 
-// Costs as in bi_tile_rule.h (a slice is 32 k, in 8 bits 64), fitted to timings of 320
-// problems drawn over 1 to 128 experts, 1 to 32768 rows split evenly or not, widths 128 ..
-// 4096 and k 256 .. 4096: the shapes chosen take 1.013 to 1.018 times the fastest one's
-// time on average (fitted to one half of them, 1.018 to 1.032 on the other).  Each shape
-// left out of its list costs 0.4 to 10 percent on average and up to 12 to 150 at worst.
+// Costs as in bi_tile_rule.h (a slice is 32 k, in 8 bits 64), fitted to timings of 437
+// problems: 320 drawn over 1 to 128 experts, 1 to 32768 rows split evenly or not, widths
+// 128 .. 4096 and k 256 .. 4096, and 117 with 8, 64 and 128 experts of 1024 x 1024 to 1536 x
+// 2048 at 8 to 32768 rows.  The shapes chosen take 1.005 to 1.019 times the fastest one's
+// time on average, 1.25 to 1.49 at worst (costs fitted to one half of the drawn
+// problems: 1.018 to 1.032 on the other).  A shape less in its list costs 0.4 to 10
+// percent on average and 12 to 150 at worst.
 static const TileShape kRowShapes[] = {
-    {16, 16, 3.04f, 0.035f, 1.36f}, {16, 32, 2.18f, 0.072f, 0.85f}, {32, 64, 1.99f, 0.097f, 1.14f}, {32, 128, 1.83f, 0.125f, 1.32f},
+    {16, 16, 2.58f, 0.033f, 1.39f}, {16, 32, 1.74f, 0.072f, 0.71f}, {32, 64, 1.73f, 0.092f, 1.33f}, {32, 128, 1.47f, 0.146f, 1.20f},
     {64, 128, 2.11f, 0.163f, 0.f},  {128, 128, 3.19f, 0.460f, 0.71f}, {256, 256, 3.89f, 0.753f, 0.f},
 };
 static const TileShape kRow8Shapes[] = {
-    {16, 16, 3.66f, 0.047f, 1.03f}, {16, 32, 2.65f, 0.086f, 0.66f}, {32, 64, 4.47f, 0.113f, 0.56f}, {32, 128, 2.81f, 0.182f, 0.99f},
-    {64, 128, 2.81f, 0.209f, 0.f},  {128, 128, 4.89f, 0.612f, 0.59f}, {256, 256, 7.00f, 0.875f, 0.f},
+    {16, 16, 3.24f, 0.046f, 1.18f}, {16, 32, 3.09f, 0.079f, 0.69f}, {32, 64, 4.07f, 0.072f, 0.73f}, {32, 128, 2.83f, 0.173f, 1.04f},
+    {64, 128, 2.82f, 0.196f, 0.f},  {128, 128, 5.48f, 0.589f, 0.65f}, {256, 256, 10.70f, 1.142f, 0.f},
 };
 static const TileShape kDxShapes[] = {
-    {16, 64, 3.48f, 0.103f, 0.96f}, {32, 32, 2.02f, 0.101f, 0.98f},  {64, 64, 1.98f, 0.128f, 1.14f},
-    {64, 128, 2.47f, 0.135f, 0.f},  {128, 128, 4.17f, 0.401f, 0.71f}, {256, 256, 8.38f, 0.694f, 0.f},
+    {16, 64, 2.38f, 0.108f, 1.20f}, {32, 32, 2.04f, 0.111f, 1.07f},  {64, 64, 1.96f, 0.144f, 1.04f},
+    {64, 128, 2.19f, 0.144f, 0.f},  {128, 128, 4.17f, 0.401f, 0.71f}, {256, 256, 9.32f, 0.509f, 0.f},
 };
 static const TileShape kDwShapes[] = {
-    {64, 64, 3.52f, 0.209f, 0.56f}, {128, 128, 3.59f, 0.622f, 0.60f}, {256, 256, 7.84f, 0.973f, 0.f},
+    {64, 64, 3.54f, 0.178f, 0.64f}, {128, 128, 3.59f, 0.622f, 0.60f}, {256, 256, 8.86f, 1.103f, 0.f},
 };
 constexpr int kNumRowShapes = 7, kNumDxShapes = 6, kNumDwShapes = 3;
 
@@ -482,6 +484,9 @@ static int64_t likely_row_tiles(int64_t T, int64_t E, int bm)
     return (int64_t)((t > a ? t : a) + 0.5f);
 }
 
+// f32_out counts for y alone: dw's stores, the same bytes in any shape, are what all its
+// shapes wait for (65 problems in fp32: 1.020 of the fastest, with the wider stores priced
+// by the tile 1.026).
 static int pick_group(GroupOp op, int64_t T, int64_t E, int64_t N, int64_t K, bool f32_out)
 {
     const TileShape* t = op == kGroupDx ? kDxShapes : op == kGroupDw ? kDwShapes : op == kGroupInt8 ? kRow8Shapes : kRowShapes;
@@ -498,7 +503,7 @@ static int pick_group(GroupOp op, int64_t T, int64_t E, int64_t N, int64_t K, bo
             tiles = likely_row_tiles(T, E, t[i].bm) * ((cols + t[i].bn - 1) / t[i].bn);
             slices = op == kGroupDx ? (N + 31) / 32 : op == kGroupInt8 ? (K + 63) / 64 : (K + 31) / 32;
         }
-        const float time = tiles_time(t[i], tiles, slices, f32_out, cus);
+        const float time = tiles_time(t[i], tiles, slices, f32_out && op != kGroupDw, cus);
         if (i == 0 || time < best_time) {
             best = i;
             best_time = time;
@@ -518,10 +523,10 @@ struct GroupBwdPlan {
     bool together;
 };
 
-static GroupBwdPlan plan_grouped_bwd(int64_t T, int64_t E, int64_t N, int64_t K, bool dw_f32)
+static GroupBwdPlan plan_grouped_bwd(int64_t T, int64_t E, int64_t N, int64_t K)
 {
     constexpr int kMostDx = kNumDxShapes - 1, kMostDw = kNumDwShapes - 1;
-    const int dx = pick_group(kGroupDx, T, E, N, K, false), dw = pick_group(kGroupDw, T, E, N, K, dw_f32);
+    const int dx = pick_group(kGroupDx, T, E, N, K, false), dw = pick_group(kGroupDw, T, E, N, K, false);
     if (dw < kMostDw)
         return {dx, dw, dx < kMostDx};
     return dx >= 3 ? GroupBwdPlan{kMostDx, kMostDw, true} : GroupBwdPlan{dx, kMostDw - 1, true};
@@ -672,10 +677,10 @@ hipError_t launch_grouped_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* 
     const GroupArgs qw{ends, (int)E, (int)T, stride_dw * (dw_bf16 ? 2 : 4), 0};
     const bool do_dx = dx && T > 0;
     if (!do_dx)
-        return dw ? run_dw(b, qw, pick_group(kGroupDw, T, E, N, K, !dw_bf16), s) : hipSuccess;
+        return dw ? run_dw(b, qw, pick_group(kGroupDw, T, E, N, K, false), s) : hipSuccess;
     if (!dw)
         return run_rows<kGroupDx>(a, qx, pick_group(kGroupDx, T, E, N, K, false), s);
-    const GroupBwdPlan plan = plan_grouped_bwd(T, E, N, K, !dw_bf16);
+    const GroupBwdPlan plan = plan_grouped_bwd(T, E, N, K);
     if (plan.together)
         return run_both(a, qx, plan.dx, b, qw, plan.dw, s);
     // both grids are checked before either launch: a refused call enqueues nothing
@@ -700,7 +705,7 @@ TileInfo grouped_tile_info(int op, int64_t T, int64_t E, int64_t N, int64_t K, i
     case BI_GROUPED_DW_ALONE: return group_shape<kGroupDw>(alone(kGroupDw), info(alone(kGroupDw)));
     default: break;
     }
-    const GroupBwdPlan plan = plan_grouped_bwd(T, E, N, K, !out_bf16);
+    const GroupBwdPlan plan = plan_grouped_bwd(T, E, N, K);
     if (op == BI_GROUPED_DX)
         return group_shape<kGroupDx>(plan.dx, info(plan.dx));
     return plan.together ? both_dw_shape(plan.dw, info(plan.dw)) : group_shape<kGroupDw>(plan.dw, info(plan.dw));

@@ -386,7 +386,7 @@ def _skewed(T, E, kind):
 
 
 @pytest.mark.parametrize("kind", ["half", "one", "last", "few"])
-@pytest.mark.parametrize("T,E,N,K", [(9000, 40, 768, 1024), (3001, 300, 512, 512), (9000, 40, 1008, 1504)])
+@pytest.mark.parametrize("T,E,N,K", [(9000, 40, 768, 1024), (3001, 300, 1024, 1024), (9000, 40, 1008, 1504)])
 def test_largest_weight_gradient_tiles(bi, T, E, N, K, kind):
     """Several tiles to a workgroup, whole and ragged ones, with experts without rows
     between, before and behind them."""
