@@ -88,6 +88,9 @@ struct NormArgs {
     int H;
 };
 
+// Bound by HBM from a few thousand rows on, by one pass of latency before: 8192 rows of
+// 4096, fp32 to bf16 with statistics, 40.7 us (201 MB, 4.95 TB/s; a large copy reaches
+// 5.1), bf16 28.2; one row of 4096 3.2 us.
 template <bool XB, bool YB, int T, int P, int TEAMS>
 __global__ __launch_bounds__(T * TEAMS) void k_layer_norm(NormArgs p)
 {
@@ -216,6 +219,10 @@ __device__ __forceinline__ void column_sums(const NormBwdArgs& p, int block, flo
         to[at] = ((part[0][col] + part[1][col]) + part[2][col]) + part[3][col];
 }
 
+// One pass over dy and x for all three outputs.  512 threads and one workgroup per compute
+// unit: fewer partials of dw and db to write and to add.  8192 rows of 4096 bf16: 43.4 us
+// with the fold (218 MB with the partials, 5.0 TB/s), 5.5 of them the second launch; 333
+// rows of 2048, columns summed beside the rows, 5.2 us.
 template <bool DB, bool XB, int T, int P, int TEAMS>
 __global__ __launch_bounds__(T * TEAMS) void k_layer_norm_bwd(NormBwdArgs p)
 {

@@ -333,8 +333,9 @@ bi_status_t bi_linear_mxfp4(const uint8_t* xq, int64_t ldxq, const uint8_t* xs, 
  *   m = sum x / H,  v = sum (x - m)^2 / H,  r = 1 / sqrt(v + eps)
  *   y = (x - m) r w + b              fp32 math, one rounding to bf16 or none
  * w, b: [H] fp32, or NULL for ones and zeros.  mean, rstd: [M] fp32 (4-byte
- * aligned), which receive m and r for the backward pass, or NULL.  Requires
- * H % 8 == 0, H <= 16384 (BI_EUNSUPPORTED otherwise) and a finite eps >= 0. */
+ * aligned), which receive m and r for the backward pass, or NULL.  y may be x
+ * itself, with its type and pitch.  Requires H % 8 == 0, H <= 16384
+ * (BI_EUNSUPPORTED otherwise) and a finite eps >= 0. */
 bi_status_t bi_layer_norm(const void* x, int32_t x_dtype, int64_t ldx, const float* w, const float* b, float eps,
                           void* y, int32_t y_dtype, int64_t ldy, float* mean, float* rstd,
                           int64_t M, int64_t H, hipStream_t stream);
