@@ -27,9 +27,40 @@ __device__ __forceinline__ int code_of(float x, float s, float inv)
     return above > 0.f || (above == 0.f && odd) ? i + 1 : below < 0.f || (below == 0.f && odd) ? i - 1 : i;
 }
 
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d)
+// The low bytes of a .. d.
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+    const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), hi = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+    return lo | hi;
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// The codes of chunk i.  Adding 1.5 * 2^23 to x inv rounds it to the nearest integer,
+// which is then in the sum's low bits.  x inv is within 127.5 * 2^-24 of x / s, so that
+// integer is the code unless one of the eight lies that near to a halfway point; only
+// then (rows of random values: one chunk in 6000) are the sides decided one by one.
+template <bool BF, int P>
+__device__ __forceinline__ u32x2 codes_of(const RowRaw<BF, P>& r, int i, float s, float inv)
+{
+    constexpr float kRound = 12582912.0f;
+    uint32_t k[8];
+    float off = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float x = r.at(i, j), t = __builtin_fmaf(x, inv, kRound);
+        off = fmaxf(off, fabsf(__builtin_fmaf(x, inv, kRound - t)));
+        k[j] = __float_as_uint(t);
+    }
+    if (off > 0.49999f) {
+        // tiny rows are scaled up by a power of two, so that no half step is subnormal
+        const float up = s < 8.67361738e-19f ? 1.84467441e19f : 1.0f;      // 2^-60, 2^64
+        const float s1 = s * up, inv1 = 1.0f / s1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            k[j] = (uint32_t)code_of(r.at(i, j) * up, s1, inv1);
+    }
+    return u32x2{pack4(k[0], k[1], k[2], k[3]), pack4(k[4], k[5], k[6], k[7])};
 }
 
 // The largest magnitude of a thread's values by bit pattern, so that NaN and
@@ -46,46 +77,48 @@ __device__ __forceinline__ uint32_t top_of(const RowRaw<BF, P>& r)
     return top;
 }
 
-// One workgroup per row, whose first P chunks of 8 values per thread stay in
+// A team of T threads per row, whose first P chunks of 8 values per thread stay in
 // registers between the search for the largest and the codes; longer rows are read
 // again.  The next row is on its way meanwhile.  Bound by latency for few rows (3.8 us
-// for 16 of 4096) and by the arithmetic of the codes beside memory for many: 4096 rows of
-// 4096 bf16 take 16.2 us (50 MB, 3.1 TB/s).
-template <bool BF, int P>
+// for 16 of 4096); 4096 rows of 4096 bf16 take 16.2 us (50 MB, 3.1 TB/s), two rows to a
+// workgroup and so as much its start and end as memory, fp32 19.0 (4.4 TB/s), 4096 rows of
+// 8192 fp32 33.3 (5.0 TB/s).
+template <bool BF, int T, int P>
 __global__ __launch_bounds__(256) void k_quantize_int8(const void* __restrict__ x, int64_t ldx, uint8_t* __restrict__ q,
                                                        int64_t ldq, float* __restrict__ sc, int64_t rows, int chunks)
 {
-    __shared__ uint32_t tops[2][4];
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    const int tid = threadIdx.x;
+    constexpr int TEAMS = 256 / T, W = T / 64;
+    __shared__ uint32_t tops[2][TEAMS][W];
+    const int t = threadIdx.x % T, team = (int)uniform(threadIdx.x / T);
     int turn = 0;
+    const int64_t step = (int64_t)gridDim.x * TEAMS;
+    int64_t m = (int64_t)blockIdx.x * TEAMS + team;
     RowRaw<BF, P> cur, next;
-    cur.template load<256>(x, (int64_t)blockIdx.x * ldx, tid, chunks);
-    for (int64_t m = blockIdx.x; m < rows; m += gridDim.x) {
-        next.template load<256>(x, min(m + gridDim.x, rows - 1) * ldx, tid, chunks);
+    cur.template load<T>(x, min(m, rows - 1) * ldx, t, chunks);
+    for (int64_t m0 = (int64_t)blockIdx.x * TEAMS; m0 < rows; m0 += step, m += step) {
+        next.template load<T>(x, min(m + step, rows - 1) * ldx, t, chunks);
+        const int64_t at = min(m, rows - 1);
         uint32_t top = top_of(cur);
-        for (int c = P * 256 + tid; c < chunks; c += 256) {
+        for (int c = P * T + t; c < chunks; c += T) {
             RowRaw<BF, 1> more;
-            more.template load<0>(x, m * ldx, c, chunks);
+            more.template load<0>(x, at * ldx, c, chunks);
             top = max(top, top_of(more));
         }
         top = wave_max(top);
-        if ((tid & 63) == 0)
-            tops[turn][tid >> 6] = top;
-        wg_barrier_reads_done();
-        top = max(max(tops[turn][0], tops[turn][1]), max(tops[turn][2], tops[turn][3]));
-        turn ^= 1;
+        if constexpr (W > 1) {
+            if ((t & 63) == 0)
+                tops[turn][team][t >> 6] = top;
+            wg_barrier_reads_done();
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                top = max(top, tops[turn][team][w]);
+            turn ^= 1;
+        }
         const bool finite = top < 0x7f800000u;
         const float s = finite ? fmaxf(__uint_as_float(top) * (1.0f / 127.0f), 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
-        // tiny rows are scaled up by a power of two, so that no half step is subnormal
-        const float up = s < 8.67361738e-19f ? 1.84467441e19f : 1.0f;      // 2^-60, 2^64
-        const float s1 = s * up, inv = 1.0f / s1;
+        const float inv = 1.0f / s;
         auto codes = [&](const auto& r, int i) __attribute__((always_inline)) {
-            int k[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                k[j] = code_of(r.at(i, j) * up, s1, inv);
-            const u32x2 v = {pack4(k[0], k[1], k[2], k[3]), pack4(k[4], k[5], k[6], k[7])};
+            const u32x2 v = codes_of(r, i, s, inv);
             return finite ? v : u32x2{0u, 0u};
         };
         u32x2 out[P];
@@ -94,33 +127,46 @@ __global__ __launch_bounds__(256) void k_quantize_int8(const void* __restrict__ 
             out[i] = codes(cur, i);
         cur = next;
         __builtin_amdgcn_sched_barrier(0);
-        uint8_t* to = q + m * ldq;
+        if (m < rows) {
+            uint8_t* to = q + m * ldq;
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-            if (i * 256 + tid < chunks)
-                *reinterpret_cast<u32x2*>(to + (i * 256 + tid) * 8) = out[i];
-        for (int c = P * 256 + tid; c < chunks; c += 256) {
-            RowRaw<BF, 1> more;
-            more.template load<0>(x, m * ldx, c, chunks);
-            *reinterpret_cast<u32x2*>(to + (int64_t)c * 8) = codes(more, 0);
+            for (int i = 0; i < P; ++i)
+                if (i * T + t < chunks)
+                    *reinterpret_cast<u32x2*>(to + (i * T + t) * 8) = out[i];
+            for (int c = P * T + t; c < chunks; c += T) {
+                RowRaw<BF, 1> more;
+                more.template load<0>(x, m * ldx, c, chunks);
+                *reinterpret_cast<u32x2*>(to + (int64_t)c * 8) = codes(more, 0);
+            }
+            if (t == 0)
+                sc[m] = s;
         }
-        if (tid == 0)
-            sc[m] = s;
     }
 }
 
-template <bool BF16IN>
+template <bool BF, int T, int P>
+static void quantize_shape(const void* x, int64_t ldx, uint8_t* q, int64_t ldq, float* sc, int64_t rows, int64_t K, hipStream_t s)
+{
+    constexpr int R = 256 / T;
+    const int64_t groups = (rows + R - 1) / R, most = (int64_t)device_cu_count() * 8;
+    k_quantize_int8<BF, T, P><<<(unsigned)(groups < most ? groups : most), 256, 0, s>>>(x, ldx, q, ldq, sc, rows, (int)(K / 8));
+}
+
+// A wave to a row while the row leaves most of a workgroup without work: 32768 rows of
+// 768 22.0 us (a workgroup 41.3), 8192 of 512 6.0 (11.4); 64 of 2048 5.7 (3.3).
+template <bool BF>
 static void quantize_rows(const void* x, int64_t ldx, uint8_t* q, int64_t ldq, float* sc, int64_t rows, int64_t K, hipStream_t s)
 {
-    const int chunks = (int)(K / 8);
-    const int64_t most = (int64_t)device_cu_count() * 8;
-    const unsigned grid = (unsigned)(rows < most ? rows : most);
-    if (chunks <= 256)
-        k_quantize_int8<BF16IN, 1><<<grid, 256, 0, s>>>(x, ldx, q, ldq, sc, rows, chunks);
-    else if (chunks <= 512)
-        k_quantize_int8<BF16IN, 2><<<grid, 256, 0, s>>>(x, ldx, q, ldq, sc, rows, chunks);
+    if (K <= 512)
+        quantize_shape<BF, 64, 1>(x, ldx, q, ldq, sc, rows, K, s);
+    else if (K <= 1024)
+        quantize_shape<BF, 64, 2>(x, ldx, q, ldq, sc, rows, K, s);
+    else if (K <= 2048)
+        quantize_shape<BF, 256, 1>(x, ldx, q, ldq, sc, rows, K, s);
+    else if (K <= 4096)
+        quantize_shape<BF, 256, 2>(x, ldx, q, ldq, sc, rows, K, s);
     else
-        k_quantize_int8<BF16IN, 4><<<grid, 256, 0, s>>>(x, ldx, q, ldq, sc, rows, chunks);
+        quantize_shape<BF, 256, 4>(x, ldx, q, ldq, sc, rows, K, s);
 }
 
 hipError_t launch_quantize_int8(const void* x, int x_bf16, int64_t ldx, int8_t* q, int64_t ldq, float* sc, int64_t rows,

@@ -237,6 +237,21 @@ def test_quantize(bi, K, dtype):
         assert torch.equal(s.cpu(), sd) and torch.equal(q.cpu(), qd)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+@pytest.mark.parametrize("K", [96, 480, 512, 544, 768, 1024, 1056])
+def test_quantize_a_wave_to_a_row(bi, K, dtype):
+    """Rows on both sides of the lengths that one wave takes, some workgroups' last rows
+    missing, more of them than workgroups are launched for; a row of NaN beside others."""
+    for rows in (2, 3, 9001):
+        x = normal((rows, K), K + rows, dtype=dtype)
+        x[rows // 2, K // 2] = float("nan")
+        q, s = bi.bi_quantize_int8(x)
+        qd, sd = ref.codes(x)
+        keep = torch.arange(rows) != rows // 2
+        assert torch.equal(s.cpu()[keep], sd[keep]) and torch.isnan(s[rows // 2])
+        assert torch.equal(q.cpu(), qd)
+
+
 def test_quantize_on_the_border(bi):
     """Halfway points and their neighbours, by one fp32 step either way, under scales
     that are not powers of two; tiny, huge, empty and non-finite rows."""
