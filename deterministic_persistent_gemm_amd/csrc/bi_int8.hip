@@ -80,7 +80,7 @@ __device__ __forceinline__ uint32_t top_of(const RowRaw<BF, P>& r)
 // A team of T threads per row, whose first P chunks of 8 values per thread stay in
 // registers between the search for the largest and the codes; longer rows are read
 // again.  The next row is on its way meanwhile.  Bound by latency for few rows (3.8 us
-// for 16 of 4096); 4096 rows of 4096 bf16 take 16.2 us (50 MB, 3.1 TB/s), two rows to a
+// for 16 of 4096); 4096 rows of 4096 bf16 take 16.5 us (50 MB, 3.0 TB/s), two rows to a
 // workgroup and so as much its start and end as memory, fp32 19.0 (4.4 TB/s), 4096 rows of
 // 8192 fp32 33.3 (5.0 TB/s).
 template <bool BF, int T, int P>
