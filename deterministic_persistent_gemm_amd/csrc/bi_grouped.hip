@@ -613,8 +613,10 @@ static hipError_t run_both(TileArgs a, const GroupArgs& qx, int sx, TileArgs b, 
                 if (!grid_ok(ndx + ndw))
                     return hipErrorInvalidConfiguration;
                 k_grouped_both<SX, SW><<<(unsigned)(ndx + ndw), kBothThreads, 0, s>>>(a, qx, b, qw, (int)(takes_all<SW>() ? ndw : ndx));
+                return hipGetLastError();
+            } else {
+                return hipErrorInvalidConfiguration;    // no such kernel: plan_grouped_bwd asks for no such pair
             }
-            return hipGetLastError();
         });
     });
 }

@@ -1,6 +1,9 @@
 """Layer norm, products grouped by expert and 8-bit products on the host: what
 the C entry points and the binding refuse, workspace sizes, and the 64-bit
 references against differences and hand-worked values.  Nothing here needs a GPU."""
+import os
+import subprocess
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -9,6 +12,7 @@ from tests import experts_ref as ref
 from tests import experts_shapes as shapes
 
 bi = pytest.importorskip("deterministic_persistent_gemm_amd")
+from deterministic_persistent_gemm_amd import _build
 L = bi.lib()
 P = 0x10000          # aligned, never dereferenced by validation
 BIG = 1 << 62
@@ -263,3 +267,37 @@ def test_counts_add_up():
     for T, E, _, _ in shapes.GROUPED + shapes.GROUPED_BWD:
         c = shapes.counts(T, E)
         assert len(c) == E and sum(c) == T and min(c) >= 0
+
+
+PAIRS = """
+#include "bi_grouped.hip"
+#include <cstdio>
+namespace bi { int device_cu_count() { return 256; } }
+int main()
+{
+    bi::TileArgs a{}, b{};
+    a.N = b.M = b.N = 512;
+    const bi::GroupArgs q{nullptr, 4, 300, 0, 0};
+    const int dx = bi::kNumDxShapes - 1, dw = bi::kNumDwShapes - 1;
+    for (int i = 0; i < dx; ++i)
+        printf("%d\\n", bi::run_both(a, q, i, b, q, dw, nullptr) == hipErrorInvalidConfiguration);
+    for (int i = 0; i < dw; ++i)
+        printf("%d\\n", bi::run_both(a, q, dx, b, q, i, nullptr) == hipErrorInvalidConfiguration);
+}
+"""
+
+
+def test_a_pair_of_gradient_tiles_without_a_kernel_is_refused(tmp_path):
+    """The largest tiles of one gradient beside smaller ones of the other: no kernel is built
+    for them in one launch, and asking for it must not look like a launch.  The host
+    half of the source alone, run without a GPU."""
+    if not os.path.exists(_build.HIPCC):
+        pytest.skip("no hipcc")
+    src, exe = tmp_path / "pairs.hip", tmp_path / "pairs"
+    src.write_text(PAIRS)
+    subprocess.run([_build.HIPCC, "--offload-host-only", "-fuse-cuid=none", f"--offload-arch={_build.ARCH}", "-O0", "-std=c++17",
+                    "-I", _build.INCLUDE, "-I", _build.CSRC, "-x", "hip", str(src), "-Wl,--defsym=__hip_fatbin=main", "-o", str(exe)],
+                   check=True, timeout=300)
+    got = subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=60,
+                         env=dict(os.environ, HIP_VISIBLE_DEVICES="-1", ROCR_VISIBLE_DEVICES="-1"))
+    assert got.stdout.split() == ["1"] * 7
