@@ -442,7 +442,9 @@ def _scratch(nbytes, device, given, name):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# missing where torch was built without GPU support: its tensors are refused before a call gets here
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(fn, name, dev, *args):

@@ -3,6 +3,7 @@ the C entry points and the binding refuse, workspace sizes, and the 64-bit
 references against differences and hand-worked values.  Nothing here needs a GPU."""
 import os
 import subprocess
+import sys
 
 import pytest
 
@@ -184,6 +185,24 @@ def test_binding_refuses_before_it_enqueues():
                  lambda: bi.bi_linear_int8(cpu(4, 64, dtype=i8), f, cpu(32, 64, dtype=i8), f, out_dtype=torch.int32)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_import_beside_a_torch_without_gpu_support():
+    """Recipe and workspace queries and refusals need no GPU entries of torch."""
+    run = subprocess.run([sys.executable, "-c", """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import deterministic_persistent_gemm_amd as bi
+assert bi.lib().bi_layer_norm_bwd_workspace_size(5000, 64) > 0
+assert bi.grouped_tile(bi.BI_GROUPED_BF16, 4, 4, 32, 64)["rows"] >= 16
+try:
+    bi.bi_layer_norm(torch.zeros((4, 64)))
+except ValueError:
+    print("refused")
+"""], capture_output=True, text=True, timeout=300, cwd=_build.ROOT)
+    assert run.returncode == 0 and run.stdout.split() == ["refused"], run.stderr
 
 
 # ----------------------------------------------------------------- the references
