@@ -111,6 +111,13 @@ bi_status_t check_grouped(int64_t T, int64_t N, int64_t K, int64_t E)
 // The step from expert to expert, in elements: 0 or more, whole 16-byte units.
 bool stride_ok(int64_t stride, int elem) { return stride >= 0 && stride < (int64_t(1) << 40) && (stride * elem) % 16 == 0; }
 
+// Matrices `stride` apart, of `rows` rows of `cols` elements at pitch ld >= cols, do not reach into
+// the next: stride >= (rows - 1) ld + cols, a product that may pass 64 bits.
+bool stride_holds(int64_t stride, int64_t rows, int64_t ld, int64_t cols)
+{
+    return stride >= cols && (stride - cols) / ld >= rows - 1;
+}
+
 bi_status_t check_norm(int64_t M, int64_t H, int32_t a_dtype, int32_t b_dtype)
 {
     if (M < 0 || H < 0 || !dtype_ok(a_dtype) || !dtype_ok(b_dtype))
@@ -608,7 +615,7 @@ bi_status_t bi_grouped_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const u
     if (!floats_ok(ends, 8))
         return BI_EINVAL;
     if (dw && (!matrix_ok(dw, lddw, K, dtype_bytes(dw_dtype)) || !stride_ok(stride_dw, dtype_bytes(dw_dtype)) ||
-               (E > 1 && stride_dw < (N - 1) * lddw + K)))
+               (E > 1 && !stride_holds(stride_dw, N, lddw, K))))
         return BI_EINVAL;
     if (T > 0 && (!matrix_ok(dy, lddy, N, 2) || (dx && (!matrix_ok(dx, lddx, K, 2) || !matrix_ok(w, ldw, K, 2) ||
                                                         !stride_ok(stride_w, 2))) ||

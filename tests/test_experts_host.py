@@ -84,6 +84,18 @@ def test_invalid_arguments(fn, kw):
     assert fn(**kw) == bi.BI_EINVAL
 
 
+def test_expert_strides_that_pass_64_bits():
+    """(N - 1) lddw + K past 2^63 is not taken for a small number; the least stride is."""
+    assert grouped_bwd(dx=None, N=1 << 28, lddy=1 << 28, lddw=1 << 36, sdw=1 << 20) == bi.BI_EINVAL
+    assert grouped_bwd(dx=None, N=(1 << 28) + 16, lddy=(1 << 28) + 16, lddw=1 << 39, sdw=1 << 39) == bi.BI_EINVAL
+    least = 31 * 72 + 64
+    for sdw in (least - 8, least):
+        for dt in (0, 1):
+            # an input that is refused later: only the stride tells the two calls apart
+            got = grouped_bwd(E=4, lddw=72, sdw=sdw, dt=dt, lddy=1 << 32)
+            assert got == (bi.BI_EINVAL if sdw < least else bi.BI_EUNSUPPORTED)
+
+
 UNSUPPORTED = [
     (norm, dict(H=60)), (norm, dict(H=0)), (norm, dict(H=16392, ldx=16392, ldy=16392)), (norm, dict(M=(1 << 30) + 1)),
     (norm_bwd, dict(H=4)), (norm_bwd, dict(H=16392)),
