@@ -646,6 +646,20 @@ def _matrix(t, dtype, rows, cols, dev, name, what):
     return p, _rows(t, dtype, rows, cols, dev, name, what)
 
 
+def _apart(rows, p, ld, width, q, ldq, widthq, name, what):
+    """Refuse an output of the caller's, `rows` rows of `width` bytes at pitch ld from
+    address p on, that shares bytes with an operand of as many rows: workgroups write
+    it while others still read.  Columns of one wide matrix side by side are apart.
+    (0.5 us: the calls ask only where the two lie within each other's rows.)"""
+    if rows == 0 or q >= p + (rows - 1) * ld + width or p >= q + (rows - 1) * ldq + widthq:
+        return
+    if rows > 1 and ld == ldq:
+        side = (q - p) % ld
+        if width <= side and side + widthq <= ld:
+            return
+    raise ValueError(f"{name}: {what} must not overlap an operand")
+
+
 def _vector(t, dtype, n, dev, name, what, align=16):
     """Address of a contiguous vector of n elements on GPU `dev`; None passes."""
     if t is None:
@@ -691,6 +705,9 @@ def bi_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: tor
         yp = out.data_ptr()
     else:
         yp, ldy = _matrix(out, ydt, M, H, dev, name, "out")
+        if yp < xp + M * ldx * 4 and xp < yp + M * ldy * 4 and (yp != xp or ydt is not xdt or (ldy != ldx and M > 1)):
+            xe, ye = _ELEM[xdt], _ELEM[ydt]
+            _apart(M, yp, ldy * ye, H * ye, xp, ldx * xe, H * xe, name, "out that is not x itself")
     if save_stats:
         mean, rstd = x.new_empty(M, dtype=torch.float32), x.new_empty(M, dtype=torch.float32)
         _call(_lib.bi_layer_norm, name, dev, xp, xcode, ldx, wp, bp, eps, yp, ycode, ldy, mean.data_ptr(), rstd.data_ptr(), M, H)
@@ -763,7 +780,8 @@ def bi_grouped_linear_bf16(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor,
     bf16, rows sorted by expert: e's are ends[e-1] .. ends[e] - 1.  w [E, N, K]
     bf16 (each expert an nn.Linear weight), ends [E] int64 on the GPU, ascending
     (torch.cumsum of the experts' row counts).  Rows from ends[-1] on are not
-    written: in a y made here they hold anything, in `out` what they held."""
+    written: in a y made here they hold anything, in `out` what they held.  out
+    must not overlap an operand."""
     name = "bi_grouped_linear_bf16"
     if x.dim() != 2:
         raise ValueError(f"{name}: x is [T, K]")
@@ -782,6 +800,9 @@ def bi_grouped_linear_bf16(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor,
         yp = out.data_ptr()
     else:
         yp, ldy = _matrix(out, ydt, T, N, dev, name, "out")
+        if yp < xp + T * ldx * 2 and xp < yp + T * ldy * 4:
+            es = _ELEM[ydt]
+            _apart(T, yp, ldy * es, N * es, xp, ldx * 2, K * 2, name, "out")
     _call(_lib.bi_grouped_linear_bf16, name, dev, xp, ldx, wp, ldw, step, ep, E, yp, code, ldy, T, N, K)
     return out
 
@@ -792,7 +813,8 @@ def bi_grouped_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, w: torc
     """Gradients of bi_grouped_linear_bf16: (dx [T, K] bf16 or None, dw [E, N, K]
     of dw_dtype or None; dw is zero for an expert without rows).  dy [T, N] bf16;
     x is read for dw only and w for dx only; the other may be None.  Rows of
-    dx from ends[-1] on are not written (out_dx: a dx of the caller's)."""
+    dx from ends[-1] on are not written (out_dx: a dx of the caller's, which must
+    not overlap an operand that is read)."""
     name = "bi_grouped_linear_bf16_bwd"
     if dy.dim() != 2 or (need_dx and (w is None or w.dim() != 3)) or (need_dw and (x is None or x.dim() != 2)):
         raise ValueError(f"{name}: dy is [T, N]; dx needs w [E, N, K] and dw needs x [T, K]")
@@ -819,8 +841,11 @@ def bi_grouped_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, w: torc
         else:
             dx = out_dx
             dxp, lddx = _matrix(dx, torch.bfloat16, T, K, dev, name, "out_dx")
+            _apart(T, dxp, lddx * 2, K * 2, dyp, lddy * 2, N * 2, name, "out_dx")
     if need_dw:
         xp, ldx = _matrix(x, torch.bfloat16, T, K, dev, name, "x")
+        if out_dx is not None and need_dx:
+            _apart(T, dxp, lddx * 2, K * 2, xp, ldx * 2, K * 2, name, "out_dx")
         dw = dy.new_empty(E, N, K, dtype=dw_dtype)
         dwp = dw.data_ptr()
     _call(_lib.bi_grouped_linear_bf16_bwd, name, dev, dyp, lddy, xp, ldx, wp, ldw, step, ep, E, dxp, lddx, dwp, code, K, N * K, T,
@@ -857,7 +882,8 @@ def bi_linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: tor
                    out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
     """y = (xq @ wq.t()) * xs[:, None] * ws + bias of 8-bit codes xq [M, K] and wq
     [N, K] (bi_quantize_int8 of activations and of an nn.Linear weight), sums
-    exact in 32-bit integers, bf16 or fp32 out, batch-invariant."""
+    exact in 32-bit integers, bf16 or fp32 out, batch-invariant.  out must not
+    overlap an operand."""
     name = "bi_linear_int8"
     if xq.dim() != 2 or wq.dim() != 2:
         raise ValueError(f"{name}: xq is [M, K] and wq is [N, K]")
@@ -879,6 +905,9 @@ def bi_linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: tor
         yp = out.data_ptr()
     else:
         yp, ldy = _matrix(out, ydt, M, N, dev, name, "out")
+        if yp < xp + M * ldx and xp < yp + M * ldy * 4:
+            es = _ELEM[ydt]
+            _apart(M, yp, ldy * es, N * es, xp, ldx, K, name, "out")
     _call(_lib.bi_linear_int8, name, dev, xp, ldx, xsp, wp, ldw, wsp, bp, yp, code, ldy, M, N, K)
     return out
 
@@ -886,7 +915,7 @@ def bi_linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: tor
 def bi_grouped_linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, ends: torch.Tensor,
                            out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
     """bi_linear_int8 with each row's own expert: xq [T, K] and xs [T] sorted by
-    expert, wq [E, N, K], ws [E, N], ends as for bi_grouped_linear_bf16."""
+    expert, wq [E, N, K], ws [E, N], ends and out as for bi_grouped_linear_bf16."""
     name = "bi_grouped_linear_int8"
     if xq.dim() != 2:
         raise ValueError(f"{name}: xq is [T, K]")
@@ -909,6 +938,9 @@ def bi_grouped_linear_int8(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor,
         yp = out.data_ptr()
     else:
         yp, ldy = _matrix(out, ydt, T, N, dev, name, "out")
+        if yp < xp + T * ldx and xp < yp + T * ldy * 4:
+            es = _ELEM[ydt]
+            _apart(T, yp, ldy * es, N * es, xp, ldx, K, name, "out")
     _call(_lib.bi_grouped_linear_int8, name, dev, xp, ldx, xsp, wp, ldw, step, wsp, lds if E > 1 else 0, ep, E, yp, code, ldy, T, N,
           K)
     return out

@@ -343,7 +343,8 @@ bi_status_t bi_layer_norm(const void* x, int32_t x_dtype, int64_t ldx, const flo
 /* Its gradients at the statistics kept by the forward pass, n = (x - m) r:
  *   g = dy w,  dx = r (g - (sum g + n sum(g n)) / H)     dx in x's type
  *   dw = sum of dy n, db = sum of dy over the rows       [H] fp32
- * Any of dx, dw, db may be NULL.  dy: bf16 or fp32.  M == 0 clears dw and db.  ws
+ * Any of dx, dw, db may be NULL.  dy: bf16 or fp32.  dx must not lie over dy or x, which
+ * other workgroups still read.  M == 0 clears dw and db.  ws
  * holds partial sums of dw and db: bi_layer_norm_bwd_workspace_size(M, H) bytes,
  * unless neither is wanted. */
 bi_status_t bi_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t lddy, const void* x, int32_t x_dtype, int64_t ldx,
@@ -370,7 +371,8 @@ bi_status_t bi_grouped_linear_bf16(const uint16_t* x, int64_t ldx, const uint16_
  * expert's rows of dy[t,:]^T x[t,:], bf16 or fp32, zero for an expert without
  * rows.  dx or dw may be NULL, and w (read for dx only) or x (for dw only) with
  * it.  T == 0 clears dw.  dw's experts lie stride_dw elements apart (at least one
- * expert's rows: (N - 1) lddw + K). */
+ * expert's rows: (N - 1) lddw + K).  dx must not lie over dy, nor over x where dw is
+ * wanted. */
 bi_status_t bi_grouped_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx,
                                        const uint16_t* w, int64_t ldw, int64_t stride_w, const int64_t* ends, int64_t E,
                                        uint16_t* dx, int64_t lddx, void* dw, int32_t dw_dtype, int64_t lddw, int64_t stride_dw,

@@ -569,3 +569,25 @@ def test_refusals_on_the_gpu(bi):
                  lambda: bi.bi_linear_int8(q.to(torch.uint8), s, wq[0], ws[0]), lambda: bi.bi_linear_int8(q, s.double(), wq[0], ws[0])):
         with pytest.raises(TypeError):
             call()
+
+
+def test_outputs_over_operands_are_refused_and_beside_them_taken(bi):
+    """Columns of one matrix: an output beside its operand, and over it."""
+    T, N, K, ends = 70, 64, 64, ends_of([30, 0, 40])
+    w, dy = ints((3, N, K), 2), ints((T, N), 3)
+    wide = torch.cat((ints((T, K), 1), torch.full((T, 2 * N), 7.0, dtype=BF, device="cuda")), 1)
+    x, keep = wide[:, :K], wide[:, :K].clone()
+    q, s = bi.bi_quantize_int8(keep)
+    wq, ws = (t.reshape(3, N, -1).squeeze(2) for t in bi.bi_quantize_int8(w.reshape(-1, K)))
+    for call in (lambda: bi.bi_grouped_linear_bf16(x, w, ends, out=x), lambda: bi.bi_grouped_linear_bf16(x, w, ends, out=wide[:, 32:96]),
+                 lambda: bi.bi_grouped_linear_bf16_bwd(dy, x, w, ends, out_dx=dy), lambda: bi.bi_grouped_linear_bf16_bwd(dy, x, w, ends, out_dx=x),
+                 lambda: bi.bi_layer_norm(x, out=wide[:, 8:8 + K]),
+                 lambda: bi.bi_linear_int8(q[:2], s[:2], wq[0], ws[0], out=q.view(BF).view(-1)[:2 * N].view(2, N)),
+                 lambda: bi.bi_grouped_linear_int8(q[:2], s[:2], wq, ws, ends, out=q.view(BF).view(-1)[:2 * N].view(2, N))):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    bi.bi_grouped_linear_bf16(x, w, ends, out=wide[:, K:K + N])
+    same_rows(wide[:, K:K + N].contiguous(), forward_ref(keep, w, ends))
+    bi.bi_grouped_linear_bf16_bwd(wide[:, K:K + N], None, w, ends, need_dw=False, out_dx=wide[:, K + N:])
+    same_rows(wide[:, K + N:].contiguous(), forward_ref(wide[:, K:K + N].contiguous(), w.transpose(1, 2), ends).to(BF).double())
+    assert torch.equal(x, keep)

@@ -199,6 +199,62 @@ def test_binding_refuses_before_it_enqueues():
             call()
 
 
+def test_overlap_of_an_output_and_an_operand():
+    """Against the bytes themselves, in every place of a small buffer."""
+    def bytes_of(p, rows, ld, width):
+        return {p + i * ld + j for i in range(rows) for j in range(width)}
+
+    def refused(*a):
+        try:
+            bi._apart(*a, "call", "out")
+            return False
+        except ValueError:
+            return True
+
+    for rows, ld, width, ldq, widthq in ((3, 10, 4, 10, 3), (4, 7, 7, 7, 2), (1, 10, 4, 6, 5), (2, 9, 1, 9, 8), (2, 9, 2, 9, 8)):
+        mine = bytes_of(100, rows, ld, width)
+        for q in range(50, 160):
+            assert refused(rows, 100, ld, width, q, ldq, widthq) == bool(mine & bytes_of(q, rows, ldq, widthq))
+    assert not refused(0, 0, 64, 64, 0, 64, 64)
+    # other pitches: nothing that shares a byte passes
+    for q in range(50, 160):
+        if bytes_of(100, 3, 10, 4) & bytes_of(q, 3, 8, 3):
+            assert refused(3, 100, 10, 4, q, 8, 3)
+
+
+def test_outputs_over_operands_are_refused(monkeypatch):
+    """The calls on host tensors that say they are on a GPU, up to the point of the launch."""
+    calls = []
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(bi, "_call", lambda fn, name, *a: calls.append(name))
+    i8 = torch.int8
+    x, w, ends = cpu(4, 64), cpu(2, 64, 64), cpu(2, dtype=torch.int64)
+    q, s, wq, ws = cpu(4, 64, dtype=i8), cpu(4, dtype=torch.float32), cpu(2, 64, 64, dtype=i8), cpu(2, 64, dtype=torch.float32)
+    wide, wide8 = cpu(4, 128), cpu(4, 256, dtype=i8)
+    over8 = wide8.view(torch.bfloat16)
+    for call in (lambda: bi.bi_grouped_linear_bf16(x, w, ends, out=x),
+                 lambda: bi.bi_grouped_linear_bf16(wide[:, :64], w, ends, out=wide[:, 56:120]),
+                 lambda: bi.bi_grouped_linear_bf16_bwd(x, cpu(4, 64), w, ends, out_dx=x),
+                 lambda: bi.bi_grouped_linear_bf16_bwd(x, None, w, ends, need_dw=False, out_dx=x),
+                 lambda: bi.bi_grouped_linear_bf16_bwd(cpu(4, 64), x, w, ends, out_dx=x),
+                 lambda: bi.bi_linear_int8(wide8[:, :64], s, wq[0], ws[0], out=over8[:, :64]),
+                 lambda: bi.bi_grouped_linear_int8(wide8[:, 64:128], s, wq, ws, ends, out=over8[:, 56:120]),
+                 lambda: bi.bi_layer_norm(wide[:, :64], out=wide[:, 32:96]),
+                 lambda: bi.bi_layer_norm(x[:3], out=x[1:])):
+        calls.clear()
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    calls.clear()
+    bi.bi_layer_norm(x, out=x)
+    bi.bi_layer_norm(wide[:, :64], out=wide[:, 64:])
+    bi.bi_grouped_linear_bf16(wide[:, :64], w, ends, out=wide[:, 64:])
+    bi.bi_grouped_linear_bf16_bwd(wide[:, :64], cpu(4, 64), w, ends, out_dx=wide[:, 64:])
+    bi.bi_grouped_linear_bf16_bwd(x, wide[:, :64], w, ends, need_dw=False, out_dx=wide[:, :64])      # x is not read
+    bi.bi_linear_int8(wide8[:, :64], s, wq[0], ws[0], out=over8[:, 64:])
+    bi.bi_grouped_linear_int8(wide8[:, 128:192], s, wq, ws, ends, out=over8[:, :64])
+    assert len(calls) == 7
+
+
 def test_import_beside_a_torch_without_gpu_support():
     """Recipe and workspace queries and refusals need no GPU entries of torch."""
     run = subprocess.run([sys.executable, "-c", """
