@@ -855,7 +855,8 @@ def bi_grouped_linear_bf16_bwd(dy: torch.Tensor, x: torch.Tensor | None, w: torc
 
 def bi_quantize_int8(x: torch.Tensor):
     """Rows of x [rows, K] (bf16 or fp32) as 8-bit integers: (codes int8 [rows, K] in
-    [-127, 127], scales fp32 [rows]), x = codes * scale up to rounding."""
+    [-127, 127], scales fp32 [rows]), x = codes * scale within half a scale.  A scale is
+    max|x| times fp32's 1/127: the quotient max|x| / 127 or one fp32 step less."""
     name = "bi_quantize_int8"
     xdt = x.dtype
     code = _DT.get(xdt)

@@ -3,7 +3,9 @@
 //
 // A row x is kept as codes q, integers in [-127, 127], and one fp32 scale s:
 //   s = max(max|x| * (1/127), 2^-126),  q = x / s to the nearest integer, ties to even
-// with 1/127 as fp32 holds it (s is within one step of the quotient).
+// with 1/127 as fp32 holds it.  That is 2^-28 below 1/127, so s is the rounded quotient
+// max|x| / 127 or the fp32 number next below (6 of bf16's 128 mantissas); a code differs
+// from the quotient's only where x / s lies within 127 * 2^-23 of halfway.
 // The product adds code products in 32-bit integers, which rounds nothing, so
 // any order of addition gives the same bits.
 #include "bi_ffn.h"

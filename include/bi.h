@@ -382,7 +382,12 @@ bi_status_t bi_grouped_linear_bf16_bwd(const uint16_t* dy, int64_t lddy, const u
  *   s = max(max|x| * c, 2^-126), c = 1/127 in fp32,  q = x / s rounded to the
  * nearest integer, ties to even: in [-127, 127].  A row that holds an infinity or a NaN gets s = NaN
  * and zero codes.  q: [rows, K] (pitch in bytes, a multiple of 16), s: [rows], 4-byte
- * aligned.  Requires K % 32 == 0. */
+ * aligned.  Requires K % 32 == 0.
+ * c is 2^-28 below 1/127: s is the fp32 quotient max|x| / 127 or the fp32 number next
+ * below it (1 in 21 maxima; of bf16's 128 mantissas 6).  Codes made with the quotient
+ * are the same but where x / s lies within 127 * 2^-23 of halfway between two integers
+ * (x of half the row's maximum does), and there each is as near to x as the other; the
+ * products take either with the scale it was made with. */
 bi_status_t bi_quantize_int8(const void* x, int32_t x_dtype, int64_t ldx, int8_t* q, int64_t ldq, float* s,
                              int64_t rows, int64_t K, hipStream_t stream);
 

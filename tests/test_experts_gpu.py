@@ -277,6 +277,24 @@ def test_quantize_on_the_border(bi):
     assert torch.equal(q.cpu(), qd)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+def test_quantize_beside_the_quotients_scale(bi, dtype):
+    """Scales are max|x| / 127 or one step less, codes within half a scale of their values,
+    and where they are not the quotient's codes the value lies next to halfway."""
+    top = 1 + torch.arange(1280, dtype=torch.float64) / 1280
+    at = torch.cat((torch.tensor([1.0, 0.5, -0.5], dtype=torch.float64), torch.linspace(-1, 1, 61, dtype=torch.float64)))
+    x = (top[:, None] * at).to(dtype)
+    q, s = (t.cpu() for t in bi.bi_quantize_int8(x.cuda()))
+    xd, sd = x.double(), s.double()[:, None]
+    sq = (xd.abs().amax(1) / 127).float()
+    step = s.view(torch.int32) - sq.view(torch.int32)
+    assert step.min() == -1 and step.max() == 0
+    assert ((q.double() * sd - xd).abs() <= 0.5 * sd).all()
+    v = xd / sq.double()[:, None]
+    far = (v - torch.floor(v) - 0.5).abs() > 127 * 2.0 ** -23
+    assert (q.double() == torch.round(v))[far].all() and (q.double() - torch.round(v)).abs().max() == 1
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 16, 32), (3, 48, 96), (17, 80, 64), (33, 272, 416), (70, 144, 1056), (130, 400, 224),
                                    (300, 528, 160), (515, 784, 352), (5, 2064, 8224)])
 def test_int8_product_bit_for_bit(bi, M, N, K):

@@ -310,6 +310,27 @@ def test_codes_by_hand():
     assert not q[3].any() and s[3] == 2.0 ** -126
 
 
+def test_scales_beside_the_quotient():
+    """max|x| times fp32's 1/127 is max|x| / 127 rounded once or the number next below,
+    for every fp32 mantissa; codes differ by one at most, and only next to halfway points,
+    and either is within half a scale of its value."""
+    top = 1 + torch.arange(1 << 23, dtype=torch.float64) / (1 << 23)
+    step = (top.float() * torch.tensor(1.0 / 127.0)).view(torch.int32) - (top / 127).float().view(torch.int32)
+    assert step.min() == -1 and step.max() == 0
+    m = 1 + torch.arange(128, dtype=torch.float64) / 128
+    x = m[:, None] * torch.cat((torch.tensor([1.0, 0.5, -0.5], dtype=torch.float64), torch.linspace(-1, 1, 61, dtype=torch.float64)))
+    x = x.to(torch.bfloat16)
+    q, s = ref.codes(x)
+    sq = (x.double().abs().amax(1) / 127).float()
+    v = x.double() / sq.double()[:, None]
+    other = torch.round(v)
+    assert int((s != sq).sum()) == 6 and ((s.view(torch.int32) - sq.view(torch.int32)) >= -1).all()
+    assert ((q.double() * s.double()[:, None] - x.double()).abs() <= 0.5 * s.double()[:, None]).all()
+    far = (v - torch.floor(v) - 0.5).abs() > 127 * 2.0 ** -23
+    assert (q.double() == other)[far].all() and (q.double() - other).abs().max() == 1
+    assert (q[s != sq, 1] == 64).all() and (other[s != sq, 1] == 63).all()
+
+
 def test_spans_of_any_ends():
     assert ref.spans([2, 2, 5], 6) == [(0, 2), (2, 2), (2, 5)]
     assert ref.spans([3, 1, -7, 99], 6) == [(0, 3), (3, 3), (3, 3), (3, 6)]
