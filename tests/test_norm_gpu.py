@@ -211,3 +211,45 @@ def test_graph_replays_and_streams(bi):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, eager))
         x.copy_(keep)
+
+
+@pytest.mark.parametrize("M", [1025, 3000])
+def test_partials_in_graphs_and_on_two_streams(bi, M):
+    """The backward pass whose partials go through a workspace: captured and replayed among
+    eager calls, and two of them under way on two streams at once."""
+    H = 2056
+    w, b = vec(H, 1, 1.0), vec(H, 2)
+    ins = [(rows(M, H, i, BF), rows(M, H, 10 + i, F32)) for i in range(2)]
+
+    def step(x, dy):
+        y, m, r = bi.bi_layer_norm(x, w, b, save_stats=True)
+        return (y, m, r) + bi.bi_layer_norm_bwd(dy, x, m, r, w)
+
+    want = [[t.clone() for t in step(*i)] for i in ins]
+    assert bi.lib().bi_layer_norm_bwd_workspace_size(M, H) > 0 and not torch.equal(want[0][4], want[1][4])
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(step(*ins[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(a, b) for run in got[k] for a, b in zip(run, want[k]))
+    x, dy = (t.clone() for t in ins[0])
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    outs = []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            outs.append(step(x, dy))
+    for i in (0, 1, 0):
+        x.copy_(ins[i][0])
+        dy.copy_(ins[i][1])
+        for g, out in zip(graphs, outs):
+            for t in out:
+                t.zero_()
+            g.replay()
+            step(*ins[1 - i])
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
