@@ -609,3 +609,92 @@ def test_outputs_over_operands_are_refused_and_beside_them_taken(bi):
     bi.bi_grouped_linear_bf16_bwd(wide[:, K:K + N], None, w, ends, need_dw=False, out_dx=wide[:, K + N:])
     same_rows(wide[:, K + N:].contiguous(), forward_ref(wide[:, K:K + N].contiguous(), w.transpose(1, 2), ends).to(BF).double())
     assert torch.equal(x, keep)
+
+
+@pytest.mark.parametrize("E", [1, 63, 129, 160, 256, 257, 512])
+def test_experts_to_a_lane(bi, E):
+    """1, 2, 4 and 16 experts to a lane of the wave that finds a workgroup's rows, at both
+    ends of each: forward, dx, dw alone and together, 8 bits, uneven rows."""
+    g = torch.Generator().manual_seed(E)
+    counts = [int(c) for c in torch.randint(0, 50, (E,), generator=g) * (torch.rand(E, generator=g) < 0.6)]
+    counts[0], counts[-1] = 3, 70
+    T, N, K, ends = sum(counts), 48, 64, ends_of(counts)
+    x, w, dy = ints((T, K), 1), ints((E, N, K), 2), ints((T, N), 3)
+    xs, ws = torch.rand(T, generator=g).cuda(), torch.rand((E, N), generator=g).cuda()
+    want, want_dx = forward_ref(x, w, ends), forward_ref(dy, w.transpose(1, 2), ends)
+    want_dw = torch.zeros((E, N, K), dtype=torch.float64)
+    want8 = torch.zeros((T, N))
+    for e, (a, b) in enumerate(ref.spans(ends.tolist(), T)):
+        want_dw[e] = dy[a:b].double().cpu().t() @ x[a:b].double().cpu()
+        want8[a:b] = ref.linear_int8(x[a:b].to(torch.int8), xs[a:b], w[e].to(torch.int8), ws[e], None, F32)
+    banner(f"grouped E={E}")
+    same_rows(bi.bi_grouped_linear_bf16(x, w, ends, out_dtype=F32), want)
+    assert torch.equal(bi.bi_grouped_linear_int8(x.to(torch.int8), xs, w.to(torch.int8), ws, ends, out_dtype=F32).cpu(), want8)
+    for dx_too, dw_too in ((True, True), (True, False), (False, True)):
+        dx, dw = bi.bi_grouped_linear_bf16_bwd(dy, x, w, ends, need_dx=dx_too, need_dw=dw_too, dw_dtype=F32)
+        assert dx is None or same_rows(dx, want_dx) is None
+        assert dw is None or torch.equal(dw.double().cpu(), want_dw)
+
+
+def _some_experts(ends, T):
+    """The experts with the most rows, the first and the last that have any."""
+    spans = ref.spans(ends.tolist(), T)
+    some = [e for e, (a, b) in enumerate(spans) if b > a]
+    big = sorted(some, key=lambda e: spans[e][0] - spans[e][1])[:2]
+    return [(e, *spans[e]) for e in sorted({*big, some[0], some[-1]})]
+
+
+def _some_rows(a, b):
+    """Rows at the expert's ends and around tile heights, as short slices."""
+    at = {a, (a + b) // 2, b - 1, *(a + h for h in (15, 63, 127, 255) if a + h < b)}
+    return [slice(i, min(i + 2, b)) for i in sorted(at)]
+
+
+@pytest.mark.parametrize("T,E,N,K", shapes.GROUPED)
+def test_rows_do_not_depend_on_the_tile(bi, T, E, N, K):
+    """Random values, whose sums round at every step, through every tile shape: rows of y
+    have the bits of the same rows alone, which take the smallest shapes."""
+    ends = ends_of(shapes.counts(T, E))
+    x, w = normal((T, K), 1), normal((E, N, K), 2, std=K ** -0.5)
+    for dt in (BF, F32):
+        banner(f"rows of tiles {T} {E} {N} {K} {dt}")
+        y = bi.bi_grouped_linear_bf16(x, w, ends, out_dtype=dt)
+        for e, a, b in _some_experts(ends, T):
+            for s in _some_rows(a, b):
+                assert torch.equal(bi.bi_grouped_linear_bf16(x[s], w[e:e + 1], ends_of([s.stop - s.start]), out_dtype=dt), y[s])
+
+
+def _check_backward_bits(bi, dy, x, w, ends):
+    """Both gradients from one call and from one each; rows of dx and experts of dw alone."""
+    T, E = len(x), len(w)
+    alone_dx, _ = bi.bi_grouped_linear_bf16_bwd(dy, None, w, ends, need_dw=False)
+    last = int(ends[-1])
+    for dt in (BF, F32):
+        _, alone_dw = bi.bi_grouped_linear_bf16_bwd(dy, x, None, ends, need_dx=False, dw_dtype=dt)
+        for _ in range(2):
+            dx, dw = bi.bi_grouped_linear_bf16_bwd(dy, x, w, ends, dw_dtype=dt)
+            assert torch.equal(dx[:last], alone_dx[:last]) and torch.equal(dw, alone_dw)
+        for e, a, b in _some_experts(ends, T):
+            one = bi.bi_grouped_linear_bf16_bwd(dy[a:b], x[a:b], None, ends_of([b - a]), need_dx=False, dw_dtype=dt)[1]
+            assert torch.equal(one[0], dw[e])
+    for e, a, b in _some_experts(ends, T):
+        for s in _some_rows(a, b):
+            few = bi.bi_grouped_linear_bf16_bwd(dy[s], None, w[e:e + 1], ends_of([s.stop - s.start]), need_dw=False)[0]
+            assert torch.equal(few, alone_dx[s])
+
+
+@pytest.mark.parametrize("T,E,N,K", shapes.GROUPED_BWD)
+def test_gradients_do_not_depend_on_the_tile(bi, T, E, N, K):
+    banner(f"gradients of tiles {T} {E} {N} {K}")
+    ends = ends_of(shapes.counts(T, E))
+    _check_backward_bits(bi, normal((T, N), 3), normal((T, K), 1), normal((E, N, K), 2), ends)
+
+
+@pytest.mark.parametrize("kind", ["half", "one", "few"])
+@pytest.mark.parametrize("T,E,N,K", [(9000, 40, 768, 1024), (3001, 300, 1024, 1024), (9000, 40, 1008, 1504)])
+def test_gradients_of_the_largest_tiles_do_not_depend_on_the_tile(bi, T, E, N, K, kind):
+    banner(f"gradients of the largest tiles {T} {E} {N} {K} {kind}")
+    assert bi.grouped_tile(bi.BI_GROUPED_DW_ALONE, T, E, N, K)["rows"] == 256
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dy, x, w = (torch.randn(s, generator=g, device="cuda").to(BF) for s in ((T, N), (T, K), (E, N, K)))
+    _check_backward_bits(bi, dy, x, w, ends_of(_skewed(T, E, kind)))
