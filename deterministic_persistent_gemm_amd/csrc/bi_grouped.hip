@@ -522,7 +522,13 @@ static int pick_group(GroupOp op, int64_t T, int64_t E, int64_t N, int64_t K, bo
 // problems, 0.62 to 1.00), the largest of both 0.94 (9 problems, 0.90 to 0.98).  Where
 // only dw's are the largest, its second largest beside small tiles of dx (0.94), or the
 // largest of both (dx's being 64 x 128 or 128 x 128: 0.92); where only dx's are, one
-// launch is the slower one (1.12 to 1.39).
+// launch is the slower one (1.12 to 1.39).  Those problems have many rows to an expert.
+// The rule does not compare times, and with few rows to an expert one launch loses, bf16
+// dw being a write that the other gradient's tiles wait beside, and dx at 256 rows a tile
+// serving a handful.  128 experts, 8 for each token, dx alone + dw alone / both, us: 1536
+// x 2048, 1 token 150 / 153, 8 223 / 266, 64 345 / 383, 500 415 / 434, 2000 564 / 538, 4096
+// 737 / 677; 2048 x 768, 1 token 86 / 81, 8 118 / 137, 64 191 / 226, 500 229 / 254, 2000 317 /
+// 298, 4096 415 / 378.
 struct GroupBwdPlan {
     int dx, dw;
     bool together;
@@ -615,7 +621,7 @@ static hipError_t run_both(TileArgs a, const GroupArgs& qx, int sx, TileArgs b, 
                 k_grouped_both<SX, SW><<<(unsigned)(ndx + ndw), kBothThreads, 0, s>>>(a, qx, b, qw, (int)(takes_all<SW>() ? ndw : ndx));
                 return hipGetLastError();
             } else {
-                return hipErrorInvalidConfiguration;    // no such kernel: plan_grouped_bwd asks for no such pair
+                return hipErrorInvalidConfiguration;    // no such kernel; plan_grouped_bwd asks for no such pair
             }
         });
     });

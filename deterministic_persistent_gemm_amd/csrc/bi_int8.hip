@@ -82,9 +82,9 @@ __device__ __forceinline__ uint32_t top_of(const RowRaw<BF, P>& r)
 // A team of T threads per row, whose first P chunks of 8 values per thread stay in
 // registers between the search for the largest and the codes; longer rows are read
 // again.  The next row is on its way meanwhile.  Bound by latency for few rows (3.8 us
-// for 16 of 4096); 4096 rows of 4096 bf16 take 16.5 us (50 MB, 3.0 TB/s), two rows to a
-// workgroup and so as much its start and end as memory, fp32 19.0 (4.4 TB/s), 4096 rows of
-// 8192 fp32 33.3 (5.0 TB/s).
+// for 16 of 4096); 4096 rows of 4096 bf16 take 16.5 us (50 MB, 3.0 TB/s), since the launch
+// gives two rows to each of 2048 workgroups, whose start and end cost as much as memory,
+// fp32 19.0 (4.4 TB/s), 4096 rows of 8192 fp32 33.3 (5.0 TB/s).
 template <bool BF, int T, int P>
 __global__ __launch_bounds__(256) void k_quantize_int8(const void* __restrict__ x, int64_t ldx, uint8_t* __restrict__ q,
                                                        int64_t ldq, float* __restrict__ sc, int64_t rows, int chunks)
@@ -199,7 +199,8 @@ struct Int8Shape {
 // Costs as in bi_tile_rule.h (a slice is 64 k), fitted to timings of 320 problems drawn
 // over M 1 .. 4096, widths 128 .. 12288 and k 256 .. 8192: the shapes chosen take 1.005
 // times the fastest one's time on average (fitted to one half of them, 1.013 on the
-// other).  128 x 128 is there twice: with four stages in its ring, one workgroup to a
+// other).  Longer k is underpriced (M 256, N 4096, K 12288 on 128 tiles of 64 x 128: 49 us
+// taken, 26 estimated).  128 x 128 is there twice: with four stages in its ring, one workgroup to a
 // compute unit, and in turns with two, two workgroups.
 static const TileShape kInt8Shapes[] = {
     {16, 16, 1.75f, 0.034f, 1.08f}, {16, 32, 1.70f, 0.042f, 1.03f}, {32, 32, 1.71f, 0.047f, 1.38f}, {32, 64, 1.89f, 0.092f, 1.05f},
@@ -232,7 +233,9 @@ static auto int8_shape(int i, F f)
 
 // v_mfma_i32_16x16x64_i8; scales and bias are applied to the sums as y is stored.  16 rows
 // through 4096 x 4096 take 6.3 us: the weight's 16.8 MB at the rate that a cold read of
-// that length has.  4096 x 12288 x 4096 takes 165 to 171 us (2.4 to 2.5 POP/s): a stage of the 256 x 256
+// that length has.  4096 x 12288 x 4096 takes 171 to 174 us on codes of normally distributed
+// values (2.4 POP/s), 176 to 178 on codes that are all equally likely, 168 on the same
+// operands again and again: a stage of the 256 x 256
 // tiles brings the same bytes as in bf16 for twice the products, and three rounds of them
 // pay 7 us each for first loads and stores.  (The same tiles one after the other, a
 // workgroup to a compute unit for the whole call: 174.6 us where these took 170.7.)
